@@ -48,6 +48,17 @@ struct FftParams {
   int vec;           // q, k, v, y 16-byte aligned and D a multiple of one 16-byte vector
 };
 
+// The spectra in the workspace are written by the kernel that runs before the reader, which a
+// programmatic launch lets start early: they are not constant while the reader lives, so they are
+// read by a coherent load that stays behind griddepcontrol.wait.  (As plain loads through a
+// pointer that the kernel only reads, the compiler may take them for constant data and move them
+// ahead of the wait: the length-65536 filter spectrum then came from the workspace's old bytes.)
+__device__ __forceinline__ float2 ld_spectrum(const float2 *p) {
+  float2 r;
+  asm volatile("ld.global.v2.f32 {%0, %1}, [%2];" : "=f"(r.x), "=f"(r.y) : "l"(p) : "memory");
+  return r;
+}
+
 __device__ __forceinline__ float2 cmul(float2 a, float2 b) {
   return make_float2(a.x * b.x - a.y * b.y, a.x * b.y + a.y * b.x);
 }
@@ -359,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, N2 <= 128 ? 8 : (kSpectrum ? 1 : 4))
   if (idx < R2) {
 #pragma unroll
     for (int m = 0; m < R1; ++m)
-      va[m] = live ? row[(idx + R2 * m) * p.PT] : make_float2(0.f, 0.f);
+      va[m] = live ? ld_spectrum(row + (idx + R2 * m) * p.PT) : make_float2(0.f, 0.f);
   }
   a_to_b<N2, false>(va, vb, ex, tw, idx, sig);  // synchronises before using ex (tw is filled)
   if constexpr (kSpectrum) {
@@ -372,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, N2 <= 128 ? 8 : (kSpectrum ? 1 : 4))
     // the group's filter spectrum at this thread's frequencies (L2-resident)
     const float2 *hk = H + k1 * N2 * p.G + (live ? (2 * (s0 + sig)) / p.d_g : 0);
 #pragma unroll
-    for (int r = 0; r < M; ++r) vb[r] = cmul(vb[r], hk[bfreq<N2>(idx, r) * p.G]);
+    for (int r = 0; r < M; ++r) vb[r] = cmul(vb[r], ld_spectrum(hk + bfreq<N2>(idx, r) * p.G));
     b_to_a<N2, true>(vb, va, ex, tw, idx, sig);
     if (idx < R2 && live) {
 #pragma unroll
@@ -405,7 +416,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int r = 0; r < BLay<N1>::M; ++r) {
       const int kk = bfreq<N1>(idx, r);
-      vb[r] = live ? cmul(ab[kk * kstride], cconj(tw2[kk])) : make_float2(0.f, 0.f);
+      vb[r] = live ? cmul(ld_spectrum(ab + kk * kstride), cconj(tw2[kk])) : make_float2(0.f, 0.f);
     }
   }
   b_to_a<N1, true>(vb, va, ex, tw, idx, sig);

@@ -117,3 +117,22 @@ def test_fft_deterministic_and_workspace_reuse():
     b = g.hyena_conv_fwd_fft(q, k, v, h, 16, 64, workspace=ws)
     torch.cuda.synchronize()
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("L", (32768, 8192, 900))
+def test_fft_result_does_not_depend_on_what_the_workspace_held(L):
+    """Every pass reads what the pass before it wrote, never the workspace's old bytes: the same
+    call over workspaces that held zeros, NaN patterns and its own last spectra."""
+    wl = custom("poison", 2, L, 80, 10, L, 64, "bf16", "mr", seed=21)
+    q, k, v, h = make_inputs(wl, device="cuda")
+    ws = torch.zeros(g.hyena_conv_fwd_fft_workspace_bytes(2, L, 80, 10, L), dtype=torch.uint8,
+                     device="cuda")
+    want = g.hyena_conv_fwd_fft(q, k, v, h, 10, 64, workspace=ws)
+    torch.cuda.synchronize()
+    _sampled_rows(want.cpu(), q.cpu(), k.cpu(), v.cpu(), h.cpu(), 10, [(0, 0), (1, L - 1)])
+    for fill in (0xff, 0x7f, None, 0xff, 0x7f):
+        if fill is not None:
+            ws.fill_(fill)
+        y = g.hyena_conv_fwd_fft(q, k, v, h, 10, 64, workspace=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want)
