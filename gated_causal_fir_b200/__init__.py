@@ -16,6 +16,8 @@ from . import _native
 from ._native import (HYENA_ALGO_AUTO, HYENA_ALGO_DIRECT, HYENA_ALGO_FFT, HYENA_ALGO_TENSOR,
                       HYENA_ALGO_WINDOW, HYENA_DEVICE_F16_RANGE, HYENA_DEVICE_TIMEOUT,
                       HYENA_DTYPE_BF16, HYENA_DTYPE_F32, ALGO_NAMES, HyenaError)
+from .recurrence import (hyena_scan_bwd, hyena_scan_bwd_workspace_bytes, hyena_scan_ckpt,
+                         hyena_scan_fwd, hyena_scan_step, hyena_scan_workspace_bytes)
 
 __all__ = [
     "hyena_conv_fwd", "hyena_conv_fwd_f32", "hyena_conv_fwd_ex", "hyena_select_algo",
@@ -29,6 +31,8 @@ __all__ = [
     "hyena_toeplitz_stages", "hyena_build_toeplitz_blocks", "hyena_conv_fwd_hist",
     "hyena_conv_fwd_fft", "hyena_conv_fwd_fft_workspace_bytes",
     "hyena_conv_fwd_from_host_workspace_bytes",
+    "hyena_scan_fwd", "hyena_scan_bwd", "hyena_scan_step", "hyena_scan_ckpt",
+    "hyena_scan_workspace_bytes", "hyena_scan_bwd_workspace_bytes",
 ]
 
 

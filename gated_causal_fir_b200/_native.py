@@ -1,4 +1,4 @@
-"""ctypes binding of the C ABI in include/hyena_conv.h.
+"""ctypes binding of the C ABI in include/hyena_conv.h and include/hyena_mixer.h.
 
 Argument marshalling only: every step of the computation runs in the CUDA kernels of
 ``libhyena_conv.so``.  There is no fallback; if the library is missing the first call raises.
@@ -10,6 +10,7 @@ import re
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libhyena_conv.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "hyena_conv.h")
+MIXER_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "hyena_mixer.h")
 TESTING_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "hyena_conv_testing.h")
 
 HYENA_OK = 0
@@ -73,6 +74,18 @@ SIGNATURES = {
     "hyena_abi_version": (_i32, []),
 }
 
+_sz = ctypes.c_size_t
+
+# include/hyena_mixer.h
+MIXER_SIGNATURES = {
+    "hyena_scan_fwd": (_i32, [_vp] * 8 + [_i64] * 3 + [_i32, _i32, _vp, _sz, _vp]),
+    "hyena_scan_workspace_bytes": (_i64, [_i64, _i64, _i64, _i32, _i32]),
+    "hyena_scan_ckpt_tiles": (_i64, [_i64, _i32]),
+    "hyena_scan_bwd": (_i32, [_vp] * 13 + [_i64] * 3 + [_i32, _i32, _vp, _sz, _vp]),
+    "hyena_scan_bwd_workspace_bytes": (_i64, [_i64, _i64, _i64, _i32, _i32, _i32]),
+    "hyena_scan_step": (_i32, [_vp] * 7 + [_i64, _i64, _i32, _i32, _vp]),
+}
+
 # include/hyena_conv_testing.h: test hooks, not part of the operation's interface
 TESTING_SIGNATURES = {
     "hyena_testing_fwd_fault": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _i32,
@@ -105,7 +118,8 @@ def lib():
             raise ImportError("libhyena_conv.so is not built (%s); run "
                               "`python -m gated_causal_fir_b200.build`" % LIB_PATH)
         handle = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in list(SIGNATURES.items()) + list(TESTING_SIGNATURES.items()):
+        for name, (res, args) in (list(SIGNATURES.items()) + list(MIXER_SIGNATURES.items()) +
+                                  list(TESTING_SIGNATURES.items())):
             fn = getattr(handle, name)
             fn.restype = res
             fn.argtypes = args

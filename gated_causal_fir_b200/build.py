@@ -6,17 +6,19 @@ or :func:`build` from Python.  Needs nvcc; cross-compiles on a host without a GP
 import os
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libhyena_conv.so")
-SOURCES = [os.path.join(CSRC, "hyena_conv.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh")] + [
-    os.path.join(ROOT, "include", "hyena_conv.h"), os.path.join(ROOT, "include", "hyena_conv_testing.h")]
+INCLUDE = os.path.join(ROOT, "include")
+SOURCES = [os.path.join(CSRC, f) for f in ("hyena_conv.cu", "hyena_scan.cu")]
+DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + [
+    os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
 
 NVCC_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17",
-              "-Xcompiler", "-fPIC", "-shared", "-Xptxas", "-warn-spills"]
+              "-Xcompiler", "-fPIC", "-Xptxas", "-warn-spills"]
 
 
 def nvcc() -> str:
@@ -38,11 +40,27 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [nvcc()] + NVCC_FLAGS + ["-I", os.path.join(ROOT, "include"), "-o", tmp] + SOURCES
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+
+    def compile_one(src):
+        obj = "%s.%s.o" % (tmp, os.path.basename(src))
+        run([nvcc()] + NVCC_FLAGS + ["-I", INCLUDE, "-c", src, "-o", obj])
+        return obj
+
+    try:
+        with ThreadPoolExecutor(len(SOURCES)) as pool:  # one nvcc per source, side by side
+            objs = list(pool.map(compile_one, SOURCES))
+        run([nvcc()] + NVCC_FLAGS + ["-shared", "-o", tmp] + objs)
+        os.replace(tmp, LIB)
+    finally:
+        for src in SOURCES:
+            obj = "%s.%s.o" % (tmp, os.path.basename(src))
+            if os.path.exists(obj):
+                os.remove(obj)
     return LIB
 
 

@@ -19,6 +19,7 @@
 #include "fir_fftblk.cuh"
 #include "fir_tc.cuh"
 #include "fir_tc_bwd.cuh"
+#include "host_util.h"
 
 namespace {
 
@@ -121,10 +122,7 @@ int current_device(DeviceState *&ds) {
   return d->err == cudaSuccess ? HYENA_OK : HYENA_ERR_CUDA;
 }
 
-using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+using hyena::host::EncodeTiledFn;
 
 EncodeTiledFn encode_tiled() {
   static EncodeTiledFn fn = nullptr;
@@ -1342,6 +1340,30 @@ int fwd_from_host(const Problem &P, int64_t chunk, void *workspace, size_t works
              ? HYENA_OK
              : HYENA_ERR_CUDA;
 }
+
+namespace hyena {
+namespace host {
+
+EncodeTiledFn encode_tiled() { return ::encode_tiled(); }
+
+int device_info(DeviceInfo *out) {
+  DeviceState *ds = nullptr;
+  if (current_device(ds) != HYENA_OK) return HYENA_ERR_CUDA;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return HYENA_ERR_CUDA;
+  static std::atomic<void *> word[kMaxDevices];
+  void *w = word[dev].load(std::memory_order_acquire);
+  if (!w) {
+    if (cudaGetSymbolAddress(&w, hyena::g_device_status) != cudaSuccess) return HYENA_ERR_CUDA;
+    word[dev].store(w, std::memory_order_release);
+  }
+  out->status = static_cast<unsigned int *>(w);
+  out->sm_count = ds->sm_count;
+  return HYENA_OK;
+}
+
+}  // namespace host
+}  // namespace hyena
 
 extern "C" {
 

@@ -1,0 +1,461 @@
+// hyena_scan.cu -- host side of the gated linear recurrence (include/hyena_mixer.h): argument
+// checks, time cuts, TMA descriptors and launches of the kernels in scan.cuh.
+#include <algorithm>
+#include <cstdint>
+#include <limits>
+#include <mutex>
+
+#include "host_util.h"
+#include "hyena_mixer.h"
+#include "scan.cuh"
+
+namespace {
+
+namespace sc = hyena::scan;
+using hyena::host::aligned;
+using hyena::host::overlap;
+using hyena::host::round_up;
+
+constexpr int kSmemMax = 227 * 1024;
+constexpr int kStaticSmem = 16 * 1024;  // bound on a kernel's static shared memory
+constexpr int64_t kI32 = std::numeric_limits<int32_t>::max();
+
+struct Shape {
+  int64_t B, L, D;
+  int d_g, dtype;
+  int64_t es() const { return dtype == HYENA_DTYPE_F32 ? 4 : 2; }
+  int64_t G() const { return D / d_g; }
+  int64_t n_cb() const { return (D + sc::kCh - 1) / sc::kCh; }
+  int64_t rows() const {
+    return dtype == HYENA_DTYPE_F32 ? sc::tile_rows<float>() : sc::tile_rows<__nv_bfloat16>();
+  }
+  int64_t n_tiles() const { return (L + rows() - 1) / rows(); }
+  int64_t numel() const { return B * L * D; }
+};
+
+int check_shape(const Shape &s) {
+  if (s.dtype != HYENA_DTYPE_BF16 && s.dtype != HYENA_DTYPE_F32) return HYENA_ERR_INVALID_ARG;
+  if (s.B < 0 || s.L < 0 || s.D < 1 || s.d_g < 1 || s.D % s.d_g != 0) return HYENA_ERR_INVALID_ARG;
+  if (s.B > kI32 || s.L > kI32 - 4096 || s.D > kI32 - 4096) return HYENA_ERR_INVALID_ARG;
+  if (s.B == 0) return HYENA_OK;
+  const int64_t lim = std::numeric_limits<int64_t>::max() / 64;
+  const int64_t l = std::max<int64_t>(s.L, 1);
+  if (s.B > lim / l || s.B * l > lim / s.D) return HYENA_ERR_INVALID_ARG;
+  return HYENA_OK;
+}
+
+// Cuts of the time axis.  A CTA streams ~50 GB/s at best, so fewer than ~100 columns of 32
+// channels leave HBM idle; every cut but one costs a second read of k, v and g, and a launch.
+// Each keeps at least two tiles.
+int64_t split_count(const Shape &s) {
+  constexpr int64_t kCtas = 148;
+  const int64_t blocks = s.B * s.n_cb();
+  if (blocks * 2 > kCtas) return 1;
+  return std::max<int64_t>(1, std::min(kCtas / blocks, s.n_tiles() / 2));
+}
+
+// What `blocks` CTAs' worth of cuts leaves after rounding to whole tiles per cut.
+struct Cuts {
+  int splits, tiles_per_split;
+};
+Cuts cuts_of(const Shape &s) {
+  const int64_t want = split_count(s), nt = s.n_tiles();
+  const int64_t per = (nt + want - 1) / want;
+  return Cuts{static_cast<int>((nt + per - 1) / per), static_cast<int>(per)};
+}
+
+int64_t agg_bytes(const Shape &s) {
+  const int64_t n = cuts_of(s).splits;
+  return n > 1 ? round_up(s.B * n * s.D * 8, 256) : 0;
+}
+int64_t ckpt_bytes(const Shape &s) { return round_up(s.B * s.n_tiles() * s.D * 4, 256); }
+
+int dg_mode(const Shape &s) {
+  if (s.d_g <= sc::kCh && (s.d_g & (s.d_g - 1)) == 0) return 0;
+  return s.d_g % sc::kCh == 0 ? 1 : 2;
+}
+int64_t dg_bytes(const Shape &s) {
+  const int m = dg_mode(s);
+  return m == 0 ? 0 : round_up(s.B * s.L * (m == 1 ? s.n_cb() : s.D) * 4, 256);
+}
+
+// One tensor [B, L, D] as boxes of one tile.
+int encode(CUtensorMap *m, const Shape &s, const void *ptr) {
+  hyena::host::EncodeTiledFn enc = hyena::host::encode_tiled();
+  if (!enc) return HYENA_ERR_CUDA;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(s.D), static_cast<cuuint64_t>(s.L),
+                              static_cast<cuuint64_t>(s.B)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s.D * s.es()),
+                                 static_cast<cuuint64_t>(s.L * s.D * s.es())};
+  const cuuint32_t box[3] = {sc::kCh, static_cast<cuuint32_t>(s.rows()), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const auto type = s.dtype == HYENA_DTYPE_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                               : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return enc(m, type, 3, const_cast<void *>(ptr), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? HYENA_OK
+             : HYENA_ERR_CUDA;
+}
+
+template <typename T, int kFeed>
+cudaError_t allow_smem() {
+  cudaError_t e = cudaSuccess;
+  const void *fns[] = {reinterpret_cast<const void *>(sc::scan_fwd_kernel<T, kFeed, true>),
+                       reinterpret_cast<const void *>(sc::scan_fwd_kernel<T, kFeed, false>),
+                       reinterpret_cast<const void *>(sc::scan_bwd_kernel<T, kFeed, true>),
+                       reinterpret_cast<const void *>(sc::scan_bwd_kernel<T, kFeed, false>)};
+  for (const void *f : fns)
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kSmemMax - kStaticSmem);
+  return e;
+}
+
+// Per-device one-time opt-in to the kernels' shared memory.
+int prepare_device(hyena::host::DeviceInfo *info) {
+  if (hyena::host::device_info(info) != HYENA_OK) return HYENA_ERR_CUDA;
+  constexpr int kMaxDevices = 64;
+  static std::once_flag once[kMaxDevices];
+  static cudaError_t err[kMaxDevices];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return HYENA_ERR_CUDA;
+  std::call_once(once[dev], [dev]() {
+    cudaError_t e = allow_smem<float, sc::kFeedChannel>();
+    if (e == cudaSuccess) e = allow_smem<float, sc::kFeedGroup>();
+    if (e == cudaSuccess) e = allow_smem<float, sc::kFeedPlain>();
+    if (e == cudaSuccess) e = allow_smem<__nv_bfloat16, sc::kFeedChannel>();
+    if (e == cudaSuccess) e = allow_smem<__nv_bfloat16, sc::kFeedGroup>();
+    if (e == cudaSuccess) e = allow_smem<__nv_bfloat16, sc::kFeedPlain>();
+    err[dev] = e;
+  });
+  return err[dev] == cudaSuccess ? HYENA_OK : HYENA_ERR_CUDA;
+}
+
+sc::Params base_params(const Shape &s, const hyena::host::DeviceInfo &info) {
+  sc::Params p{};
+  const Cuts c = cuts_of(s);
+  p.status = info.status;
+  p.B = static_cast<int>(s.B);
+  p.L = static_cast<int>(s.L);
+  p.D = static_cast<int>(s.D);
+  p.d_g = s.d_g;
+  p.G = static_cast<int>(s.G());
+  p.n_cb = static_cast<int>(s.n_cb());
+  p.n_tiles = static_cast<int>(s.n_tiles());
+  p.splits = c.splits;
+  p.tiles_per_split = c.tiles_per_split;
+  p.pieces = s.d_g % sc::kCh == 0   ? 1
+             : sc::kCh % s.d_g == 0 ? sc::kCh / s.d_g
+                                    : (sc::kCh + s.d_g - 2) / s.d_g + 1;
+  p.dg_mode = dg_mode(s);
+  return p;
+}
+
+// Cuts [first, first + count) of the problem with `streams` tiles per stage (and the decays).
+struct Launch {
+  unsigned grid;
+  size_t smem;
+};
+template <typename T>
+Launch plan(sc::Params &p, int feed, int streams, int first, int count, int sm_count) {
+  const int decays =
+      feed == sc::kFeedChannel
+          ? sc::stream_bytes<T>()
+          : static_cast<int>(round_up(sc::tile_rows<T>() * p.pieces * 4, sc::kStageAlign));
+  p.stage_bytes = streams * sc::stream_bytes<T>() + decays;
+  p.stages = std::min(sc::kMaxStages, (kSmemMax - kStaticSmem - sc::kStageAlign) / p.stage_bytes);
+  p.unit_split0 = first;
+  p.unit_splits = count;
+  p.n_units = p.B * count * p.n_cb;
+  Launch l;
+  l.grid = static_cast<unsigned>(std::min(p.n_units, sm_count));
+  l.smem = static_cast<size_t>(p.stages) * p.stage_bytes + sc::kStageAlign;
+  return l;
+}
+
+template <typename T, int kFeed, bool kOut>
+int run_fwd(const Shape &s, sc::Params p, int first, int count, int sms, cudaStream_t stream) {
+  const Launch l = plan<T>(p, kFeed, kOut ? 3 : 2, first, count, sms);
+  CUtensorMap mk{}, mv{}, mq{}, mg{};
+  if (kFeed != sc::kFeedPlain) {
+    if (encode(&mk, s, p.k) || encode(&mv, s, p.v) || (kOut && encode(&mq, s, p.q)) ||
+        (kFeed == sc::kFeedChannel && encode(&mg, s, p.g)))
+      return HYENA_ERR_CUDA;
+  }
+  return hyena::host::launch(sc::scan_fwd_kernel<T, kFeed, kOut>, dim3(l.grid),
+                             dim3(sc::kThreads), l.smem, stream, mk, mv, mq, mg,
+                             p) == cudaSuccess
+             ? HYENA_OK
+             : HYENA_ERR_CUDA;
+}
+
+template <typename T, int kFeed, bool kOut>
+int run_bwd(const Shape &s, sc::Params p, int first, int count, int sms, cudaStream_t stream) {
+  const Launch l = plan<T>(p, kFeed, kOut ? 4 : 2, first, count, sms);
+  CUtensorMap mq{}, mdy{}, mk{}, mv{}, mg{};
+  if (kFeed != sc::kFeedPlain) {
+    if (encode(&mq, s, p.q) || encode(&mdy, s, p.dy) || (kOut && encode(&mk, s, p.k)) ||
+        (kOut && encode(&mv, s, p.v)) || (kFeed == sc::kFeedChannel && encode(&mg, s, p.g)))
+      return HYENA_ERR_CUDA;
+  }
+  return hyena::host::launch(sc::scan_bwd_kernel<T, kFeed, kOut>, dim3(l.grid),
+                             dim3(sc::kThreads), l.smem, stream, mq, mdy, mk, mv, mg,
+                             p) == cudaSuccess
+             ? HYENA_OK
+             : HYENA_ERR_CUDA;
+}
+
+// The states pass over the whole problem: y and the last state, or (kOut = false) checkpoints.
+template <typename T, int kFeed, bool kOut>
+int states(const Shape &s, sc::Params p, float2 *agg, int sms, cudaStream_t stream) {
+  if (p.splits > 1) {
+    sc::Params a = p;
+    a.agg = agg;
+    a.ckpt = nullptr;
+    a.s_out = nullptr;
+    const int rc = run_fwd<T, kFeed, false>(s, a, 0, p.splits - 1, sms, stream);
+    if (rc != HYENA_OK) return rc;
+    p.agg = agg;
+  }
+  return run_fwd<T, kFeed, kOut>(s, p, 0, p.splits, sms, stream);
+}
+
+template <typename T, int kFeed>
+int forward(const Shape &s, const sc::Params &p, void *ws, int sms, cudaStream_t stream) {
+  return states<T, kFeed, true>(s, p, static_cast<float2 *>(ws), sms, stream);
+}
+
+template <typename T, int kFeed>
+int backward(const Shape &s, sc::Params p, void *ws, int sms, cudaStream_t stream) {
+  uint8_t *at = static_cast<uint8_t *>(ws);
+  float2 *agg = reinterpret_cast<float2 *>(at);
+  at += agg_bytes(s);
+  p.dg_part = reinterpret_cast<float *>(at);
+  at += dg_bytes(s);
+  int rc = HYENA_OK;
+  if (!p.ckpt) {
+    p.ckpt = reinterpret_cast<float *>(at);
+    rc = states<T, kFeed, false>(s, p, agg, sms, stream);
+    if (rc != HYENA_OK) return rc;
+  }
+  if (p.splits > 1) {
+    p.agg = agg;
+    rc = run_bwd<T, kFeed, false>(s, p, 1, p.splits - 1, sms, stream);
+    if (rc != HYENA_OK) return rc;
+  }
+  rc = run_bwd<T, kFeed, true>(s, p, 0, p.splits, sms, stream);
+  if (rc != HYENA_OK || p.dg_mode == 0) return rc;
+  const int64_t n = s.B * s.L * s.G();
+  const int width = p.dg_mode == 1 ? s.d_g / sc::kCh : s.d_g;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((n + 255) / 256, 16 * sms));
+  return hyena::host::launch(sc::scan_dg_kernel<T>, dim3(grid), dim3(256), 0, stream,
+                             static_cast<const float *>(p.dg_part), static_cast<T *>(p.dg), n,
+                             width) == cudaSuccess
+             ? HYENA_OK
+             : HYENA_ERR_CUDA;
+}
+
+// Which feed takes the tensors: TMA needs 16-byte rows and bases.
+int choose_feed(const Shape &s, std::initializer_list<const void *> streams, const void *g) {
+  bool tma = s.D * s.es() % 16 == 0 && s.D * s.es() * s.L < (int64_t{1} << 40);
+  for (const void *t : streams) tma = tma && aligned(t, 16);
+  if (!tma) return sc::kFeedPlain;
+  if (s.d_g > 1) return sc::kFeedGroup;
+  return aligned(g, 16) ? sc::kFeedChannel : sc::kFeedGroup;
+}
+
+template <typename T, typename F>
+int with_feed(int feed, F &&f) {
+  if (feed == sc::kFeedChannel) return f(std::integral_constant<int, sc::kFeedChannel>());
+  if (feed == sc::kFeedGroup) return f(std::integral_constant<int, sc::kFeedGroup>());
+  return f(std::integral_constant<int, sc::kFeedPlain>());
+}
+
+// Copies a state (zeros if null) for problems of no tokens.
+int copy_state(const float *from, float *to, int64_t n, cudaStream_t stream) {
+  if (!to || n == 0) return HYENA_OK;
+  const size_t bytes = static_cast<size_t>(n) * 4;
+  const cudaError_t e = from ? cudaMemcpyAsync(to, from, bytes, cudaMemcpyDeviceToDevice, stream)
+                             : cudaMemsetAsync(to, 0, bytes, stream);
+  return e == cudaSuccess ? HYENA_OK : HYENA_ERR_CUDA;
+}
+
+struct Buf {
+  const void *p;
+  int64_t bytes;
+};
+// Whether an output overlaps an input or another output.
+bool clash(std::initializer_list<Buf> outs, std::initializer_list<Buf> ins) {
+  for (const Buf *o = outs.begin(); o != outs.end(); ++o) {
+    for (const Buf &i : ins)
+      if (overlap(o->p, o->bytes, i.p, i.bytes)) return true;
+    for (const Buf *q = o + 1; q != outs.end(); ++q)
+      if (overlap(o->p, o->bytes, q->p, q->bytes)) return true;
+  }
+  return false;
+}
+
+bool misaligned(uintptr_t a, std::initializer_list<const void *> ptrs) {
+  for (const void *p : ptrs)
+    if (!aligned(p, a)) return true;
+  return false;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t hyena_scan_ckpt_tiles(int64_t L, int dtype) {
+  const Shape s{1, L, 1, 1, dtype};
+  if (check_shape(s) != HYENA_OK) return -HYENA_ERR_INVALID_ARG;
+  return s.n_tiles();
+}
+
+int64_t hyena_scan_workspace_bytes(int64_t B, int64_t L, int64_t D, int d_g, int dtype) {
+  const Shape s{B, L, D, d_g, dtype};
+  if (check_shape(s) != HYENA_OK) return -HYENA_ERR_INVALID_ARG;
+  return B == 0 || L == 0 ? 0 : agg_bytes(s);
+}
+
+int64_t hyena_scan_bwd_workspace_bytes(int64_t B, int64_t L, int64_t D, int d_g, int dtype,
+                                       int have_ckpt) {
+  const Shape s{B, L, D, d_g, dtype};
+  if (check_shape(s) != HYENA_OK) return -HYENA_ERR_INVALID_ARG;
+  if (B == 0 || L == 0) return 0;
+  return agg_bytes(s) + dg_bytes(s) + (have_ckpt ? 0 : ckpt_bytes(s));
+}
+
+int hyena_scan_fwd(const void *q, const void *k, const void *v, const void *g, const float *s0,
+                   void *y, float *s_out, float *ckpt, int64_t B, int64_t L, int64_t D, int d_g,
+                   int dtype, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+  const Shape s{B, L, D, d_g, dtype};
+  int rc = check_shape(s);
+  if (rc != HYENA_OK) return rc;
+  if (misaligned(4, {s0, s_out, ckpt})) return HYENA_ERR_MISALIGNED;
+  if (B == 0) return HYENA_OK;
+  const int64_t st = B * D * 4, n = s.numel() * s.es(), ng = B * L * s.G() * s.es();
+  if (overlap(s_out, st, s0, st)) return HYENA_ERR_INVALID_ARG;
+  if (L == 0) return copy_state(s0, s_out, B * D, stream);
+  if (!q || !k || !v || !g || !y) return HYENA_ERR_INVALID_ARG;
+  if (misaligned(static_cast<uintptr_t>(s.es()), {q, k, v, g, y}) || !aligned(workspace, 16))
+    return HYENA_ERR_MISALIGNED;
+  const int64_t need = agg_bytes(s);
+  if (need > 0 && (!workspace || static_cast<int64_t>(workspace_bytes) < need))
+    return HYENA_ERR_INVALID_ARG;
+  const int64_t nck = ckpt ? B * s.n_tiles() * D * 4 : 0;
+  const Buf ws{need > 0 ? workspace : nullptr, need};
+  if (clash({{y, n}, {s_out, st}, {ckpt, nck}, ws},
+            {{q, n}, {k, n}, {v, n}, {g, ng}, {s0, st}}))
+    return HYENA_ERR_INVALID_ARG;
+  if (B * s.n_cb() * cuts_of(s).splits > kI32) return HYENA_ERR_UNSUPPORTED;
+  hyena::host::DeviceInfo info;
+  if (prepare_device(&info) != HYENA_OK) return HYENA_ERR_CUDA;
+  sc::Params p = base_params(s, info);
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.g = g;
+  p.s0 = s0;
+  p.s_out = s_out;
+  p.ckpt = ckpt;
+  p.y = y;
+  const int feed = choose_feed(s, {q, k, v, y}, g);
+  return with_feed<void>(feed, [&](auto f) {
+    constexpr int kFeed = decltype(f)::value;
+    return dtype == HYENA_DTYPE_F32
+               ? forward<float, kFeed>(s, p, workspace, info.sm_count, stream)
+               : forward<__nv_bfloat16, kFeed>(s, p, workspace, info.sm_count, stream);
+  });
+}
+
+int hyena_scan_bwd(const void *q, const void *k, const void *v, const void *g, const float *s0,
+                   const void *dy, const float *ds_out, const float *ckpt, void *dq, void *dk,
+                   void *dv, void *dg, float *ds0, int64_t B, int64_t L, int64_t D, int d_g,
+                   int dtype, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+  const Shape s{B, L, D, d_g, dtype};
+  int rc = check_shape(s);
+  if (rc != HYENA_OK) return rc;
+  if (misaligned(4, {s0, ds_out, ckpt, ds0})) return HYENA_ERR_MISALIGNED;
+  if (B == 0) return HYENA_OK;
+  const int64_t st = B * D * 4, n = s.numel() * s.es(), ng = B * L * s.G() * s.es();
+  if (overlap(ds0, st, ds_out, st)) return HYENA_ERR_INVALID_ARG;
+  if (L == 0) return copy_state(ds_out, ds0, B * D, stream);
+  if (!q || !k || !v || !g || !dy || !dq || !dk || !dv || !dg) return HYENA_ERR_INVALID_ARG;
+  if (misaligned(static_cast<uintptr_t>(s.es()), {q, k, v, g, dy, dq, dk, dv, dg}) ||
+      !aligned(workspace, 16))
+    return HYENA_ERR_MISALIGNED;
+  const int64_t need = hyena_scan_bwd_workspace_bytes(B, L, D, d_g, dtype, ckpt != nullptr);
+  if (need > 0 && (!workspace || static_cast<int64_t>(workspace_bytes) < need))
+    return HYENA_ERR_INVALID_ARG;
+  const int64_t nck = ckpt ? B * s.n_tiles() * D * 4 : 0;
+  const Buf ws{need > 0 ? workspace : nullptr, need};
+  if (clash({{dq, n}, {dk, n}, {dv, n}, {dg, ng}, {ds0, st}, ws},
+            {{q, n}, {k, n}, {v, n}, {g, ng}, {dy, n}, {s0, st}, {ds_out, st}, {ckpt, nck}}))
+    return HYENA_ERR_INVALID_ARG;
+  if (B * s.n_cb() * cuts_of(s).splits > kI32) return HYENA_ERR_UNSUPPORTED;
+  hyena::host::DeviceInfo info;
+  if (prepare_device(&info) != HYENA_OK) return HYENA_ERR_CUDA;
+  sc::Params p = base_params(s, info);
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.g = g;
+  p.dy = dy;
+  p.s0 = s0;
+  p.ds_out = ds_out;
+  p.ckpt = const_cast<float *>(ckpt);
+  p.dq = dq;
+  p.dk = dk;
+  p.dv = dv;
+  p.dg = dg;
+  p.ds0 = ds0;
+  const int feed = choose_feed(s, {q, k, v, dy, dq, dk, dv}, g);
+  // the per-channel feed also stores dg in pairs
+  const int use = feed == sc::kFeedChannel && !aligned(dg, 16) ? sc::kFeedPlain : feed;
+  return with_feed<void>(use, [&](auto f) {
+    constexpr int kFeed = decltype(f)::value;
+    return dtype == HYENA_DTYPE_F32
+               ? backward<float, kFeed>(s, p, workspace, info.sm_count, stream)
+               : backward<__nv_bfloat16, kFeed>(s, p, workspace, info.sm_count, stream);
+  });
+}
+
+int hyena_scan_step(const void *q, const void *k, const void *v, const void *g, const float *s,
+                    void *y, float *s_out, int64_t B, int64_t D, int d_g, int dtype,
+                    cudaStream_t stream) {
+  const Shape sh{B, 1, D, d_g, dtype};
+  const int rc = check_shape(sh);
+  if (rc != HYENA_OK) return rc;
+  if (B == 0) return HYENA_OK;
+  if (!q || !k || !v || !g || !s || !y || !s_out) return HYENA_ERR_INVALID_ARG;
+  if (misaligned(static_cast<uintptr_t>(sh.es()), {q, k, v, g, y}) || misaligned(4, {s, s_out}))
+    return HYENA_ERR_MISALIGNED;
+  const int64_t st = B * D * 4, n = B * D * sh.es(), ng = B * sh.G() * sh.es();
+  if ((s_out != s && overlap(s_out, st, s, st)) || overlap(y, n, s, st) ||
+      clash({{y, n}, {s_out, st}}, {{q, n}, {k, n}, {v, n}, {g, ng}}))
+    return HYENA_ERR_INVALID_ARG;
+  const int vec = dtype == HYENA_DTYPE_F32 ? 4 : 8;
+  const bool wide = D % vec == 0 && !misaligned(16, {q, k, v, y, s, s_out}) &&
+                    (d_g > 1 || aligned(g, 16));
+  const int64_t per = 128 * (wide ? vec : 1), blocks = (B * D + per - 1) / per;
+  if (blocks > kI32) return HYENA_ERR_UNSUPPORTED;
+  const auto go = [&](auto *type, auto vn) {
+    using T = std::remove_pointer_t<decltype(type)>;
+    return hyena::host::launch(sc::scan_step_kernel<T, decltype(vn)::value>,
+                               dim3(static_cast<unsigned>(blocks)), dim3(128), 0, stream,
+                               static_cast<const T *>(q), static_cast<const T *>(k),
+                               static_cast<const T *>(v), static_cast<const T *>(g), s,
+                               static_cast<T *>(y), s_out, B * D, static_cast<int>(D), d_g,
+                               static_cast<int>(sh.G())) == cudaSuccess
+               ? HYENA_OK
+               : HYENA_ERR_CUDA;
+  };
+  if (dtype == HYENA_DTYPE_F32)
+    return wide ? go(static_cast<float *>(nullptr), std::integral_constant<int, 4>())
+                : go(static_cast<float *>(nullptr), std::integral_constant<int, 1>());
+  return wide ? go(static_cast<__nv_bfloat16 *>(nullptr), std::integral_constant<int, 8>())
+              : go(static_cast<__nv_bfloat16 *>(nullptr), std::integral_constant<int, 1>());
+}
+
+}  // extern "C"
