@@ -36,7 +36,7 @@ struct Shape {
 int check_shape(const Shape &s) {
   if (s.dtype != HYENA_DTYPE_BF16 && s.dtype != HYENA_DTYPE_F32) return HYENA_ERR_INVALID_ARG;
   if (s.B < 0 || s.L < 0 || s.D < 1 || s.d_g < 1 || s.D % s.d_g != 0) return HYENA_ERR_INVALID_ARG;
-  if (s.B > kI32 || s.L > kI32 - 4096 || s.D > kI32 - 4096) return HYENA_ERR_INVALID_ARG;
+  if (s.B > kI32 || s.L > kI32 - 4096 || s.D > (int64_t{1} << 28)) return HYENA_ERR_INVALID_ARG;
   if (s.B == 0) return HYENA_OK;
   const int64_t lim = std::numeric_limits<int64_t>::max() / 64;
   const int64_t l = std::max<int64_t>(s.L, 1);
@@ -79,15 +79,24 @@ int64_t dg_bytes(const Shape &s) {
   return m == 0 ? 0 : round_up(s.B * s.L * (m == 1 ? s.n_cb() : s.D) * 4, 256);
 }
 
-// One tensor [B, L, D] as boxes of one tile.
-int encode(CUtensorMap *m, const Shape &s, const void *ptr) {
+// Groups per row of g's tile: from a 16-byte boundary at or before a block's first group to its
+// last.  0 where TMA cannot take g's rows.
+int g_box(const Shape &s, const void *g, int pieces) {
+  const int64_t per = 16 / s.es();
+  if (s.G() % per != 0 || !aligned(g, 16)) return 0;
+  const bool whole = s.d_g % sc::kCh == 0 || sc::kCh % s.d_g == 0;  // blocks start at their groups
+  return static_cast<int>(round_up(whole ? pieces : pieces + per - 1, per));
+}
+
+// One tensor [B, L, width] as boxes of `box_w` columns and one tile's rows.
+int encode(CUtensorMap *m, const Shape &s, const void *ptr, int64_t width, int box_w) {
   hyena::host::EncodeTiledFn enc = hyena::host::encode_tiled();
   if (!enc) return HYENA_ERR_CUDA;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(s.D), static_cast<cuuint64_t>(s.L),
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(s.L),
                               static_cast<cuuint64_t>(s.B)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s.D * s.es()),
-                                 static_cast<cuuint64_t>(s.L * s.D * s.es())};
-  const cuuint32_t box[3] = {sc::kCh, static_cast<cuuint32_t>(s.rows()), 1};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(width * s.es()),
+                                 static_cast<cuuint64_t>(s.L * width * s.es())};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_w), static_cast<cuuint32_t>(s.rows()), 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   const auto type = s.dtype == HYENA_DTYPE_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                                : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -96,6 +105,10 @@ int encode(CUtensorMap *m, const Shape &s, const void *ptr) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? HYENA_OK
              : HYENA_ERR_CUDA;
+}
+
+int encode(CUtensorMap *m, const Shape &s, const void *ptr) {
+  return encode(m, s, ptr, s.D, sc::kCh);
 }
 
 template <typename T, int kFeed>
@@ -132,7 +145,7 @@ int prepare_device(hyena::host::DeviceInfo *info) {
   return err[dev] == cudaSuccess ? HYENA_OK : HYENA_ERR_CUDA;
 }
 
-sc::Params base_params(const Shape &s, const hyena::host::DeviceInfo &info) {
+sc::Params base_params(const Shape &s, const void *g, const hyena::host::DeviceInfo &info) {
   sc::Params p{};
   const Cuts c = cuts_of(s);
   p.status = info.status;
@@ -149,6 +162,7 @@ sc::Params base_params(const Shape &s, const hyena::host::DeviceInfo &info) {
              : sc::kCh % s.d_g == 0 ? sc::kCh / s.d_g
                                     : (sc::kCh + s.d_g - 2) / s.d_g + 1;
   p.dg_mode = dg_mode(s);
+  p.g_box = g_box(s, g, p.pieces);
   return p;
 }
 
@@ -159,10 +173,12 @@ struct Launch {
 };
 template <typename T>
 Launch plan(sc::Params &p, int feed, int streams, int first, int count, int sm_count) {
-  const int decays =
-      feed == sc::kFeedChannel
-          ? sc::stream_bytes<T>()
-          : static_cast<int>(round_up(sc::tile_rows<T>() * p.pieces * 4, sc::kStageAlign));
+  if (feed != sc::kFeedGroup) p.g_box = 0;
+  const int decays = feed == sc::kFeedChannel
+                         ? sc::stream_bytes<T>()
+                         : sc::decay_bytes<T>(p.pieces) +
+                               static_cast<int>(round_up(sc::tile_rows<T>() * p.g_box * sizeof(T),
+                                                         sc::kStageAlign));
   p.stage_bytes = streams * sc::stream_bytes<T>() + decays;
   p.stages = std::min(sc::kMaxStages, (kSmemMax - kStaticSmem - sc::kStageAlign) / p.stage_bytes);
   p.unit_split0 = first;
@@ -180,7 +196,8 @@ int run_fwd(const Shape &s, sc::Params p, int first, int count, int sms, cudaStr
   CUtensorMap mk{}, mv{}, mq{}, mg{};
   if (kFeed != sc::kFeedPlain) {
     if (encode(&mk, s, p.k) || encode(&mv, s, p.v) || (kOut && encode(&mq, s, p.q)) ||
-        (kFeed == sc::kFeedChannel && encode(&mg, s, p.g)))
+        (kFeed == sc::kFeedChannel && encode(&mg, s, p.g)) ||
+        (p.g_box && encode(&mg, s, p.g, s.G(), p.g_box)))
       return HYENA_ERR_CUDA;
   }
   return hyena::host::launch(sc::scan_fwd_kernel<T, kFeed, kOut>, dim3(l.grid),
@@ -196,7 +213,8 @@ int run_bwd(const Shape &s, sc::Params p, int first, int count, int sms, cudaStr
   CUtensorMap mq{}, mdy{}, mk{}, mv{}, mg{};
   if (kFeed != sc::kFeedPlain) {
     if (encode(&mq, s, p.q) || encode(&mdy, s, p.dy) || (kOut && encode(&mk, s, p.k)) ||
-        (kOut && encode(&mv, s, p.v)) || (kFeed == sc::kFeedChannel && encode(&mg, s, p.g)))
+        (kOut && encode(&mv, s, p.v)) || (kFeed == sc::kFeedChannel && encode(&mg, s, p.g)) ||
+        (p.g_box && encode(&mg, s, p.g, s.G(), p.g_box)))
       return HYENA_ERR_CUDA;
   }
   return hyena::host::launch(sc::scan_bwd_kernel<T, kFeed, kOut>, dim3(l.grid),
@@ -261,8 +279,8 @@ int choose_feed(const Shape &s, std::initializer_list<const void *> streams, con
   bool tma = s.D * s.es() % 16 == 0 && s.D * s.es() * s.L < (int64_t{1} << 40);
   for (const void *t : streams) tma = tma && aligned(t, 16);
   if (!tma) return sc::kFeedPlain;
-  if (s.d_g > 1) return sc::kFeedGroup;
-  return aligned(g, 16) ? sc::kFeedChannel : sc::kFeedGroup;
+  if (s.d_g > 1) return s.d_g % 2 == 0 ? sc::kFeedGroup : sc::kFeedPlain;
+  return aligned(g, 16) ? sc::kFeedChannel : sc::kFeedPlain;
 }
 
 template <typename T, typename F>
@@ -351,7 +369,7 @@ int hyena_scan_fwd(const void *q, const void *k, const void *v, const void *g, c
   if (B * s.n_cb() * cuts_of(s).splits > kI32) return HYENA_ERR_UNSUPPORTED;
   hyena::host::DeviceInfo info;
   if (prepare_device(&info) != HYENA_OK) return HYENA_ERR_CUDA;
-  sc::Params p = base_params(s, info);
+  sc::Params p = base_params(s, g, info);
   p.q = q;
   p.k = k;
   p.v = v;
@@ -396,7 +414,7 @@ int hyena_scan_bwd(const void *q, const void *k, const void *v, const void *g, c
   if (B * s.n_cb() * cuts_of(s).splits > kI32) return HYENA_ERR_UNSUPPORTED;
   hyena::host::DeviceInfo info;
   if (prepare_device(&info) != HYENA_OK) return HYENA_ERR_CUDA;
-  sc::Params p = base_params(s, info);
+  sc::Params p = base_params(s, g, info);
   p.q = q;
   p.k = k;
   p.v = v;

@@ -19,9 +19,9 @@
 //
 // Within a CTA: one warp streams the tiles in with TMA through a ring of shared-memory stages;
 // eight warps compute.  Half a warp (16 lanes of 2 channels) owns a segment of R consecutive
-// rows: it takes the segment into registers, frees the stage, forms the segment's (A, S), and
-// after one barrier every lane joins the 16 segments of its channels in order, which gives each
-// segment its own start and every warp the next tile's.  R is odd for bf16: the two halves of a
+// rows: it takes the segment into registers, frees the stage, forms the segment's (A, S) and joins
+// it with the other half's, and after one barrier every lane joins the 8 warps' of its channels in
+// order, which gives each its own start and all of them the next tile's.  R is odd for bf16: the two halves of a
 // warp then read rows an odd number of 64-byte rows apart, from different banks.
 //
 // All arithmetic is fp32; q, k, v, g, dy are read once, y, dq, dk, dv, dg rounded once.
@@ -48,7 +48,9 @@ constexpr unsigned int kTimeout = 1u; // HYENA_DEVICE_TIMEOUT
 // How a tile's inputs reach shared memory.
 enum Feed {
   kFeedChannel = 0,  // TMA, one decay per channel: g is a stream like k and v
-  kFeedGroup = 1,    // TMA for the streams; the helper warps form the decays of the groups
+  kFeedGroup = 1,    // TMA for the streams and the groups' g, of which the helper warps form the
+                     // decays (TMA for the streams alone where rows of g are no multiple of 16
+                     // bytes)
   kFeedPlain = 2     // element loads by the helper warps (rows TMA cannot address), any d_g
 };
 
@@ -62,6 +64,12 @@ template <typename T>
 __host__ __device__ constexpr int tile_rows() { return kSegs * Rows<T>::R; }
 template <typename T>
 __host__ __device__ constexpr int stream_bytes() { return tile_rows<T>() * kCh * static_cast<int>(sizeof(T)); }
+
+// fp32 decays of a tile's rows and groups, rounded up to keep what follows them aligned.
+template <typename T>
+__host__ __device__ constexpr int decay_bytes(int pieces) {
+  return (tile_rows<T>() * pieces * 4 + 127) / 128 * 128;
+}
 
 struct Params {
   const void *q, *k, *v, *g, *dy;   // for kFeedPlain; g also for kFeedGroup
@@ -80,50 +88,65 @@ struct Params {
   int unit_split0, unit_splits;     // the cuts this launch works on
   int n_units;                      // B x unit_splits x n_cb
   int pieces;                       // groups a block of 32 channels touches at most
+  int g_box;                        // groups per row of g's tile (kFeedGroup); 0: element loads
   int stages, stage_bytes;
   int dg_mode;                      // 0: dg itself, 1: one partial per block, 2: per channel
 };
 
 // ---------------------------------------------------------------------------- two channels
-// One lane's two channels of a row as read from shared memory, and packed fp32 arithmetic on
-// them (one instruction for both).
+// A lane's two channels as one packed pair of fp32 (fma.f32x2 takes both in one instruction).
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pack(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack(F2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// The two channels of a row as they lie in shared memory.
 template <typename T> struct Pair;
 template <> struct Pair<__nv_bfloat16> {
   using Raw = uint32_t;
-  __device__ static float2 f(Raw r) {
-    return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
+  __device__ static F2 f(Raw r) {
+    return pack(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
   }
-  __device__ static void store(__nv_bfloat16 *p, float2 x) {
+  __device__ static void store(__nv_bfloat16 *p, F2 v) {
+    const float2 x = unpack(v);
     const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
     *reinterpret_cast<__nv_bfloat162 *>(p) = b;
   }
 };
 template <> struct Pair<float> {
-  using Raw = float2;
-  __device__ static float2 f(Raw r) { return r; }
-  __device__ static void store(float *p, float2 x) { *reinterpret_cast<float2 *>(p) = x; }
+  using Raw = F2;
+  __device__ static F2 f(Raw r) { return r; }
+  __device__ static void store(float *p, F2 x) { *reinterpret_cast<F2 *>(p) = x; }
 };
 __device__ __forceinline__ void store_one(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
 __device__ __forceinline__ void store_one(float *p, float x) { *p = x; }
 __device__ __forceinline__ float load_one(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
 __device__ __forceinline__ float load_one(const float *p) { return *p; }
 
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  mul_f32x2(d.x, d.y, a.x, a.y, b.x, b.y);
-  return d;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
-      "mov.b64 ra, {%2, %3};\n\t"
-      "mov.b64 rb, {%4, %5};\n\t"
-      "mov.b64 rc, {%6, %7};\n\t"
-      "fma.rn.f32x2 rd, ra, rb, rc;\n\t"
-      "mov.b64 {%0, %1}, rd;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
+// exp(g): one multiply and the hardware's 2^x.  The product's rounding moves the result by
+// |g| 2^-24 of itself, which is small wherever the decay is not (|g| exp(g) < 0.37); 2^x is within
+// 2^-22.  exp(-inf) = 0, and decays below fp32's normal range are 0.
+__device__ __forceinline__ float decay(float g) {
+  float a;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(g * 1.4426950408889634f));
+  return a;
 }
 
 __device__ __forceinline__ void compute_barrier() {
@@ -137,7 +160,7 @@ __device__ __forceinline__ uint8_t *align_stage(uint8_t *dynamic) {
 }
 
 struct Ring {
-  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t full[kMaxStages], empty[kMaxStages], raw[kMaxStages];  // raw: g's tile has landed
   int abort;
 };
 
@@ -163,8 +186,17 @@ __device__ __forceinline__ void fill_decays(const Params &p, float *as, int b, i
   for (int e = thread; e < tile_rows<T>() * p.pieces; e += threads) {
     const int row = e / p.pieces, t = t0 + row, gi = g0 + e % p.pieces;
     // rows past the end leave the state as it is
-    as[e] = t < p.L && gi < p.G ? expf(load_one(g + static_cast<int64_t>(t) * p.G + gi)) : 1.0f;
+    as[e] = t < p.L && gi < p.G ? decay(load_one(g + static_cast<int64_t>(t) * p.G + gi)) : 1.0f;
   }
+}
+
+// The decays of a tile from its rows of g in shared memory (rows past the end were filled with 0
+// and decay by 1).
+template <typename T>
+__device__ __forceinline__ void convert_decays(const Params &p, float *as, const T *g, int first,
+                                               int thread, int threads) {
+  for (int e = thread; e < tile_rows<T>() * p.pieces; e += threads)
+    as[e] = decay(load_one(g + e / p.pieces * p.g_box + first + e % p.pieces));
 }
 
 // Element loads of one stream's tile; zero outside the tensor, as TMA fills.
@@ -187,6 +219,7 @@ __device__ __forceinline__ void feed(const Params &p, Ring &ring, uint8_t *stage
   const int warp = threadIdx.x / 32 - kComputeThreads / 32, lane = threadIdx.x % 32;
   constexpr int kStreams = NS + (kFeed == kFeedChannel ? 1 : 0);
   constexpr int kBytes = stream_bytes<T>();
+  constexpr int kGroups = 16 / static_cast<int>(sizeof(T));  // groups in 16 bytes of g
   if (kFeed == kFeedChannel && (warp != 0 || lane != 0)) return;
   if (kFeed == kFeedGroup && warp == 0 && lane != 0) return;
   int it = 0, last = 0;
@@ -199,6 +232,12 @@ __device__ __forceinline__ void feed(const Params &p, Ring &ring, uint8_t *stage
       if (round > 0 && !mbar_wait(&ring.empty[st], (round - 1) & 1, &ring.abort, p.status, kTimeout))
         goto out;
       if (kFeed != kFeedPlain && warp == 0) {
+        if (kFeed == kFeedGroup && p.g_box) {
+          uint8_t *g_at = buf + NS * kBytes + decay_bytes<T>(p.pieces);
+          const int x = un.cb * kCh / p.d_g / kGroups * kGroups;
+          mbar_arrive_expect_tx(&ring.raw[st], tile_rows<T>() * p.g_box * sizeof(T));
+          tma_load_3d(g_at, maps[4], &ring.raw[st], x, tile * tile_rows<T>(), un.b);
+        }
         mbar_arrive_expect_tx(&ring.full[st], kStreams * kBytes);
 #pragma unroll
         for (int s = 0; s < kStreams; ++s)
@@ -207,9 +246,17 @@ __device__ __forceinline__ void feed(const Params &p, Ring &ring, uint8_t *stage
         last = it + 1;
       }
       if (kFeed == kFeedGroup && warp > 0) {
-        fill_decays<T>(p, reinterpret_cast<float *>(buf + NS * kBytes), un.b, un.cb * kCh,
-                       tile * tile_rows<T>(), threadIdx.x - kComputeThreads - 32,
-                       32 * (kHelperWarps - 1));
+        const int th = threadIdx.x - kComputeThreads - 32, n = 32 * (kHelperWarps - 1);
+        float *as = reinterpret_cast<float *>(buf + NS * kBytes);
+        if (p.g_box) {
+          if (!mbar_wait(&ring.raw[st], round & 1, &ring.abort, p.status, kTimeout)) goto out;
+          convert_decays<T>(p, as,
+                            reinterpret_cast<const T *>(buf + NS * kBytes +
+                                                        decay_bytes<T>(p.pieces)),
+                            un.cb * kCh / p.d_g % kGroups, th, n);
+        } else {
+          fill_decays<T>(p, as, un.b, un.cb * kCh, tile * tile_rows<T>(), th, n);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&ring.full[st]);
       }
@@ -231,6 +278,8 @@ out:
   if (kFeed != kFeedPlain && warp == 0) {
     for (int j = max(0, last - p.stages); j < last; ++j) {
       int no_abort = 0;
+      if (kFeed == kFeedGroup && p.g_box)
+        mbar_wait(&ring.raw[j % p.stages], (j / p.stages) & 1, &no_abort, p.status, kTimeout);
       mbar_wait(&ring.full[j % p.stages], (j / p.stages) & 1, &no_abort, p.status, kTimeout);
     }
   }
@@ -243,6 +292,7 @@ __device__ __forceinline__ void ring_init(const Params &p, Ring &ring) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&ring.full[i], arrivals);
       mbar_init(&ring.empty[i], kComputeThreads / 32);
+      mbar_init(&ring.raw[i], 1);
     }
     ring.abort = 0;
     fence_mbar_init();
@@ -250,62 +300,106 @@ __device__ __forceinline__ void ring_init(const Params &p, Ring &ring) {
   __syncthreads();
 }
 
-// The decays of this lane's two channels in row r of its segment.
+// A lane's decays in the rows of its segment.
+template <typename T, int kFeed> struct Decays;
+template <typename T>
+struct Decays<T, kFeedChannel> {  // from the lane's pairs of g
+  using Held = F2;
+  const uint8_t *at;
+  __device__ Decays(const Params &, const uint8_t *tile, int seg, int l, int)
+      : at(tile + (seg * Rows<T>::R * kCh + 2 * l) * static_cast<int>(sizeof(T))) {}
+  __device__ Held load(int r) const {
+    const float2 g = unpack(Pair<T>::f(*reinterpret_cast<const typename Pair<T>::Raw *>(
+        at + r * kCh * static_cast<int>(sizeof(T)))));
+    return pack(decay(g.x), decay(g.y));
+  }
+  __device__ static F2 pair(Held a) { return a; }
+};
+template <typename T>
+struct Decays<T, kFeedGroup> {  // d_g is even: the two channels share one
+  using Held = float;
+  const float *at;
+  int step;
+  __device__ Decays(const Params &p, const uint8_t *tile, int seg, int l, int c0) {
+    const int c = min(c0 + 2 * l, p.D - 1);
+    at = reinterpret_cast<const float *>(tile) + seg * Rows<T>::R * p.pieces + c / p.d_g -
+         c0 / p.d_g;
+    step = p.pieces;
+  }
+  __device__ Held load(int r) const { return at[r * step]; }
+  __device__ static F2 pair(Held a) { return pack(a, a); }
+};
+template <typename T>
+struct Decays<T, kFeedPlain> {
+  using Held = F2;
+  const float *at;
+  int step, second;
+  __device__ Decays(const Params &p, const uint8_t *tile, int seg, int l, int c0) {
+    const int g0 = c0 / p.d_g, i0 = min(c0 + 2 * l, p.D - 1) / p.d_g - g0;
+    at = reinterpret_cast<const float *>(tile) + seg * Rows<T>::R * p.pieces + i0;
+    second = min(c0 + 2 * l + 1, p.D - 1) / p.d_g - g0 - i0;
+    step = p.pieces;
+  }
+  __device__ Held load(int r) const { return pack(at[r * step], at[r * step + second]); }
+  __device__ static F2 pair(Held a) { return a; }
+};
+
+// A lane's two channels in consecutive rows of a [B, L, D] tensor, from (b, t0) on; rows past the
+// end and channels past D are not written (live: rows to write; hi: whether the second is inside).
 template <typename T, int kFeed>
-struct Decays {
-  const uint8_t *at;  // kFeedChannel: the lane's g pair in its segment's first row; else the rows
-                      // of fp32 decays
-  int pieces, i0, i1;
-  __device__ float2 operator()(int r) const {
-    if (kFeed == kFeedChannel) {
-      const float2 g = Pair<T>::f(*reinterpret_cast<const typename Pair<T>::Raw *>(
-          at + r * kCh * static_cast<int>(sizeof(T))));
-      return make_float2(expf(g.x), expf(g.y));
+struct Out {
+  T *at;
+  uint32_t stride;  // bytes per row; D is below 2^28
+  int live;
+  bool hi;
+  __device__ Out(void *base, const Params &p, int b, int t0, int c, bool dead) {
+    at = static_cast<T *>(base) + (static_cast<int64_t>(b) * p.L + t0) * p.D + c;
+    stride = static_cast<uint32_t>(p.D) * static_cast<uint32_t>(sizeof(T));
+    live = dead || c >= p.D ? 0 : p.L - t0;
+    hi = c + 1 < p.D;
+  }
+  __device__ void put(int r, F2 x) const {
+    if (r >= live) return;
+    T *to = reinterpret_cast<T *>(reinterpret_cast<uint8_t *>(at) +
+                                  static_cast<uint64_t>(stride) * static_cast<uint32_t>(r));
+    if (kFeed != kFeedPlain) {  // rows are a multiple of 16 bytes: a pair is inside or outside
+      Pair<T>::store(to, x);
+    } else {
+      const float2 v = unpack(x);
+      store_one(to, v.x);
+      if (hi) store_one(to + 1, v.y);
     }
-    const float *a = reinterpret_cast<const float *>(at) + r * pieces;
-    return make_float2(a[i0], a[i1]);
   }
 };
 
-template <typename T, int kFeed>
-__device__ __forceinline__ Decays<T, kFeed> decays_at(const Params &p, const uint8_t *streams_end,
-                                                      int seg, int l, int c0) {
-  Decays<T, kFeed> d;
-  constexpr int R = Rows<T>::R;
-  if (kFeed == kFeedChannel) {
-    d.at = streams_end + (seg * R * kCh + 2 * l) * static_cast<int>(sizeof(T));
-    d.pieces = d.i0 = d.i1 = 0;
-  } else {
-    const int g0 = c0 / p.d_g, c = c0 + 2 * l;
-    d.at = streams_end + seg * R * p.pieces * 4;
-    d.pieces = p.pieces;
-    d.i0 = min(c, p.D - 1) / p.d_g - g0;
-    d.i1 = min(c + 1, p.D - 1) / p.d_g - g0;
-  }
-  return d;
-}
-
-// Stores a lane's two channels of one row (nothing outside the tensor).
-template <typename T, int kFeed>
-__device__ __forceinline__ void put(T *row, int c, int D, float2 x) {
-  if (kFeed != kFeedPlain) {  // D is a multiple of 16 bytes: a pair is inside or outside
-    if (c < D) Pair<T>::store(row + c, x);
-  } else {
-    if (c < D) store_one(row + c, x.x);
-    if (c + 1 < D) store_one(row + c + 1, x.y);
-  }
-}
-
-__device__ __forceinline__ float2 get_state(const float *s, int64_t row, int c, int D) {
-  if (!s) return make_float2(0.f, 0.f);
+__device__ __forceinline__ F2 get_state(const float *s, int64_t row, int c, int D) {
+  if (!s) return 0;
   s += row * D;
-  return make_float2(c < D ? s[c] : 0.f, c + 1 < D ? s[c + 1] : 0.f);
+  return pack(c < D ? s[c] : 0.f, c + 1 < D ? s[c + 1] : 0.f);
 }
-__device__ __forceinline__ void put_state(float *s, int64_t row, int c, int D, float2 x) {
+__device__ __forceinline__ void put_state(float *s, int64_t row, int c, int D, F2 v) {
+  const float2 x = unpack(v);
   s += row * D;
   if (c < D) s[c] = x.x;
   if (c + 1 < D) s[c + 1] = x.y;
 }
+// s after the cut with (A, S) in agg[c], agg[c + 1]
+__device__ __forceinline__ F2 through_cut(const float2 *agg, int c, int D, F2 v) {
+  float2 s = unpack(v);
+  if (c < D) s.x = fmaf(agg[c].x, s.x, agg[c].y);
+  if (c + 1 < D) s.y = fmaf(agg[c + 1].x, s.y, agg[c + 1].y);
+  return pack(s.x, s.y);
+}
+__device__ __forceinline__ void put_cut(float2 *agg, int c, int D, F2 a, F2 v) {
+  const float2 A = unpack(a), S = unpack(v);
+  if (c < D) agg[c] = make_float2(A.x, S.x);
+  if (c + 1 < D) agg[c + 1] = make_float2(A.y, S.y);
+}
+
+constexpr F2 kOnes = 0x3f8000003f800000ull;
+constexpr int kWarps = kComputeThreads / 32;
+
+__device__ __forceinline__ F2 from_other_half(F2 x) { return __shfl_xor_sync(0xffffffffu, x, 16); }
 
 // ---------------------------------------------------------------------------- forward
 // kOut: y and the last state (streams k, v, q); otherwise only states: checkpoints, or the (A, S)
@@ -318,95 +412,116 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t dynamic[];
   uint8_t *stages = align_stage(dynamic);
   __shared__ Ring ring;
-  __shared__ float4 joint[2][kSegs][kCh / 2];  // (A, A, S, S) of a segment's two channels
+  __shared__ ulonglong2 joint[2][kWarps][kCh / 2];  // (A, S) of a warp's rows
   constexpr int R = Rows<T>::R, NS = kOut ? 3 : 2, kBytes = stream_bytes<T>();
   using Raw = typename Pair<T>::Raw;
+  using Dec = Decays<T, kFeed>;
   ring_init<kFeed>(p, ring);
   griddep_launch_dependents();
   griddep_wait();
   if (threadIdx.x >= kComputeThreads) {
-    const CUtensorMap *const maps[5] = {&mk, &mv, kOut ? &mq : &mg, &mg, nullptr};
+    const CUtensorMap *const maps[5] = {&mk, &mv, kOut ? &mq : &mg, &mg, &mg};
     const void *const ptrs[5] = {p.k, p.v, p.q, nullptr, nullptr};
     feed<T, kFeed, false, NS>(p, ring, stages, maps, ptrs);
     return;
   }
-  const int lane = threadIdx.x % 32, l = lane % 16, seg = threadIdx.x / 16;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, l = lane % 16;
+  const int seg = threadIdx.x / 16;
+  const bool second = lane >= 16;
   bool dead = false;
   int it = 0;
   for (int u = blockIdx.x; u < p.n_units; u += gridDim.x) {
     const Unit un(p, u);
     const int c0 = un.cb * kCh, c = c0 + 2 * l;
-    // the state before the unit: s0 through the cuts before it
-    float2 carry = make_float2(0.f, 0.f), whole = make_float2(1.f, 1.f);
-    if (kOut || !p.agg || p.ckpt) {
+    const bool from_zero = !kOut && !p.ckpt;  // (A, S) of a cut
+    float2 *agg = p.agg + static_cast<int64_t>(un.b) * p.splits * p.D;
+    F2 carry = 0, whole = kOnes;
+    if (!from_zero) {  // the state before the unit: s0 through the cuts before it
       carry = get_state(p.s0, un.b, c, p.D);
-      if (p.agg)
-        for (int j = 0; j < un.split; ++j) {
-          const float2 *ag = p.agg + (static_cast<int64_t>(un.b) * p.splits + j) * p.D;
-          if (c < p.D) carry.x = fmaf(ag[c].x, carry.x, ag[c].y);
-          if (c + 1 < p.D) carry.y = fmaf(ag[c + 1].x, carry.y, ag[c + 1].y);
-        }
+      for (int j = 0; j < un.split; ++j)
+        carry = through_cut(agg + static_cast<int64_t>(j) * p.D, c, p.D, carry);
     }
     for (int tile = un.tile0; tile < un.tile1; ++tile, ++it) {
       const int st = it % p.stages;
       const uint8_t *buf = stages + st * p.stage_bytes;
       if (!mbar_wait(&ring.full[st], (it / p.stages) & 1, &ring.abort, p.status, kTimeout))
         dead = true;
-      float2 x[R], a[R];
+      F2 x[R];
+      typename Dec::Held a[R];
       Raw qr[R];
-      const Decays<T, kFeed> dec = decays_at<T, kFeed>(p, buf + NS * kBytes, seg, l, c0);
+      const Dec dec(p, buf + NS * kBytes, seg, l, c0);
+      const uint8_t *at = buf + (seg * R * kCh + 2 * l) * static_cast<int>(sizeof(T));
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const int at = ((seg * R + r) * kCh + 2 * l) * static_cast<int>(sizeof(T));
-        x[r] = mul2(Pair<T>::f(*reinterpret_cast<const Raw *>(buf + at)),
-                    Pair<T>::f(*reinterpret_cast<const Raw *>(buf + kBytes + at)));
-        if (kOut) qr[r] = *reinterpret_cast<const Raw *>(buf + 2 * kBytes + at);
-        a[r] = dec(r);
+        const int o = r * kCh * static_cast<int>(sizeof(T));
+        x[r] = mul2(Pair<T>::f(*reinterpret_cast<const Raw *>(at + o)),
+                    Pair<T>::f(*reinterpret_cast<const Raw *>(at + kBytes + o)));
+        if (kOut) qr[r] = *reinterpret_cast<const Raw *>(at + 2 * kBytes + o);
+        a[r] = dec.load(r);
       }
-      float2 A = a[0], S = x[0];
+      F2 A = Dec::pair(a[0]), S = x[0];
 #pragma unroll
       for (int r = 1; r < R; ++r) {
-        S = fma2(a[r], S, x[r]);
-        A = mul2(A, a[r]);
+        S = fma2(Dec::pair(a[r]), S, x[r]);
+        A = mul2(A, Dec::pair(a[r]));
       }
-      joint[it & 1][seg][l] = make_float4(A.x, A.y, S.x, S.y);
+      // the halves of the warp, joined by the first; the second keeps the first's
+      const F2 Ao = from_other_half(A), So = from_other_half(S);
+      if (!second) joint[it & 1][warp][l] = make_ulonglong2(mul2(Ao, A), fma2(Ao, S, So));
       __syncwarp();
       if (lane == 0) mbar_arrive(&ring.empty[st]);  // the segment is in registers
       compute_barrier();
       if (p.ckpt && seg == 0 && !dead)
         put_state(p.ckpt, static_cast<int64_t>(un.b) * p.n_tiles + tile, c, p.D, carry);
-      float2 s = carry;
+      F2 s = carry;
 #pragma unroll
-      for (int j = 0; j < kSegs; ++j) {
-        const float4 m = joint[it & 1][j][l];
-        if (j == seg) s = carry;
-        carry = fma2(make_float2(m.x, m.y), carry, make_float2(m.z, m.w));
-        if (!kOut) whole = mul2(whole, make_float2(m.x, m.y));
+      for (int j = 0; j < kWarps; ++j) {
+        const ulonglong2 m = joint[it & 1][j][l];
+        if (j == warp) s = carry;
+        carry = fma2(m.x, carry, m.y);
+        if (!kOut) whole = mul2(whole, m.x);
       }
-      if (kOut && !dead) {
-        const int t0 = tile * tile_rows<T>() + seg * R;
-        T *row = static_cast<T *>(p.y) + (static_cast<int64_t>(un.b) * p.L + t0) * p.D;
-        const int rows = min(R, p.L - t0);
+      if (kOut) {
+        if (second) s = fma2(Ao, s, So);
+        const Out<T, kFeed> y(p.y, p, un.b, tile * tile_rows<T>() + seg * R, c, dead);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-          s = fma2(a[r], s, x[r]);
-          if (r < rows) put<T, kFeed>(row + static_cast<int64_t>(r) * p.D, c, p.D,
-                                      mul2(Pair<T>::f(qr[r]), s));
+          s = fma2(Dec::pair(a[r]), s, x[r]);
+          y.put(r, mul2(Pair<T>::f(qr[r]), s));
         }
       }
     }
     if (seg == 0 && !dead) {
       if (p.s_out && un.tile1 == p.n_tiles) put_state(p.s_out, un.b, c, p.D, carry);
-      if (!kOut && p.agg && !p.ckpt) {
-        float2 *ag = p.agg + (static_cast<int64_t>(un.b) * p.splits + un.split) * p.D;
-        if (c < p.D) ag[c] = make_float2(whole.x, carry.x);
-        if (c + 1 < p.D) ag[c + 1] = make_float2(whole.y, carry.y);
-      }
+      if (from_zero) put_cut(agg + static_cast<int64_t>(un.split) * p.D, c, p.D, whole, carry);
     }
   }
 }
 
 // ---------------------------------------------------------------------------- backward
+// Sums over `kSpan` neighbouring lanes of one value per row, kSpan rows at a time: each exchange
+// halves the rows a lane holds, so that lane i of the group ends with row i (kSpan - 1 exchanges
+// for kSpan rows).  put(row, group of lanes, sum) gets each row's.
+template <int kSpan, int R, typename F>
+__device__ __forceinline__ void sum_groups(const float (&v)[R], int l, F &&put) {
+#pragma unroll
+  for (int r0 = 0; r0 < R; r0 += kSpan) {
+    float w[kSpan];
+#pragma unroll
+    for (int i = 0; i < kSpan; ++i) w[i] = r0 + i < R ? v[r0 + i] : 0.f;
+#pragma unroll
+    for (int o = kSpan / 2; o >= 1; o /= 2) {
+      const bool up = l & o;
+#pragma unroll
+      for (int i = 0; i < o; ++i) {
+        const float give = up ? w[i] : w[i + o], keep = up ? w[i + o] : w[i];
+        w[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+      }
+    }
+    put(r0 + l % kSpan, l / kSpan, w[0]);
+  }
+}
+
 // kOut: the gradients (streams q, dy, k, v and the checkpoints); otherwise the (A, W) of the
 // unit's time cut from w = 0 (streams q, dy).
 template <typename T, int kFeed, bool kOut>
@@ -417,10 +532,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t dynamic[];
   uint8_t *stages = align_stage(dynamic);
   __shared__ Ring ring;
-  __shared__ float4 joint[2][kSegs][kCh / 2];   // (A, A, S, S)
-  __shared__ float2 joint_w[2][kSegs][kCh / 2];
+  __shared__ ulonglong2 joint[2][kWarps][kCh / 2];  // (A, S) of a warp's rows
+  __shared__ F2 joint_w[2][kWarps][kCh / 2];
   constexpr int R = Rows<T>::R, NS = kOut ? 4 : 2, kBytes = stream_bytes<T>();
   using Raw = typename Pair<T>::Raw;
+  using Dec = Decays<T, kFeed>;
   ring_init<kFeed>(p, ring);
   griddep_launch_dependents();
   griddep_wait();
@@ -430,123 +546,134 @@ __global__ void __launch_bounds__(kThreads, 1)
     feed<T, kFeed, true, NS>(p, ring, stages, maps, ptrs);
     return;
   }
-  const int lane = threadIdx.x % 32, l = lane % 16, seg = threadIdx.x / 16;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, l = lane % 16;
+  const int seg = threadIdx.x / 16;
+  const bool second = lane >= 16;
   bool dead = false;
   int it = 0;
   for (int u = blockIdx.x; u < p.n_units; u += gridDim.x) {
     const Unit un(p, u);
     const int c0 = un.cb * kCh, c = c0 + 2 * l;
-    // what reaches the last state of the unit: ds_out through the cuts after it
-    float2 w_in = make_float2(0.f, 0.f), whole = make_float2(1.f, 1.f);
-    if (kOut) {
+    float2 *agg = p.agg + static_cast<int64_t>(un.b) * p.splits * p.D;
+    F2 w_in = 0, whole = kOnes;
+    if (kOut) {  // what reaches the last state of the unit: ds_out through the cuts after it
       w_in = get_state(p.ds_out, un.b, c, p.D);
-      for (int j = p.splits - 1; j > un.split; --j) {
-        const float2 *ag = p.agg + (static_cast<int64_t>(un.b) * p.splits + j) * p.D;
-        if (c < p.D) w_in.x = fmaf(ag[c].x, w_in.x, ag[c].y);
-        if (c + 1 < p.D) w_in.y = fmaf(ag[c + 1].x, w_in.y, ag[c + 1].y);
-      }
+      for (int j = p.splits - 1; j > un.split; --j)
+        w_in = through_cut(agg + static_cast<int64_t>(j) * p.D, c, p.D, w_in);
     }
     for (int tile = un.tile1 - 1; tile >= un.tile0; --tile, ++it) {
       const int st = it % p.stages;
       const uint8_t *buf = stages + st * p.stage_bytes;
-      float2 s = make_float2(0.f, 0.f);
+      F2 s = 0;
       if (kOut) s = get_state(p.ckpt, static_cast<int64_t>(un.b) * p.n_tiles + tile, c, p.D);
       if (!mbar_wait(&ring.full[st], (it / p.stages) & 1, &ring.abort, p.status, kTimeout))
         dead = true;
       Raw qr[R], dyr[R], kr[R], vr[R];
-      float2 a[R];
-      const Decays<T, kFeed> dec = decays_at<T, kFeed>(p, buf + NS * kBytes, seg, l, c0);
+      typename Dec::Held a[R];
+      const Dec dec(p, buf + NS * kBytes, seg, l, c0);
+      const uint8_t *at = buf + (seg * R * kCh + 2 * l) * static_cast<int>(sizeof(T));
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const int at = ((seg * R + r) * kCh + 2 * l) * static_cast<int>(sizeof(T));
-        qr[r] = *reinterpret_cast<const Raw *>(buf + at);
-        dyr[r] = *reinterpret_cast<const Raw *>(buf + kBytes + at);
+        const int o = r * kCh * static_cast<int>(sizeof(T));
+        qr[r] = *reinterpret_cast<const Raw *>(at + o);
+        dyr[r] = *reinterpret_cast<const Raw *>(at + kBytes + o);
         if (kOut) {
-          kr[r] = *reinterpret_cast<const Raw *>(buf + 2 * kBytes + at);
-          vr[r] = *reinterpret_cast<const Raw *>(buf + 3 * kBytes + at);
+          kr[r] = *reinterpret_cast<const Raw *>(at + 2 * kBytes + o);
+          vr[r] = *reinterpret_cast<const Raw *>(at + 3 * kBytes + o);
         }
-        a[r] = dec(r);
+        a[r] = dec.load(r);
       }
-      float2 A = make_float2(1.f, 1.f), S = make_float2(0.f, 0.f), W = S;
+      F2 A = kOnes, S = 0, W = 0;
 #pragma unroll
       for (int r = R - 1; r >= 0; --r)
-        W = mul2(a[r], fma2(Pair<T>::f(qr[r]), Pair<T>::f(dyr[r]), W));
+        W = mul2(Dec::pair(a[r]), fma2(Pair<T>::f(qr[r]), Pair<T>::f(dyr[r]), W));
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        A = mul2(A, a[r]);
-        if (kOut) S = fma2(a[r], S, mul2(Pair<T>::f(kr[r]), Pair<T>::f(vr[r])));
+        A = mul2(A, Dec::pair(a[r]));
+        if (kOut) S = fma2(Dec::pair(a[r]), S, mul2(Pair<T>::f(kr[r]), Pair<T>::f(vr[r])));
       }
-      joint[it & 1][seg][l] = make_float4(A.x, A.y, S.x, S.y);
-      joint_w[it & 1][seg][l] = W;
+      const F2 Ao = from_other_half(A), So = from_other_half(S), Wo = from_other_half(W);
+      if (!second) {  // S through the second half, W through the first
+        joint[it & 1][warp][l] = make_ulonglong2(mul2(Ao, A), fma2(Ao, S, So));
+        joint_w[it & 1][warp][l] = fma2(A, Wo, W);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ring.empty[st]);
       compute_barrier();
-      float2 w = w_in, sj = s;
+      F2 w = w_in, state = s;
 #pragma unroll
-      for (int j = 0; j < kSegs; ++j) {  // states before each segment, in order
-        const float4 m = joint[it & 1][j][l];
-        if (j == seg) s = sj;
-        if (kOut) sj = fma2(make_float2(m.x, m.y), sj, make_float2(m.z, m.w));
+      for (int j = 0; j < kWarps; ++j) {  // states before each warp's rows, in order
+        if (!kOut) break;
+        const ulonglong2 m = joint[it & 1][j][l];
+        if (j == warp) s = state;
+        state = fma2(m.x, state, m.y);
       }
 #pragma unroll
-      for (int j = kSegs - 1; j >= 0; --j) {  // what reaches the end of each, backwards
-        const float4 m = joint[it & 1][j][l];
-        if (j == seg) w = w_in;
-        w_in = fma2(make_float2(m.x, m.y), w_in, joint_w[it & 1][j][l]);
-        if (!kOut) whole = mul2(whole, make_float2(m.x, m.y));
+      for (int j = kWarps - 1; j >= 0; --j) {  // what reaches the end of each, backwards
+        const F2 m = joint[it & 1][j][l].x;
+        if (j == warp) w = w_in;
+        w_in = fma2(m, w_in, joint_w[it & 1][j][l]);
+        if (!kOut) whole = mul2(whole, m);
       }
       if (kOut) {
+        if (second)
+          s = fma2(Ao, s, So);
+        else
+          w = fma2(Ao, w, Wo);
         const int t0 = tile * tile_rows<T>() + seg * R;
-        const int rows = min(R, p.L - t0);
-        const int64_t row0 = static_cast<int64_t>(un.b) * p.L + t0;
-        float2 before[R];  // s_{t-1}
+        F2 before[R];  // s_{t-1}
+        const Out<T, kFeed> dq(p.dq, p, un.b, t0, c, dead);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           before[r] = s;
-          const float2 k = Pair<T>::f(kr[r]), v = Pair<T>::f(vr[r]);
-          s = fma2(a[r], s, mul2(k, v));
-          if (r < rows && !dead)
-            put<T, kFeed>(static_cast<T *>(p.dq) + (row0 + r) * p.D, c, p.D,
-                          mul2(Pair<T>::f(dyr[r]), s));
+          s = fma2(Dec::pair(a[r]), s, mul2(Pair<T>::f(kr[r]), Pair<T>::f(vr[r])));
+          dq.put(r, mul2(Pair<T>::f(dyr[r]), s));
         }
+        const Out<T, kFeed> dk(p.dk, p, un.b, t0, c, dead), dv(p.dv, p, un.b, t0, c, dead);
+        const Out<T, kFeed> dg(p.dg, p, un.b, t0, c, dead);  // where d_g = 1
+        float sum[R];
 #pragma unroll
         for (int r = R - 1; r >= 0; --r) {
-          const float2 un_t = fma2(Pair<T>::f(qr[r]), Pair<T>::f(dyr[r]), w);
-          w = mul2(a[r], un_t);
-          const float2 dg = mul2(w, before[r]);
-          const bool live = r < rows && !dead;
-          if (live) {
-            put<T, kFeed>(static_cast<T *>(p.dk) + (row0 + r) * p.D, c, p.D,
-                          mul2(un_t, Pair<T>::f(vr[r])));
-            put<T, kFeed>(static_cast<T *>(p.dv) + (row0 + r) * p.D, c, p.D,
-                          mul2(un_t, Pair<T>::f(kr[r])));
-          }
-          if (kFeed == kFeedChannel || p.d_g == 1) {
-            if (live) put<T, kFeed>(static_cast<T *>(p.dg) + (row0 + r) * p.D, c, p.D, dg);
+          const F2 ut = fma2(Pair<T>::f(qr[r]), Pair<T>::f(dyr[r]), w);
+          w = mul2(Dec::pair(a[r]), ut);
+          const F2 d = mul2(w, before[r]);
+          dk.put(r, mul2(ut, Pair<T>::f(vr[r])));
+          dv.put(r, mul2(ut, Pair<T>::f(kr[r])));
+          if (kFeed == kFeedChannel || (kFeed == kFeedPlain && p.d_g == 1)) {
+            dg.put(r, d);
           } else if (p.dg_mode == 2) {
-            if (live) put_state(p.dg_part, row0 + r, c, p.D, dg);
+            if (r < dg.live)
+              put_state(p.dg_part, static_cast<int64_t>(un.b) * p.L + t0 + r, c, p.D, d);
           } else {
-            // groups of 2, 4, ..., 16 channels, or whole blocks: a sum over neighbouring lanes
-            const int span = min(p.d_g, kCh) / 2;
-            float sum = dg.x + dg.y;
-            for (int o = 1; o < span; o *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (live && c < p.D && l % span == 0) {
-              if (p.dg_mode == 1)
-                p.dg_part[(row0 + r) * p.n_cb + un.cb] = sum;
-              else
-                store_one(static_cast<T *>(p.dg) + (row0 + r) * p.G + c / p.d_g, sum);
-            }
+            const float2 two = unpack(d);
+            sum[r] = two.x + two.y;
+          }
+        }
+        if (kFeed != kFeedChannel && p.d_g > 1 && p.dg_mode != 2) {
+          // groups of 2, 4, ..., 16 channels or whole blocks: sums over neighbouring lanes
+          const int64_t row0 = static_cast<int64_t>(un.b) * p.L + t0;
+          const int rows = dead ? 0 : min(R, p.L - t0);
+          const int g0 = p.dg_mode == 1 ? 0 : c0 / p.d_g;
+          const auto put = [&](int r, int grp, float v) {
+            if (r >= rows) return;
+            if (p.dg_mode == 1)
+              p.dg_part[(row0 + r) * p.n_cb + un.cb] = v;
+            else if (g0 + grp < p.G)
+              store_one(static_cast<T *>(p.dg) + (row0 + r) * p.G + g0 + grp, v);
+          };
+          switch (p.d_g) {
+            case 2: sum_groups<1>(sum, l, put); break;
+            case 4: sum_groups<2>(sum, l, put); break;
+            case 8: sum_groups<4>(sum, l, put); break;
+            case 16: sum_groups<8>(sum, l, put); break;
+            default: sum_groups<16>(sum, l, put);
           }
         }
       }
     }
     if (seg == 0 && !dead) {
       if (kOut && p.ds0 && un.tile0 == 0) put_state(p.ds0, un.b, c, p.D, w_in);
-      if (!kOut) {
-        float2 *ag = p.agg + (static_cast<int64_t>(un.b) * p.splits + un.split) * p.D;
-        if (c < p.D) ag[c] = make_float2(whole.x, w_in.x);
-        if (c + 1 < p.D) ag[c + 1] = make_float2(whole.y, w_in.y);
-      }
+      if (!kOut) put_cut(agg + static_cast<int64_t>(un.split) * p.D, c, p.D, whole, w_in);
     }
   }
 }
@@ -588,13 +715,13 @@ __global__ void __launch_bounds__(128)
   const T *gr = g + b * G;
   if (d_g == 1) gv = *reinterpret_cast<const Vt *>(gr + c);
   int grp = c / d_g, left = d_g - c % d_g;  // channels of group grp from c on
-  float a = d_g == 1 ? 0.f : expf(load_one(gr + grp));
+  float a = d_g == 1 ? 0.f : decay(load_one(gr + grp));
 #pragma unroll
   for (int e = 0; e < VN; ++e) {
     if (d_g == 1) {
-      a = expf(load_one(&gv.e[e]));
+      a = decay(load_one(&gv.e[e]));
     } else if (left == 0) {
-      a = expf(load_one(gr + ++grp));
+      a = decay(load_one(gr + ++grp));
       left = d_g;
     }
     --left;

@@ -34,7 +34,8 @@ extern "C" {
  * The state is fp32 throughout; y is rounded once.  Sums have a fixed order: results are the
  * same in every call on one device.
  * Any B, L, D, d_g dividing D and element-aligned pointers; rows that are a multiple of 16 bytes
- * in 16-byte aligned tensors take the fast path (TMA).  L and D below 2^31.
+ * in 16-byte aligned tensors and d_g 1 or even take the fast path (TMA).  L < 2^31 - 4096,
+ * D <= 2^28.
  * workspace: at least hyena_scan_workspace_bytes(B, L, D, d_g, dtype) bytes, 16-byte aligned;
  * NULL where that is 0.
  * B == 0 or L == 0: nothing is launched, except that L == 0 copies s0 (zeros if NULL) to s_out.
