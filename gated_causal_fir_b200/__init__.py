@@ -16,6 +16,10 @@ from . import _native
 from ._native import (HYENA_ALGO_AUTO, HYENA_ALGO_DIRECT, HYENA_ALGO_FFT, HYENA_ALGO_TENSOR,
                       HYENA_ALGO_WINDOW, HYENA_DEVICE_F16_RANGE, HYENA_DEVICE_TIMEOUT,
                       HYENA_DTYPE_BF16, HYENA_DTYPE_F32, ALGO_NAMES, HyenaError)
+from ._native import (HYENA_ACT_GELU, HYENA_ACT_LOGSIGMOID, HYENA_ACT_NONE, HYENA_ACT_SIGMOID,
+                      HYENA_ACT_SILU)
+from .projection import (hyena_proj_bwd, hyena_proj_bwd_workspace_bytes, hyena_proj_fwd,
+                         hyena_proj_workspace_bytes)
 from .recurrence import (hyena_scan_bwd, hyena_scan_bwd_workspace_bytes, hyena_scan_ckpt,
                          hyena_scan_fwd, hyena_scan_step, hyena_scan_workspace_bytes)
 
@@ -33,6 +37,9 @@ __all__ = [
     "hyena_conv_fwd_from_host_workspace_bytes",
     "hyena_scan_fwd", "hyena_scan_bwd", "hyena_scan_step", "hyena_scan_ckpt",
     "hyena_scan_workspace_bytes", "hyena_scan_bwd_workspace_bytes",
+    "hyena_proj_fwd", "hyena_proj_bwd", "hyena_proj_workspace_bytes",
+    "hyena_proj_bwd_workspace_bytes", "HYENA_ACT_NONE", "HYENA_ACT_GELU", "HYENA_ACT_SILU",
+    "HYENA_ACT_SIGMOID", "HYENA_ACT_LOGSIGMOID",
 ]
 
 

@@ -30,6 +30,14 @@ HYENA_ALGO_FFT = 4
 ALGO_NAMES = {HYENA_ALGO_AUTO: "auto", HYENA_ALGO_TENSOR: "tensor", HYENA_ALGO_WINDOW: "window",
               HYENA_ALGO_DIRECT: "direct", HYENA_ALGO_FFT: "fft"}
 
+HYENA_ACT_NONE = 0
+HYENA_ACT_GELU = 1
+HYENA_ACT_SILU = 2
+HYENA_ACT_SIGMOID = 3
+HYENA_ACT_LOGSIGMOID = 4
+ACT_CODES = {"none": HYENA_ACT_NONE, "gelu": HYENA_ACT_GELU, "silu": HYENA_ACT_SILU,
+             "sigmoid": HYENA_ACT_SIGMOID, "logsigmoid": HYENA_ACT_LOGSIGMOID}
+
 HYENA_DEVICE_TIMEOUT = 1
 HYENA_DEVICE_F16_RANGE = 2
 
@@ -83,6 +91,10 @@ MIXER_SIGNATURES = {
     "hyena_scan_ckpt_tiles": (_i64, [_i64, _i32]),
     "hyena_scan_bwd": (_i32, [_vp] * 13 + [_i64] * 3 + [_i32, _i32, _vp, _sz, _vp]),
     "hyena_scan_bwd_workspace_bytes": (_i64, [_i64, _i64, _i64, _i32, _i32, _i32]),
+    "hyena_proj_fwd": (_i32, [_vp] * 6 + [_i64] * 3 + [_i32, _i32, _vp, _sz, _vp]),
+    "hyena_proj_workspace_bytes": (_i64, [_i64, _i64, _i64, _i32]),
+    "hyena_proj_bwd": (_i32, [_vp] * 8 + [_i64] * 3 + [_i32, _i32, _vp, _sz, _vp]),
+    "hyena_proj_bwd_workspace_bytes": (_i64, [_i64, _i64, _i64, _i32, _i32]),
     "hyena_scan_step": (_i32, [_vp] * 7 + [_i64, _i64, _i32, _i32, _vp]),
 }
 

@@ -13,7 +13,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libhyena_conv.so")
 INCLUDE = os.path.join(ROOT, "include")
-SOURCES = [os.path.join(CSRC, f) for f in ("hyena_conv.cu", "hyena_scan.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("hyena_conv.cu", "hyena_scan.cu", "hyena_proj.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + [
     os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE) if f.endswith(".h")]
 

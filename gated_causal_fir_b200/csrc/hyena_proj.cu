@@ -1,0 +1,444 @@
+// hyena_proj.cu -- host side of the projections (include/hyena_mixer.h): argument checks, the
+// choice of tiles and k cuts, TMA descriptors and launches of the kernels in proj.cuh.
+#include <algorithm>
+#include <cstdint>
+#include <limits>
+#include <mutex>
+
+#include "host_util.h"
+#include "hyena_mixer.h"
+#include "proj.cuh"
+
+namespace {
+
+namespace pj = hyena::proj;
+using hyena::host::aligned;
+using hyena::host::overlap;
+using hyena::host::round_up;
+
+constexpr int64_t kMaxDim = int64_t{1} << 30;
+constexpr int kSms = 148;
+constexpr int kMaxSplits = 16;
+
+int64_t elem(int dtype) { return dtype == HYENA_DTYPE_F32 ? 4 : 2; }
+int planes(int dtype) { return dtype == HYENA_DTYPE_F32 ? 3 : 1; }
+
+// ------------------------------------------------------------------------------- plan
+enum Shape { kPair256 = 0, kOne128 = 1, kOne64 = 2 };
+
+struct Plan {
+  int shape, splits, kb, pairs, per;  // per: blocks per split
+  int64_t tiles_m, tiles_n;
+};
+
+// The tile shape and the number of k cuts with the least estimated time: waves of persistent
+// workers x (k-blocks of one worker's tile x the time of a block + its epilogue), and for cut
+// products a second kernel over the partial sums.
+Plan plan_of(int64_t M, int64_t N, int64_t K, int dtype) {
+  const struct {
+    int tm, tn, workers;
+    double block, tail;  // ns per k-block of 64, per tile
+  } shapes[] = {{256, 256, kSms / 2, 290, 1500}, {128, 128, kSms, 190, 900}, {128, 64, kSms, 150, 600}};
+  Plan best{};
+  double best_ns = 0;
+  const int kb = static_cast<int>((K + pj::kBK - 1) / pj::kBK), pairs = dtype == HYENA_DTYPE_F32 ? 6 : 1;
+  const int64_t total = static_cast<int64_t>(kb) * pairs;
+  for (int s = 0; s < 3; ++s) {
+    const int64_t tm = (M + shapes[s].tm - 1) / shapes[s].tm, tn = (N + shapes[s].tn - 1) / shapes[s].tn;
+    for (int want = 1; want <= kMaxSplits; ++want) {
+      const int64_t per = (total + want - 1) / want;
+      const int splits = static_cast<int>((total + per - 1) / per);
+      if (splits != want || (want > 1 && (per < 4 || tm * tn * want > 2 * shapes[s].workers))) continue;
+      const int64_t waves = (tm * tn * splits + shapes[s].workers - 1) / shapes[s].workers;
+      double ns = static_cast<double>(waves) * (static_cast<double>(per) * shapes[s].block + shapes[s].tail);
+      if (splits > 1) ns += 2500 + static_cast<double>(splits) * M * N * 8 / 4000;
+      if (best_ns == 0 || ns < best_ns) {
+        best_ns = ns;
+        best = Plan{s, splits, kb, pairs, static_cast<int>(per), tm, tn};
+      }
+    }
+  }
+  return best;
+}
+
+int64_t partial_bytes(int64_t M, int64_t N, int64_t K, int dtype) {
+  const int s = plan_of(M, N, K, dtype).splits;
+  return s > 1 ? round_up(s * M * N * 4, 256) : 0;
+}
+
+// An operand [rows][cols] in memory: `ptr` with rows of `ld` elements, as bf16 planes.
+struct Operand {
+  const void *ptr;
+  int64_t rows, cols, ld;
+};
+
+bool needs_pack(int64_t cols, int dtype) { return dtype == HYENA_DTYPE_F32 || cols % 8 != 0; }
+int64_t pack_bytes(int64_t rows, int64_t cols, int dtype) {
+  return round_up(planes(dtype) * rows * round_up(cols, 8) * 2, 256);
+}
+
+int encode(CUtensorMap *m, const Operand &o, int n_planes, int box_rows) {
+  hyena::host::EncodeTiledFn enc = hyena::host::encode_tiled();
+  if (!enc) return HYENA_ERR_CUDA;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(o.cols), static_cast<cuuint64_t>(o.rows),
+                              static_cast<cuuint64_t>(n_planes)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(o.ld) * 2,
+                                 static_cast<cuuint64_t>(o.rows * o.ld) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(o.ptr), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? HYENA_OK
+             : HYENA_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------------------- launches
+struct Device {
+  hyena::host::DeviceInfo info;
+  int pairs;  // resident pairs of CTAs
+};
+
+template <typename T, int kCG, int kBN, bool kAMn, bool kBMn>
+cudaError_t allow(int *resident) {
+  using L = pj::Tile<kCG, kBN>;
+  auto *fn = pj::proj_kernel<T, kCG, kBN, kAMn, kBMn>;
+  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+  if (e == cudaSuccess && kCG == 2 && resident) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {2, 1, 1};
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(kSms);
+    cfg.blockDim = dim3(pj::kThreads);
+    cfg.dynamicSmemBytes = L::kSmem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(resident, fn, &cfg);
+  }
+  return e;
+}
+template <typename T, bool kAMn, bool kBMn>
+cudaError_t allow_all(int *resident) {
+  cudaError_t e = allow<T, 2, 256, kAMn, kBMn>(resident);
+  if (e == cudaSuccess) e = allow<T, 1, 128, kAMn, kBMn>(nullptr);
+  if (e == cudaSuccess) e = allow<T, 1, 64, kAMn, kBMn>(nullptr);
+  return e;
+}
+
+int prepare_device(Device *d) {
+  if (hyena::host::device_info(&d->info) != HYENA_OK) return HYENA_ERR_CUDA;
+  constexpr int kMaxDevices = 64;
+  static std::once_flag once[kMaxDevices];
+  static cudaError_t err[kMaxDevices];
+  static int pairs[kMaxDevices];
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return HYENA_ERR_CUDA;
+  std::call_once(once[dev], [dev]() {
+    int r = 0;
+    cudaError_t e = allow_all<float, false, false>(&r);
+    if (e == cudaSuccess) e = allow_all<float, false, true>(nullptr);
+    if (e == cudaSuccess) e = allow_all<float, true, true>(nullptr);
+    if (e == cudaSuccess) e = allow_all<__nv_bfloat16, false, false>(nullptr);
+    if (e == cudaSuccess) e = allow_all<__nv_bfloat16, false, true>(nullptr);
+    if (e == cudaSuccess) e = allow_all<__nv_bfloat16, true, true>(nullptr);
+    err[dev] = e;
+    pairs[dev] = std::max(1, r);
+  });
+  d->pairs = pairs[dev];
+  return err[dev] == cudaSuccess ? HYENA_OK : HYENA_ERR_CUDA;
+}
+
+template <typename T, int kCG, int kBN, bool kAMn, bool kBMn>
+cudaError_t launch_shape(const CUtensorMap &ma, const CUtensorMap &mb, const pj::Params &p,
+                         const Device &d, cudaStream_t stream) {
+  using L = pj::Tile<kCG, kBN>;
+  const int64_t works = static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.splits;
+  const int64_t workers = std::min<int64_t>(works, kCG == 2 ? d.pairs : d.info.sm_count);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {2, 1, 1};
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(workers * kCG));
+  cfg.blockDim = dim3(pj::kThreads);
+  cfg.dynamicSmemBytes = L::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = kCG == 2 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, pj::proj_kernel<T, kCG, kBN, kAMn, kBMn>, ma, mb, p);
+}
+
+// C = A B^T with its epilogue.  p: outputs, epilogue and status; K: the reduced dimension.  a, b:
+// operands as they lie (kAMn / kBMn: [k][m] / [k][n]).
+template <typename T, bool kAMn, bool kBMn>
+int product(const Operand &a, const Operand &b, int64_t K, pj::Params p, int dtype, float *partial,
+            const Device &d, cudaStream_t stream) {
+  const Plan pl = plan_of(p.M, p.N, K, dtype);
+  if (pl.tiles_m * pl.tiles_n * pl.splits > std::numeric_limits<int32_t>::max())
+    return HYENA_ERR_UNSUPPORTED;
+  p.kb = pl.kb;
+  p.pairs = pl.pairs;
+  p.tiles_m = static_cast<int>(pl.tiles_m);
+  p.tiles_n = static_cast<int>(pl.tiles_n);
+  p.splits = pl.splits;
+  p.kb_per_split = pl.per;
+  p.group_m = pl.shape == kPair256 ? 8 : 16;
+  p.partial = partial;
+  const int64_t per16 = 16 / elem(dtype);
+  p.vec = p.N % per16 == 0 && aligned(p.y, 16) && aligned(p.z, 16) && aligned(p.residual, 16);
+  CUtensorMap ma, mb;
+  const int b_rows = pl.shape == kOne64 ? 64 : 128;
+  if (encode(&ma, a, planes(dtype), kAMn ? 64 : pj::kRows) ||
+      encode(&mb, b, planes(dtype), kBMn ? 64 : b_rows))
+    return HYENA_ERR_CUDA;
+  cudaError_t e;
+  switch (pl.shape) {
+    case kPair256: e = launch_shape<T, 2, 256, kAMn, kBMn>(ma, mb, p, d, stream); break;
+    case kOne128: e = launch_shape<T, 1, 128, kAMn, kBMn>(ma, mb, p, d, stream); break;
+    default: e = launch_shape<T, 1, 64, kAMn, kBMn>(ma, mb, p, d, stream);
+  }
+  if (e != cudaSuccess) return HYENA_ERR_CUDA;
+  if (p.splits == 1) return HYENA_OK;
+  const int64_t n = static_cast<int64_t>(p.M) * ((p.N + 3) / 4);
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((n + 255) / 256, 8 * d.info.sm_count));
+  return hyena::host::launch(pj::proj_join_kernel<T>, dim3(grid), dim3(256), 0, stream, p) ==
+                 cudaSuccess
+             ? HYENA_OK
+             : HYENA_ERR_CUDA;
+}
+
+// An input as a product's operand: itself, or (`at` advances) bf16 planes in the workspace.
+template <typename T>
+int operand(Operand *o, const void *ptr, int64_t rows, int64_t cols, int dtype, uint8_t *&at,
+            const Device &d, cudaStream_t stream) {
+  if (!needs_pack(cols, dtype)) {
+    *o = Operand{ptr, rows, cols, cols};
+    return HYENA_OK;
+  }
+  const int64_t ld = round_up(cols, 8), n = rows * (ld / 8);
+  *o = Operand{at, rows, cols, ld};
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((n + 255) / 256, 16 * d.info.sm_count));
+  const cudaError_t e = hyena::host::launch(
+      pj::proj_pack_kernel<T>, dim3(grid), dim3(256), 0, stream, static_cast<const T *>(ptr),
+      reinterpret_cast<__nv_bfloat16 *>(at), rows, static_cast<int>(cols), static_cast<int>(ld));
+  at += pack_bytes(rows, cols, dtype);
+  return e == cudaSuccess ? HYENA_OK : HYENA_ERR_CUDA;
+}
+
+int check_shape(int64_t M, int64_t N, int64_t K, int dtype) {
+  if (dtype != HYENA_DTYPE_BF16 && dtype != HYENA_DTYPE_F32) return HYENA_ERR_INVALID_ARG;
+  if (M < 0 || N < 1 || K < 1 || M > kMaxDim || N > kMaxDim || K > kMaxDim)
+    return HYENA_ERR_INVALID_ARG;
+  return HYENA_OK;
+}
+
+struct Buf {
+  const void *p;
+  int64_t bytes;
+};
+bool clash(std::initializer_list<Buf> outs, std::initializer_list<Buf> ins) {
+  for (const Buf *o = outs.begin(); o != outs.end(); ++o) {
+    for (const Buf &i : ins)
+      if (overlap(o->p, o->bytes, i.p, i.bytes)) return true;
+    for (const Buf *q = o + 1; q != outs.end(); ++q)
+      if (overlap(o->p, o->bytes, q->p, q->bytes)) return true;
+  }
+  return false;
+}
+
+template <typename T>
+int forward(const void *x, const void *w, const pj::Params &p, int64_t K, int dtype, uint8_t *ws,
+            const Device &d, cudaStream_t stream) {
+  Operand a, b;
+  int rc = operand<T>(&a, x, p.M, K, dtype, ws, d, stream);
+  if (rc == HYENA_OK) rc = operand<T>(&b, w, p.N, K, dtype, ws, d, stream);
+  if (rc != HYENA_OK) return rc;
+  return product<T, false, false>(a, b, K, p, dtype, reinterpret_cast<float *>(ws), d, stream);
+}
+
+template <typename T, int kAct>
+cudaError_t launch_dz(const void *dy, const void *z, __nv_bfloat16 *dz, float *part, int64_t M,
+                      int64_t N, int64_t ld, int vec, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>((ld + pj::kDbCols - 1) / pj::kDbCols),
+                  static_cast<unsigned>((M + pj::kDbRows - 1) / pj::kDbRows));
+  return hyena::host::launch(pj::proj_dz_kernel<T, kAct>, grid, dim3(256), 0, stream,
+                             static_cast<const T *>(dy), static_cast<const T *>(z), dz, part, M,
+                             static_cast<int>(N), static_cast<int>(ld), vec);
+}
+
+bool needs_dz(int64_t N, int act, int dtype) {
+  return act != HYENA_ACT_NONE || needs_pack(N, dtype);
+}
+int64_t db_blocks(int64_t M) { return (M + pj::kDbRows - 1) / pj::kDbRows; }
+
+template <typename T>
+int backward(const void *x, const void *w, const void *z, const void *dy, const void *dx_add,
+             void *dx, void *dw, float *db, int64_t M, int64_t N, int64_t K, int act, int dtype,
+             uint8_t *ws, const Device &d, cudaStream_t stream) {
+  Operand dzo{dy, M, N, N};
+  const bool make_dz = needs_dz(N, act, dtype) && (dx || dw);
+  if (make_dz || db) {
+    const int64_t ld = round_up(N, 8);
+    __nv_bfloat16 *dz = nullptr;
+    if (make_dz) {
+      dz = reinterpret_cast<__nv_bfloat16 *>(ws);
+      dzo = Operand{ws, M, N, ld};
+      ws += pack_bytes(M, N, dtype);
+    }
+    float *part = nullptr;
+    if (db) {
+      part = reinterpret_cast<float *>(ws);
+      ws += round_up(db_blocks(M) * N * 4, 256);
+    }
+    const int vec = N % (16 / elem(dtype)) == 0 ? 1 : 0;
+    cudaError_t e;
+    switch (act) {
+      case HYENA_ACT_GELU: e = launch_dz<T, pj::kGelu>(dy, z, dz, part, M, N, ld, vec, stream); break;
+      case HYENA_ACT_SILU: e = launch_dz<T, pj::kSilu>(dy, z, dz, part, M, N, ld, vec, stream); break;
+      case HYENA_ACT_SIGMOID:
+        e = launch_dz<T, pj::kSigmoid>(dy, z, dz, part, M, N, ld, vec, stream);
+        break;
+      case HYENA_ACT_LOGSIGMOID:
+        e = launch_dz<T, pj::kLogSigmoid>(dy, z, dz, part, M, N, ld, vec, stream);
+        break;
+      default: e = launch_dz<T, pj::kNone>(dy, z, dz, part, M, N, ld, vec, stream);
+    }
+    if (e == cudaSuccess && db)
+      e = hyena::host::launch(pj::proj_db_kernel, dim3(static_cast<unsigned>((N + 31) / 32)),
+                              dim3(256), 0, stream, static_cast<const float *>(part), db,
+                              static_cast<int>(db_blocks(M)), static_cast<int>(N));
+    if (e != cudaSuccess) return HYENA_ERR_CUDA;
+  }
+  pj::Params p{};
+  p.status = d.info.status;
+  p.act = pj::kNone;
+  int rc = HYENA_OK;
+  if (dx) {  // [M, K] = dz [M, N] w [N, K]
+    Operand wo;
+    uint8_t *at = ws;
+    rc = operand<T>(&wo, w, N, K, dtype, at, d, stream);
+    if (rc != HYENA_OK) return rc;
+    p.M = static_cast<int>(M);
+    p.N = static_cast<int>(K);
+    p.residual = dx_add;
+    p.y = dx;
+    rc = product<T, false, true>(dzo, wo, N, p, dtype, reinterpret_cast<float *>(at), d, stream);
+    if (rc != HYENA_OK) return rc;
+  }
+  if (dw) {  // [N, K] = dz^T [N, M] x [M, K]
+    Operand xo;
+    uint8_t *at = ws;
+    rc = operand<T>(&xo, x, M, K, dtype, at, d, stream);
+    if (rc != HYENA_OK) return rc;
+    p.M = static_cast<int>(N);
+    p.N = static_cast<int>(K);
+    p.residual = nullptr;
+    p.y = dw;
+    rc = product<T, true, true>(dzo, xo, M, p, dtype, reinterpret_cast<float *>(at), d, stream);
+  }
+  return rc;
+}
+
+bool misaligned16(std::initializer_list<const void *> ptrs) {
+  for (const void *p : ptrs)
+    if (!aligned(p, 16)) return true;
+  return false;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t hyena_proj_workspace_bytes(int64_t M, int64_t N, int64_t K, int dtype) {
+  if (check_shape(M, N, K, dtype) != HYENA_OK) return -HYENA_ERR_INVALID_ARG;
+  if (M == 0) return 0;
+  int64_t n = partial_bytes(M, N, K, dtype);
+  if (needs_pack(K, dtype)) n += pack_bytes(M, K, dtype) + pack_bytes(N, K, dtype);
+  return n;
+}
+
+int64_t hyena_proj_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int act, int dtype) {
+  if (check_shape(M, N, K, dtype) != HYENA_OK || act < HYENA_ACT_NONE || act > HYENA_ACT_LOGSIGMOID)
+    return -HYENA_ERR_INVALID_ARG;
+  if (M == 0) return 0;
+  int64_t n = round_up(db_blocks(M) * N * 4, 256);
+  if (needs_dz(N, act, dtype)) n += pack_bytes(M, N, dtype);
+  // the two products run one after the other in the same room
+  const bool pack = needs_pack(K, dtype);
+  const int64_t for_dx = (pack ? pack_bytes(N, K, dtype) : 0) + partial_bytes(M, K, N, dtype);
+  const int64_t for_dw = (pack ? pack_bytes(M, K, dtype) : 0) + partial_bytes(N, K, M, dtype);
+  return n + std::max(for_dx, for_dw);
+}
+
+int hyena_proj_fwd(const void *x, const void *w, const float *bias, const void *residual, void *y,
+                   void *z, int64_t M, int64_t N, int64_t K, int act, int dtype, void *workspace,
+                   size_t workspace_bytes, cudaStream_t stream) {
+  const int rc = check_shape(M, N, K, dtype);
+  if (rc != HYENA_OK) return rc;
+  if (act < HYENA_ACT_NONE || act > HYENA_ACT_LOGSIGMOID) return HYENA_ERR_INVALID_ARG;
+  if (M == 0) return HYENA_OK;
+  if (!x || !w || !y) return HYENA_ERR_INVALID_ARG;
+  if (misaligned16({x, w, residual, y, z}) || !aligned(bias, 4) || !aligned(workspace, 256))
+    return HYENA_ERR_MISALIGNED;
+  const int64_t need = hyena_proj_workspace_bytes(M, N, K, dtype), es = elem(dtype);
+  if (need > 0 && (!workspace || static_cast<int64_t>(workspace_bytes) < need))
+    return HYENA_ERR_INVALID_ARG;
+  const int64_t nx = M * K * es, nw = N * K * es, ny = M * N * es;
+  const Buf ws{need > 0 ? workspace : nullptr, need};
+  if (clash({{y, ny}, {z, ny}, ws}, {{x, nx}, {w, nw}, {bias, N * 4}}) ||
+      clash({{z, ny}, ws}, {{residual, ny}}) || (residual != y && overlap(residual, ny, y, ny)))
+    return HYENA_ERR_INVALID_ARG;
+  Device d;
+  if (prepare_device(&d) != HYENA_OK) return HYENA_ERR_CUDA;
+  pj::Params p{};
+  p.M = static_cast<int>(M);
+  p.N = static_cast<int>(N);
+  p.bias = bias;
+  p.residual = residual;
+  p.y = y;
+  p.z = z;
+  p.act = act;
+  p.status = d.info.status;
+  uint8_t *at = static_cast<uint8_t *>(workspace);
+  return dtype == HYENA_DTYPE_F32 ? forward<float>(x, w, p, K, dtype, at, d, stream)
+                                  : forward<__nv_bfloat16>(x, w, p, K, dtype, at, d, stream);
+}
+
+int hyena_proj_bwd(const void *x, const void *w, const void *z, const void *dy,
+                   const void *dx_add, void *dx, void *dw, float *db, int64_t M, int64_t N,
+                   int64_t K, int act, int dtype, void *workspace, size_t workspace_bytes,
+                   cudaStream_t stream) {
+  const int rc = check_shape(M, N, K, dtype);
+  if (rc != HYENA_OK) return rc;
+  if (act < HYENA_ACT_NONE || act > HYENA_ACT_LOGSIGMOID) return HYENA_ERR_INVALID_ARG;
+  if (misaligned16({x, w, z, dy, dx_add, dx, dw}) || !aligned(db, 4) || !aligned(workspace, 256))
+    return HYENA_ERR_MISALIGNED;
+  const int64_t es = elem(dtype), nx = M * K * es, nw = N * K * es, ny = M * N * es;
+  if (M == 0) {
+    if ((dw && cudaMemsetAsync(dw, 0, static_cast<size_t>(nw), stream) != cudaSuccess) ||
+        (db && cudaMemsetAsync(db, 0, static_cast<size_t>(N) * 4, stream) != cudaSuccess))
+      return HYENA_ERR_CUDA;
+    return HYENA_OK;
+  }
+  if (!dy || (dx && !w) || (dw && !x) || (act != HYENA_ACT_NONE && !z)) return HYENA_ERR_INVALID_ARG;
+  if (db_blocks(M) > 65535) return HYENA_ERR_UNSUPPORTED;
+  const int64_t need = hyena_proj_bwd_workspace_bytes(M, N, K, act, dtype);
+  if (!workspace || static_cast<int64_t>(workspace_bytes) < need) return HYENA_ERR_INVALID_ARG;
+  if (clash({{dx, nx}, {dw, nw}, {db, N * 4}, {workspace, need}},
+            {{x, nx}, {w, nw}, {z, ny}, {dy, ny}}) ||
+      clash({{dw, nw}, {db, N * 4}, {workspace, need}}, {{dx_add, nx}}) ||
+      (dx_add != dx && overlap(dx_add, nx, dx, nx)))
+    return HYENA_ERR_INVALID_ARG;
+  Device d;
+  if (prepare_device(&d) != HYENA_OK) return HYENA_ERR_CUDA;
+  uint8_t *at = static_cast<uint8_t *>(workspace);
+  return dtype == HYENA_DTYPE_F32
+             ? backward<float>(x, w, z, dy, dx_add, dx, dw, db, M, N, K, act, dtype, at, d, stream)
+             : backward<__nv_bfloat16>(x, w, z, dy, dx_add, dx, dw, db, M, N, K, act, dtype, at, d,
+                                       stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,641 @@
+// proj.cuh -- the matrix products around a sequence mixer, on tcgen05 tensor cores (sm_100a).
+//
+//     C[m][n] = sum_k A[m][k] B[n][k],      y = act(C + bias[n]) + residual[m][n]
+//
+// One kernel serves the projection (A = x, B = w) and its two gradients (dx: A = dz, B = w read
+// along its other axis; dw: both read along the other axis): an operand whose rows run along m or
+// n instead of k is staged as it lies and named so in the instruction descriptor.
+//
+// fp32 operands are split into three bf16 planes a = a0 + a1 + a2 (8 bits of the mantissa each),
+// and C is the sum of the six products of planes i + j <= 2, smallest first; the three left out
+// are below 2^-26 of a b.  They run 6 bf16 products, ~4x the rate that fp32 FMA units would give.
+//
+// Tiles.  kCG = 2: a pair of CTAs works on 256 x 256 outputs with tcgen05.mma.cta_group::2, each
+// holding 128 rows of A, 128 rows of B and 128 rows of the accumulator.  Each byte staged then
+// feeds 128 products, twice what a single CTA's 128 x 128 tile gives; at the tensor cores' rate the
+// pair draws 64 bytes per SM and cycle from L2, which L2 can serve, where 96 or 128 bytes starve
+// it.  kCG = 1: 128 x kBN by one CTA, for problems with too few 256 x 256 tiles.  Where even those
+// are few, k is cut (splits) and fp32 partial products are summed, in order, by a second kernel.
+//
+// Persistent CTAs: warp 0 streams k-blocks of 64 through a ring of shared-memory stages with TMA
+// (128-byte swizzle; zero fill at the ragged edges), warp 1 issues the MMAs into one of two
+// accumulators in tensor memory, warps 2-5 drain the other: through shared memory, so that global
+// rows are read and written in 128-byte pieces.  Bound: the tensor pipe for large products, the
+// bytes of w for a few rows.
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cstdint>
+#include <type_traits>
+
+#include "ptx.cuh"
+
+namespace hyena {
+namespace proj {
+
+constexpr int kBK = 64;                        // k per stage: one 128-byte swizzled row
+constexpr int kRows = 128;                     // rows of A (and of the accumulator) per CTA
+constexpr int kEpiWarps = 4;
+constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kChunk = 64;                     // columns an epilogue warp stages at a time
+constexpr int kStageOut = 32 * kChunk * 4;     // its staging bytes
+constexpr int kMaxStages = 8;
+constexpr unsigned int kTimeout = 1u;          // HYENA_DEVICE_TIMEOUT
+
+enum Act { kNone = 0, kGelu = 1, kSilu = 2, kSigmoid = 3, kLogSigmoid = 4 };
+
+// The six products of bf16 planes, smallest first, as (plane of A, plane of B).
+__device__ constexpr uint8_t kPlaneA[6] = {0, 2, 1, 0, 1, 0};
+__device__ constexpr uint8_t kPlaneB[6] = {2, 0, 1, 1, 0, 0};
+
+template <int kCG, int kBN>
+struct Tile {
+  static constexpr int kM = kRows * kCG;               // of the whole tile
+  static constexpr int kN = kBN;
+  static constexpr int kBRows = kBN / kCG;             // rows of B per CTA
+  static constexpr int kABytes = kRows * kBK * 2, kBBytes = kBRows * kBK * 2;
+  static constexpr int kStage = kABytes + kBBytes;
+  static constexpr int kFixed = kEpiWarps * kStageOut + 1024;
+  static constexpr int kStages =
+      (226 * 1024 - kFixed) / kStage < kMaxStages ? (226 * 1024 - kFixed) / kStage : kMaxStages;
+  static constexpr int kSmem = kStages * kStage + kFixed;
+  static constexpr int kTmemCols = 2 * kBN < 32 ? 32 : 2 * kBN;  // two accumulators
+};
+
+struct Params {
+  int M, N, kb;                 // outputs; k-blocks of one product
+  int pairs;                    // 1 (bf16) or 6 (planes of fp32)
+  int tiles_m, tiles_n, splits, kb_per_split;  // splits cut the pairs * kb blocks
+  int group_m;                  // tiles of m that run together (their w tiles stay in L2)
+  const float *bias;            // [N] or null
+  const void *residual;         // [M, N] or null
+  void *y, *z;                  // [M, N]; z (before the activation) or null
+  float *partial;               // [splits, M, N] when splits > 1
+  int act;
+  int vec;                      // rows of y, z, residual are whole, aligned 16-byte vectors
+  unsigned int *status;
+};
+
+// ------------------------------------------------------------------------------- activations
+// fp32 results take the accurate exp; a bf16 result rounds away what the fast one loses.
+template <typename T> __device__ __forceinline__ float exp_of(float x) { return __expf(x); }
+template <> __device__ __forceinline__ float exp_of<float>(float x) { return expf(x); }
+
+template <typename T, int kAct>
+__device__ __forceinline__ float act_of(float z) {
+  if constexpr (kAct == kGelu) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
+  if constexpr (kAct == kSilu) return z / (1.0f + exp_of<T>(-z));
+  if constexpr (kAct == kSigmoid) return 1.0f / (1.0f + exp_of<T>(-z));
+  if constexpr (kAct == kLogSigmoid) return fminf(z, 0.0f) - log1pf(exp_of<T>(-fabsf(z)));
+  return z;
+}
+
+template <typename T, int kAct>
+__device__ __forceinline__ float act_slope(float z) {
+  if constexpr (kAct == kGelu)
+    return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * 0.39894228f * exp_of<T>(-0.5f * z * z);
+  if constexpr (kAct == kSilu) {
+    const float p = 1.0f / (1.0f + exp_of<T>(-z));
+    return p * (1.0f + z * (1.0f - p));
+  }
+  if constexpr (kAct == kSigmoid) {
+    const float p = 1.0f / (1.0f + exp_of<T>(-z));
+    return p * (1.0f - p);
+  }
+  if constexpr (kAct == kLogSigmoid) return 1.0f / (1.0f + exp_of<T>(z));
+  return 1.0f;
+}
+
+// f(integral constant of the activation), one branch for all the elements that f handles.
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F &&f) {
+  switch (act) {
+    case kGelu: f(std::integral_constant<int, kGelu>()); break;
+    case kSilu: f(std::integral_constant<int, kSilu>()); break;
+    case kSigmoid: f(std::integral_constant<int, kSigmoid>()); break;
+    case kLogSigmoid: f(std::integral_constant<int, kLogSigmoid>()); break;
+    default: f(std::integral_constant<int, kNone>());
+  }
+}
+
+// ------------------------------------------------------------------------------- elements
+template <typename T, int n> struct alignas(sizeof(T) * n) VecOf { T e[n]; };
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ void from_f(float x, __nv_bfloat16 *o) { *o = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void from_f(float x, float *o) { *o = x; }
+
+// Activation, residual and the one rounding of n neighbouring outputs of a row; z is the product
+// with its bias.
+template <typename T, int n>
+__device__ __forceinline__ void finish(const Params &p, const float (&z)[n], int64_t row, int col) {
+  constexpr int V = 16 / static_cast<int>(sizeof(T)) < n ? 16 / static_cast<int>(sizeof(T)) : n;
+  const int64_t at = row * p.N + col;
+  float y[n];
+  with_act(p.act, [&](auto act) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) y[i] = act_of<T, decltype(act)::value>(z[i]);
+  });
+  if (p.vec && col + n <= p.N) {
+#pragma unroll
+    for (int i0 = 0; i0 < n; i0 += V) {
+      VecOf<T, V> r, o;
+      if (p.residual) {
+        r = *reinterpret_cast<const VecOf<T, V> *>(static_cast<const T *>(p.residual) + at + i0);
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[i0 + i] += to_f(r.e[i]);
+      }
+      if (p.z) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) from_f(z[i0 + i], &o.e[i]);
+        *reinterpret_cast<VecOf<T, V> *>(static_cast<T *>(p.z) + at + i0) = o;
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) from_f(y[i0 + i], &o.e[i]);
+      *reinterpret_cast<VecOf<T, V> *>(static_cast<T *>(p.y) + at + i0) = o;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      if (col + i >= p.N) break;
+      if (p.residual) y[i] += to_f(static_cast<const T *>(p.residual)[at + i]);
+      if (p.z) from_f(z[i], static_cast<T *>(p.z) + at + i);
+      from_f(y[i], static_cast<T *>(p.y) + at + i);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------- pairs of CTAs
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+// The address of this CTA's shared variable in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_cta(const void *p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+template <int kCG>
+__device__ __forceinline__ void load_tile(uint8_t *dst, const CUtensorMap *map, uint32_t bar, int x,
+                                          int y, int plane) {
+  if constexpr (kCG == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile"
+        ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(plane)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile"
+        ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(plane)
+        : "memory");
+}
+template <int kCG>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                    uint32_t accumulate) {
+  if constexpr (kCG == 2)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b),
+        "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    umma_f16(d, a, b, idesc, accumulate);
+}
+// Arrives on `bar` (of every CTA of the group) when the MMAs issued so far are done.
+template <int kCG>
+__device__ __forceinline__ void commit(uint64_t *bar) {
+  if constexpr (kCG == 2)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    umma_commit(bar);
+}
+template <int kCG>
+__device__ __forceinline__ void tmem_get(uint32_t *dst, uint32_t cols) {
+  if constexpr (kCG == 2)
+    asm volatile(
+        "tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n\t"
+        "tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::"r"(smem_u32(dst)),
+        "r"(cols)
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n\t"
+        "tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::"r"(smem_u32(dst)),
+        "r"(cols)
+        : "memory");
+}
+template <int kCG>
+__device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
+  if constexpr (kCG == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols)
+                 : "memory");
+  else
+    tmem_dealloc(base, cols);
+}
+
+// Instruction descriptor: bf16 operands, fp32 accumulator, major-ness of each (1: rows along m/n).
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_mn) {
+  return umma_idesc_f16_f32_mn(M, N, a_mn, b_mn) | (1u << 7) | (1u << 10);
+}
+
+// ------------------------------------------------------------------------------- work
+struct Work {
+  int m, n, split, kb0, kb1;  // tile coordinates; blocks [kb0, kb1) of the pairs * kb
+};
+__device__ __forceinline__ Work work_at(const Params &p, int w) {
+  Work k;
+  const int tiles = p.tiles_m * p.tiles_n, t = w % tiles;
+  k.split = w / tiles;
+  const int per = p.group_m * p.tiles_n, g = t / per, r = t % per;
+  const int gm = min(p.group_m, p.tiles_m - g * p.group_m);
+  k.m = g * p.group_m + r % gm;
+  k.n = r / gm;
+  const int total = p.pairs * p.kb;
+  k.kb0 = k.split * p.kb_per_split;
+  k.kb1 = min(k.kb0 + p.kb_per_split, total);
+  return k;
+}
+
+// ------------------------------------------------------------------------------- the product
+// kAMn / kBMn: the operand's rows run along m / n (its tensor map is [k][m]), else along k.
+template <typename T, int kCG, int kBN, bool kAMn, bool kBMn>
+__global__ void __launch_bounds__(kThreads, 1)
+    proj_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
+                const Params p) {
+  using L = Tile<kCG, kBN>;
+  extern __shared__ uint8_t dynamic[];
+  __shared__ uint64_t full[L::kStages], empty[L::kStages], acc_full[2], acc_empty[2];
+  __shared__ uint32_t tmem_at;
+  __shared__ int abort;
+  uint8_t *stages = dynamic + (1024 - smem_u32(dynamic) % 1024) % 1024;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t rank = kCG == 2 ? cluster_rank() : 0;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], kEpiWarps * kCG);
+    }
+    abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_get<kCG>(&tmem_at, L::kTmemCols);
+  tc_fence_before_sync();
+  __syncthreads();
+  if (kCG == 2) cluster_sync();
+  tc_fence_after_sync();
+  const uint32_t tmem = tmem_at;
+  const int works = p.tiles_m * p.tiles_n * p.splits;
+  const int first = blockIdx.x / kCG, step = gridDim.x / kCG;
+  griddep_launch_dependents();
+  griddep_wait();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------------------- TMA
+      int it = 0;
+      bool ok = true;
+      for (int w = first; w < works && ok; w += step) {
+        const Work k = work_at(p, w);
+        const int m0 = k.m * L::kM + static_cast<int>(rank) * kRows;
+        const int n0 = k.n * L::kN + static_cast<int>(rank) * L::kBRows;
+        for (int kb = k.kb0; kb < k.kb1; ++kb, ++it) {
+          const int st = it % L::kStages, round = it / L::kStages;
+          if (round > 0 && !mbar_wait(&empty[st], (round - 1) & 1, &abort, p.status, kTimeout)) {
+            ok = false;
+            break;
+          }
+          const int pair = kb / p.kb, k0 = (kb - pair * p.kb) * kBK;
+          const int pa = p.pairs > 1 ? kPlaneA[pair] : 0, pb = p.pairs > 1 ? kPlaneB[pair] : 0;
+          uint8_t *a = stages + st * L::kStage, *b = a + L::kABytes;
+          if (rank == 0) mbar_arrive_expect_tx(&full[st], kCG * L::kStage);
+          const uint32_t bar = kCG == 2 ? in_cta(&full[st], 0) : smem_u32(&full[st]);
+          if (kAMn) {
+            for (int h = 0; h < kRows / 64; ++h)
+              load_tile<kCG>(a + h * 8192, &ma, bar, m0 + h * 64, k0, pa);
+          } else {
+            load_tile<kCG>(a, &ma, bar, k0, m0, pa);
+          }
+          if (kBMn) {
+            for (int h = 0; h < L::kBRows / 64; ++h)
+              load_tile<kCG>(b + h * 8192, &mb, bar, n0 + h * 64, k0, pb);
+          } else {
+            load_tile<kCG>(b, &mb, bar, k0, n0, pb);
+          }
+        }
+      }
+      // Before the CTA ends every copy has landed and every release of a stage has arrived.  In
+      // the leader `full` covers both CTAs' copies.
+      for (int j = it > L::kStages ? it - L::kStages : 0; j < it; ++j) {
+        const int st = j % L::kStages, parity = (j / L::kStages) & 1;
+        int no_abort = 0;
+        if (!mbar_wait(&empty[st], parity, &abort, p.status, kTimeout) && rank == 0)
+          mbar_wait(&full[st], parity, &no_abort, p.status, kTimeout);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // ------------------------------------------------------------------------- MMA
+      constexpr uint32_t id = idesc_bf16(L::kM, L::kN, kAMn, kBMn);
+      constexpr uint32_t kStepA = (kAMn ? 16 * 128 : 32) >> 4, kStepB = (kBMn ? 16 * 128 : 32) >> 4;
+      int it = 0, n = 0;
+      bool ok = true;
+      for (int w = first; w < works && ok; w += step, ++n) {
+        const Work k = work_at(p, w);
+        const int acc = n & 1;
+        if (n >= 2 && !mbar_wait(&acc_empty[acc], (n / 2 - 1) & 1, &abort, p.status, kTimeout)) break;
+        tc_fence_after_sync();
+        const uint32_t d = tmem + acc * kBN;
+        for (int kb = k.kb0; kb < k.kb1; ++kb, ++it) {
+          const int st = it % L::kStages;
+          if (!mbar_wait(&full[st], (it / L::kStages) & 1, &abort, p.status, kTimeout)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t a = smem_u32(stages + st * L::kStage), b = a + L::kABytes;
+          const uint64_t da = umma_smem_desc(a, kAMn ? 8192 : 16, 1024, 2);
+          const uint64_t db = umma_smem_desc(b, kBMn ? 8192 : 16, 1024, 2);
+#pragma unroll
+          for (int s = 0; s < kBK / 16; ++s)
+            mma<kCG>(d, da + s * kStepA, db + s * kStepB, id, kb > k.kb0 || s > 0);
+          commit<kCG>(&empty[st]);
+        }
+        if (ok) commit<kCG>(&acc_full[acc]);
+      }
+      // MMAs still reading shared memory when a wait gave up: let them finish
+      if (!ok || abort) {
+        int no_abort = 0;
+        for (int j = it > L::kStages ? it - L::kStages : 0; j < it; ++j)
+          mbar_wait(&empty[j % L::kStages], (j / L::kStages) & 1, &no_abort, p.status, kTimeout);
+      }
+    }
+  } else {
+    // --------------------------------------------------------------------------- epilogue
+    const int quad = warp % 4;  // the 32 lanes of tensor memory that this warp may read
+    float *out = reinterpret_cast<float *>(stages + L::kStages * L::kStage + (warp - 2) * kStageOut);
+    int n = 0;
+    for (int w = first; w < works; w += step, ++n) {
+      const Work k = work_at(p, w);
+      const int acc = n & 1;
+      const bool ok = mbar_wait(&acc_full[acc], (n / 2) & 1, &abort, p.status, kTimeout);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after_sync();
+      const int row0 = k.m * L::kM + static_cast<int>(rank) * kRows + quad * 32;
+#pragma unroll 1
+      for (int c0 = 0; c0 < kBN; c0 += kChunk) {
+        const uint32_t at = tmem + acc * kBN + c0 + (static_cast<uint32_t>(quad * 32) << 16);
+        uint32_t r0[32], r1[32];
+        tmem_ld_32x32b_x32(at, r0);
+        tmem_ld_32x32b_x32(at + 32, r1);
+        tmem_wait_ld();
+        reg_fence(r0);
+        reg_fence(r1);
+        if (c0 + kChunk >= kBN) {  // the accumulator is in registers: the next tile may start
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) {
+            if (kCG == 2)
+              arrive_at(in_cta(&acc_empty[acc], 0));
+            else
+              mbar_arrive(&acc_empty[acc]);
+          }
+        }
+        // row `lane`, in 16-byte pieces at positions swizzled by the row
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          *reinterpret_cast<uint4 *>(out + lane * kChunk + ((j ^ (lane & 7)) * 4)) =
+              make_uint4(r0[4 * j], r0[4 * j + 1], r0[4 * j + 2], r0[4 * j + 3]);
+          *reinterpret_cast<uint4 *>(out + lane * kChunk + 32 + ((j ^ (lane & 7)) * 4)) =
+              make_uint4(r1[4 * j], r1[4 * j + 1], r1[4 * j + 2], r1[4 * j + 3]);
+        }
+        __syncwarp();
+        const int col = k.n * L::kN + c0 + (lane % 8) * 8;
+        float bias[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          bias[e] = p.bias && p.splits == 1 && col + e < p.N ? p.bias[col + e] : 0.0f;
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) {  // four rows at a time, eight lanes of eight columns each
+          const int r = i * 4 + lane / 8;
+          const int j = 2 * (lane % 8);
+          const float *src = out + r * kChunk + (j & 8) * 4;
+          const float4 u = *reinterpret_cast<const float4 *>(src + (((j & 7) ^ (r & 7)) * 4));
+          const float4 v = *reinterpret_cast<const float4 *>(src + ((((j & 7) + 1) ^ (r & 7)) * 4));
+          float c[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+          const int64_t row = row0 + r;
+          if (row >= p.M || col >= p.N) continue;
+          if (p.splits > 1) {
+            float *to = p.partial + (static_cast<int64_t>(k.split) * p.M + row) * p.N + col;
+            if (p.N % 4 == 0 && col + 8 <= p.N) {
+              *reinterpret_cast<float4 *>(to) = u;
+              *reinterpret_cast<float4 *>(to + 4) = v;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (col + e < p.N) to[e] = c[e];
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) c[e] += bias[e];
+            finish<T, 8>(p, c, row, col);
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+  // Both CTAs' MMAs read each other's shared memory and signal each other's barriers.
+  tc_fence_before_sync();
+  __syncthreads();
+  if (kCG == 2) cluster_sync();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after_sync();
+    tmem_free<kCG>(tmem, L::kTmemCols);
+  }
+}
+
+// The sum of a product's k cuts, in order, and its epilogue: four columns per thread.
+template <typename T>
+__global__ void __launch_bounds__(256) proj_join_kernel(const Params p) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int per_row = (p.N + 3) / 4;
+  const int64_t n = static_cast<int64_t>(p.M) * per_row;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) {
+    const int64_t row = i / per_row;
+    const int col = static_cast<int>(i - row * per_row) * 4;
+    float c[4] = {0.f, 0.f, 0.f, 0.f};
+    const float *from = p.partial + row * p.N + col;
+    for (int s = 0; s < p.splits; ++s, from += static_cast<int64_t>(p.M) * p.N) {
+      if (p.N % 4 == 0) {
+        const float4 v = *reinterpret_cast<const float4 *>(from);
+        c[0] += v.x;
+        c[1] += v.y;
+        c[2] += v.z;
+        c[3] += v.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (col + e < p.N) c[e] += from[e];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] += p.bias && col + e < p.N ? p.bias[col + e] : 0.0f;
+    finish<T, 4>(p, c, row, col);
+  }
+}
+
+// ------------------------------------------------------------------------------- operands
+// x as a sum of bf16 planes, each the nearest to what the ones before leave (the first towards
+// zero where the nearest would overflow); values that are not finite stay in the first.
+template <int kPlanes>
+__device__ __forceinline__ void planes_of(float x, __nv_bfloat16 (&o)[kPlanes]) {
+#pragma unroll
+  for (int i = 0; i < kPlanes; ++i) {
+    o[i] = __float2bfloat16_rn(x);
+    if (i == 0 && isinf(__bfloat162float(o[0])) && !isinf(x)) o[0] = __float2bfloat16_rz(x);
+    const float rest = x - __bfloat162float(o[i]);
+    x = isfinite(x) ? rest : 0.0f;
+  }
+}
+
+// Rows of `cols` elements as rows of `ld` bf16 (a multiple of 8, zero past cols): one plane for
+// bf16, three for fp32.  Eight elements of a row per thread.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    proj_pack_kernel(const T *src, __nv_bfloat16 *dst, int64_t rows, int cols, int ld) {
+  constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int per_row = ld / 8;
+  const int64_t n = rows * per_row, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) {
+    const int64_t row = i / per_row;
+    const int col = static_cast<int>(i - row * per_row) * 8;
+    VecOf<__nv_bfloat16, 8> o[kPlanes];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      __nv_bfloat16 pl[kPlanes];
+      planes_of<kPlanes>(col + e < cols ? to_f(src[row * cols + col + e]) : 0.0f, pl);
+#pragma unroll
+      for (int q = 0; q < kPlanes; ++q) o[q].e[e] = pl[q];
+    }
+#pragma unroll
+    for (int q = 0; q < kPlanes; ++q)
+      *reinterpret_cast<VecOf<__nv_bfloat16, 8> *>(dst + (q * rows + row) * ld + col) = o[q];
+  }
+}
+
+// dz = dy act'(z) as a product's operand (planes and row length as above; null where dy itself
+// serves) and its column sums over kDbRows rows, part[row block][N].  A CTA takes 64 columns:
+// 8 threads of 8 columns x 32 rows at a time.
+constexpr int kDbRows = 128, kDbCols = 64;
+template <typename T, int kAct>
+__global__ void __launch_bounds__(256)
+    proj_dz_kernel(const T *dy, const T *z, __nv_bfloat16 *dz, float *part, int64_t M, int N,
+                   int ld, int vec) {
+  constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1, V = 16 / static_cast<int>(sizeof(T));
+  __shared__ float sums[32][kDbCols + 1];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int c8 = threadIdx.x % 8, rr = threadIdx.x / 8;
+  const int col = blockIdx.x * kDbCols + c8 * 8;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.y) * kDbRows;
+  float sum[8] = {};
+  for (int r = rr; r < kDbRows; r += 32) {
+    const int64_t row = row0 + r;
+    if (row >= M || col >= ld) break;
+    float d[8];
+    const int64_t at = row * N + col;
+    if (vec && col + 8 <= N) {
+#pragma unroll
+      for (int i0 = 0; i0 < 8; i0 += V) {
+        const VecOf<T, V> g = *reinterpret_cast<const VecOf<T, V> *>(dy + at + i0);
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i0 + i] = to_f(g.e[i]);
+        if constexpr (kAct != kNone) {
+          const VecOf<T, V> zv = *reinterpret_cast<const VecOf<T, V> *>(z + at + i0);
+#pragma unroll
+          for (int i = 0; i < V; ++i) d[i0 + i] *= act_slope<T, kAct>(to_f(zv.e[i]));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        d[i] = col + i < N ? to_f(dy[at + i]) : 0.0f;
+        if (kAct != kNone && col + i < N) d[i] *= act_slope<T, kAct>(to_f(z[at + i]));
+      }
+    }
+    if (dz) {
+      VecOf<__nv_bfloat16, 8> o[kPlanes];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        __nv_bfloat16 pl[kPlanes];
+        planes_of<kPlanes>(d[e], pl);
+#pragma unroll
+        for (int q = 0; q < kPlanes; ++q) o[q].e[e] = pl[q];
+      }
+#pragma unroll
+      for (int q = 0; q < kPlanes; ++q)
+        *reinterpret_cast<VecOf<__nv_bfloat16, 8> *>(dz + (q * M + row) * ld + col) = o[q];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] += d[e];
+  }
+  if (!part) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sums[rr][c8 * 8 + e] = sum[e];
+  __syncthreads();
+  if (threadIdx.x < kDbCols && blockIdx.x * kDbCols + threadIdx.x < N) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s += sums[i][threadIdx.x];
+    part[static_cast<int64_t>(blockIdx.y) * N + blockIdx.x * kDbCols + threadIdx.x] = s;
+  }
+}
+
+// db[n]: the sum of the row blocks' sums, in order within each of 8 threads, then over them.
+__global__ void __launch_bounds__(256)
+    proj_db_kernel(const float *part, float *db, int blocks, int N) {
+  __shared__ float sums[8][33];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int c = threadIdx.x % 32, r = threadIdx.x / 32, col = blockIdx.x * 32 + c;
+  float s = 0.0f;
+  if (col < N)
+    for (int b = r; b < blocks; b += 8) s += part[static_cast<int64_t>(b) * N + col];
+  sums[r][c] = s;
+  __syncthreads();
+  if (r == 0 && col < N) {
+    float t = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t += sums[i][c];
+    db[col] = t;
+  }
+}
+
+}  // namespace proj
+}  // namespace hyena

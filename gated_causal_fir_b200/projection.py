@@ -1,0 +1,108 @@
+"""The projections around a sequence mixer (C: ``hyena_proj_*`` of ``include/hyena_mixer.h``).
+
+    y = act(x w^T + bias) + residual        act: none, gelu, silu, sigmoid, logsigmoid
+
+x: CUDA [..., K], w: [N, K], all bf16 or all fp32; bias fp32 [N].  The functions marshal torch
+CUDA tensors into pointers, sizes and a stream; outputs and workspaces that are not given come
+from torch.
+"""
+from . import _native
+from ._args import On, code as code_of, nbytes, need, ptr, torch_, workspace as workspace_of
+from ._native import ACT_CODES, HYENA_DTYPE_BF16
+
+
+def _act(act):
+    if act not in ACT_CODES:
+        raise ValueError("act must be one of %s, got %r" % (", ".join(ACT_CODES), act))
+    return ACT_CODES[act]
+
+
+def _rows(x, w):
+    """(type code, M, N, K) of x [..., K] and w [N, K]."""
+    torch = torch_()
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() < 2:
+        raise TypeError("x must be a CUDA [..., K] tensor of at least two dimensions")
+    code = code_of(x, "x")
+    K = x.shape[-1]
+    need("x", x, x.shape, x.dtype, x.device)
+    if not isinstance(w, torch.Tensor) or w.dim() != 2 or w.shape[1] != K:
+        raise ValueError("w must be a [N, %d] tensor" % K)
+    need("w", w, w.shape, x.dtype, x.device)
+    N = w.shape[0]
+    if N < 1 or K < 1:
+        raise ValueError("w must not be empty")
+    return code, x.numel() // K, N, K
+
+
+def hyena_proj_workspace_bytes(M, N, K, dtype=HYENA_DTYPE_BF16):
+    """Host-only: device workspace bytes hyena_proj_fwd needs for this shape."""
+    return nbytes("hyena_proj_workspace_bytes", M, N, K, dtype)
+
+
+def hyena_proj_bwd_workspace_bytes(M, N, K, act="none", dtype=HYENA_DTYPE_BF16):
+    """Host-only: device workspace bytes hyena_proj_bwd needs for this shape."""
+    return nbytes("hyena_proj_bwd_workspace_bytes", M, N, K, _act(act), dtype)
+
+
+def hyena_proj_fwd(x, w, bias=None, act="none", residual=None, y=None, z=None, workspace=None,
+                   stream=None):
+    """y = act(x w^T + bias) + residual, [..., N]; returns y.
+
+    z: optional [..., N] tensor of x's type that receives the value before the activation, for
+    hyena_proj_bwd.  y may be ``residual`` itself.  Runs asynchronously on ``stream`` (default:
+    the current stream of x's device).
+    """
+    torch = torch_()
+    code, M, N, K = _rows(x, w)
+    shape = tuple(x.shape[:-1]) + (N,)
+    if bias is not None:
+        need("bias", bias, (N,), torch.float32, x.device)
+    for name, t in (("residual", residual), ("y", y), ("z", z)):
+        if t is not None:
+            need(name, t, shape, x.dtype, x.device)
+    with On(x.device, stream) as on:
+        if y is None:
+            y = torch.empty(shape, dtype=x.dtype, device=x.device)
+            on.keep(y)
+        size = nbytes("hyena_proj_workspace_bytes", M, N, K, code)
+        ws, nws = workspace_of(workspace, size, x.device, on)
+        _native.check("hyena_proj_fwd", _native.lib().hyena_proj_fwd(
+            x.data_ptr(), w.data_ptr(), ptr(bias), ptr(residual), y.data_ptr(), ptr(z), M, N, K,
+            _act(act), code, ws, nws, on.stream.cuda_stream))
+    return y
+
+
+def hyena_proj_bwd(x, w, dy, z=None, act="none", dx_add=None, grads=None, workspace=None,
+                   stream=None):
+    """Gradients (dx, dw, db) of hyena_proj_fwd for dy [..., N]; the residual's is dy itself.
+
+    z: as the forward left it (not needed for act "none").  dx_add: [..., K], added to dx (the
+    residual branch, or another projection of x).  grads: optional (dx, dw, db) to fill; an entry
+    None is not computed.  dx may be ``dx_add`` itself.
+    """
+    torch = torch_()
+    code, M, N, K = _rows(x, w)
+    need("dy", dy, tuple(x.shape[:-1]) + (N,), x.dtype, x.device)
+    if z is not None:
+        need("z", z, dy.shape, x.dtype, x.device)
+    elif act != "none":
+        raise ValueError("z, the value before the activation, is needed for act %r" % (act,))
+    if dx_add is not None:
+        need("dx_add", dx_add, x.shape, x.dtype, x.device)
+    made = ()
+    if grads is None:
+        grads = made = (torch.empty_like(x), torch.empty_like(w),
+                        torch.empty((N,), dtype=torch.float32, device=x.device))
+    dx, dw, db = grads
+    for name, t, like, dt in (("dx", dx, x.shape, x.dtype), ("dw", dw, w.shape, x.dtype),
+                              ("db", db, (N,), torch.float32)):
+        if t is not None:
+            need(name, t, like, dt, x.device)
+    with On(x.device, stream) as on:
+        on.keep(*made)
+        size = nbytes("hyena_proj_bwd_workspace_bytes", M, N, K, _act(act), code)
+        ws, nws = workspace_of(workspace, size, x.device, on)
+        _native.check("hyena_proj_bwd", _native.lib().hyena_proj_bwd(
+            x.data_ptr(), w.data_ptr(), ptr(z), dy.data_ptr(), ptr(dx_add), ptr(dx), ptr(dw),
+            ptr(db), M, N, K, _act(act), code, ws, nws, on.stream.cuda_stream))
+    return dx, dw, db

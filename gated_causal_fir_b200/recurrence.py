@@ -8,133 +8,52 @@ CUDA tensors into pointers, sizes and a stream; outputs and workspaces that are 
 from torch.
 """
 from . import _native
-from ._native import HYENA_DTYPE_BF16, HYENA_DTYPE_F32
-
-
-def _torch():
-    import torch
-    return torch
-
-
-def _code(t, what):
-    torch = _torch()
-    if t.dtype == torch.bfloat16:
-        return HYENA_DTYPE_BF16
-    if t.dtype == torch.float32:
-        return HYENA_DTYPE_F32
-    raise TypeError("%s must be bfloat16 or float32, got %s" % (what, t.dtype))
-
-
-def _need(name, t, shape, dtype, device):
-    """``t`` must be a contiguous CUDA tensor of this shape and type on this device."""
-    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
-        raise TypeError("%s must be a CUDA tensor" % name)
-    if t.dtype != dtype:
-        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.device != device:
-        raise ValueError("%s is on %s, the first input on %s" % (name, t.device, device))
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-class _On:
-    """The launch context of a call: the tensors' device made current, and the stream (by default
-    that device's current one).  ``keep`` marks buffers made here as in use on a given stream."""
-
-    def __init__(self, device, stream):
-        cuda = _torch().cuda
-        self._given = stream
-        self.stream = cuda.current_stream(device) if stream is None else stream
-        same = device.index == cuda.current_device()
-        self._guard = None if same else cuda.device(device)
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
-
-    def keep(self, *tensors):
-        if self._given is not None:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self._given)
-
-
-def _workspace(given, need, device, on):
-    """(pointer, bytes) of the workspace: the caller's, or one made here; (None, 0) for none."""
-    torch = _torch()
-    if given is not None:
-        if not isinstance(given, torch.Tensor) or not given.is_cuda or given.device != device \
-                or not given.is_contiguous():
-            raise ValueError("workspace must be a contiguous CUDA tensor on the inputs' device")
-        return given.data_ptr(), given.numel() * given.element_size()
-    if need == 0:
-        return None, 0
-    ws = torch.empty(need, dtype=torch.uint8, device=device)
-    on.keep(ws)
-    return ws.data_ptr(), need
+from ._args import On, code as code_of, nbytes, need, ptr, torch_, workspace as workspace_of
+from ._native import HYENA_DTYPE_BF16
 
 
 def _shapes(q, k, v, g, d_g, dims):
-    torch = _torch()
+    torch = torch_()
     if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != len(dims):
         raise TypeError("q must be a CUDA [%s] tensor" % ", ".join(dims))
-    code = _code(q, "q")
+    code = code_of(q, "q")
     D = q.shape[-1]
     if not isinstance(d_g, int) or d_g < 1 or D < 1 or D % d_g != 0:
         raise ValueError("d_g = %s must divide D = %d" % (d_g, D))
     for name, t in (("q", q), ("k", k), ("v", v)):
-        _need(name, t, q.shape, q.dtype, q.device)
-    _need("g", g, tuple(q.shape[:-1]) + (D // d_g,), q.dtype, q.device)
+        need(name, t, q.shape, q.dtype, q.device)
+    need("g", g, tuple(q.shape[:-1]) + (D // d_g,), q.dtype, q.device)
     return code
 
 
 def _state(name, t, q):
-    torch = _torch()
-    return None if t is None else _need(name, t, (q.shape[0], q.shape[-1]), torch.float32,
+    torch = torch_()
+    return None if t is None else need(name, t, (q.shape[0], q.shape[-1]), torch.float32,
                                         q.device)
-
-
-def _bytes(fn, *args):
-    n = int(getattr(_native.lib(), fn)(*args))
-    if n < 0:
-        raise _native.HyenaError(fn, -n)
-    return n
 
 
 def hyena_scan_workspace_bytes(B, L, D, d_g, dtype=HYENA_DTYPE_BF16):
     """Host-only: device workspace bytes hyena_scan_fwd needs for this shape."""
-    return _bytes("hyena_scan_workspace_bytes", B, L, D, d_g, dtype)
+    return nbytes("hyena_scan_workspace_bytes", B, L, D, d_g, dtype)
 
 
 def hyena_scan_bwd_workspace_bytes(B, L, D, d_g, dtype=HYENA_DTYPE_BF16, have_ckpt=True):
     """Host-only: device workspace bytes hyena_scan_bwd needs for this shape."""
-    return _bytes("hyena_scan_bwd_workspace_bytes", B, L, D, d_g, dtype, 1 if have_ckpt else 0)
+    return nbytes("hyena_scan_bwd_workspace_bytes", B, L, D, d_g, dtype, 1 if have_ckpt else 0)
 
 
 def hyena_scan_ckpt(q):
     """An uninitialised checkpoint tensor for sequences like q [B, L, D]: fp32 [B, tiles, D]."""
-    torch = _torch()
-    tiles = _bytes("hyena_scan_ckpt_tiles", q.shape[1], _code(q, "q"))
+    torch = torch_()
+    tiles = nbytes("hyena_scan_ckpt_tiles", q.shape[1], code_of(q, "q"))
     return torch.empty((q.shape[0], tiles, q.shape[2]), dtype=torch.float32, device=q.device)
 
 
 def _ckpt(t, q, code):
     if t is None:
         return None
-    tiles = _bytes("hyena_scan_ckpt_tiles", q.shape[1], code)
-    return _need("ckpt", t, (q.shape[0], tiles, q.shape[2]), _torch().float32, q.device)
+    tiles = nbytes("hyena_scan_ckpt_tiles", q.shape[1], code)
+    return need("ckpt", t, (q.shape[0], tiles, q.shape[2]), torch_().float32, q.device)
 
 
 def hyena_scan_fwd(q, k, v, g, d_g, s0=None, y=None, s_out=None, ckpt=None, workspace=None,
@@ -147,7 +66,7 @@ def hyena_scan_fwd(q, k, v, g, d_g, s0=None, y=None, s_out=None, ckpt=None, work
     tensor of hyena_scan_ckpt(q), filled for hyena_scan_bwd.  Runs asynchronously on ``stream``
     (default: the current stream of q's device).
     """
-    torch = _torch()
+    torch = torch_()
     code = _shapes(q, k, v, g, d_g, ("B", "L", "D"))
     B, L, D = q.shape
     _state("s0", s0, q)
@@ -157,19 +76,19 @@ def hyena_scan_fwd(q, k, v, g, d_g, s0=None, y=None, s_out=None, ckpt=None, work
         y = torch.empty_like(q)
         made.append(y)
     else:
-        _need("y", y, q.shape, q.dtype, q.device)
+        need("y", y, q.shape, q.dtype, q.device)
     if s_out is None:
         s_out = torch.empty((B, D), dtype=torch.float32, device=q.device)
         made.append(s_out)
     else:
         _state("s_out", s_out, q)
-    with _On(q.device, stream) as on:
+    with On(q.device, stream) as on:
         on.keep(*made)
-        need = _bytes("hyena_scan_workspace_bytes", B, L, D, d_g, code)
-        ws, nws = _workspace(workspace, need, q.device, on)
+        size = nbytes("hyena_scan_workspace_bytes", B, L, D, d_g, code)
+        ws, nws = workspace_of(workspace, size, q.device, on)
         _native.check("hyena_scan_fwd", _native.lib().hyena_scan_fwd(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _ptr(s0), y.data_ptr(),
-            s_out.data_ptr(), _ptr(ckpt), B, L, D, d_g, code, ws, nws, on.stream.cuda_stream))
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), ptr(s0), y.data_ptr(),
+            s_out.data_ptr(), ptr(ckpt), B, L, D, d_g, code, ws, nws, on.stream.cuda_stream))
     return y, s_out
 
 
@@ -181,10 +100,10 @@ def hyena_scan_bwd(q, k, v, g, dy, d_g, s0=None, ds_out=None, ckpt=None, grads=N
     ckpt: as hyena_scan_fwd filled it for the same inputs; without it a pass over k, v and g
     finds the states again.  grads: optional preallocated (dq, dk, dv, dg, ds0), overwritten.
     """
-    torch = _torch()
+    torch = torch_()
     code = _shapes(q, k, v, g, d_g, ("B", "L", "D"))
     B, L, D = q.shape
-    _need("dy", dy, q.shape, q.dtype, q.device)
+    need("dy", dy, q.shape, q.dtype, q.device)
     _state("s0", s0, q)
     _state("ds_out", ds_out, q)
     _ckpt(ckpt, q, code)
@@ -196,18 +115,18 @@ def hyena_scan_bwd(q, k, v, g, dy, d_g, s0=None, ds_out=None, ckpt=None, grads=N
     dq, dk, dv, dg, ds0 = grads
     if not made:
         for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
-            _need(name, t, q.shape, q.dtype, q.device)
-        _need("dg", dg, g.shape, g.dtype, q.device)
+            need(name, t, q.shape, q.dtype, q.device)
+        need("dg", dg, g.shape, g.dtype, q.device)
         if ds0 is None:
             raise ValueError("ds0 must be an fp32 [B, D] tensor")
         _state("ds0", ds0, q)
-    with _On(q.device, stream) as on:
+    with On(q.device, stream) as on:
         on.keep(*made)
-        need = _bytes("hyena_scan_bwd_workspace_bytes", B, L, D, d_g, code, int(ckpt is not None))
-        ws, nws = _workspace(workspace, need, q.device, on)
+        size = nbytes("hyena_scan_bwd_workspace_bytes", B, L, D, d_g, code, int(ckpt is not None))
+        ws, nws = workspace_of(workspace, size, q.device, on)
         _native.check("hyena_scan_bwd", _native.lib().hyena_scan_bwd(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), _ptr(s0), dy.data_ptr(),
-            _ptr(ds_out), _ptr(ckpt), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(),
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), ptr(s0), dy.data_ptr(),
+            ptr(ds_out), ptr(ckpt), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(),
             ds0.data_ptr(), B, L, D, d_g, code, ws, nws, on.stream.cuda_stream))
     return dq, dk, dv, dg, ds0
 
@@ -217,7 +136,7 @@ def hyena_scan_step(q, k, v, g, state, d_g, y=None, state_out=None, stream=None)
 
     q, k, v: CUDA [B, D]; g: [B, D // d_g]; state: fp32 [B, D].  state_out None advances
     ``state`` in place."""
-    torch = _torch()
+    torch = torch_()
     code = _shapes(q, k, v, g, d_g, ("B", "D"))
     B, D = q.shape
     if state is None:
@@ -227,12 +146,12 @@ def hyena_scan_step(q, k, v, g, state, d_g, y=None, state_out=None, stream=None)
         state_out = state
     else:
         _state("state_out", state_out, q)
-    with _On(q.device, stream) as on:
+    with On(q.device, stream) as on:
         if y is None:
             y = torch.empty_like(q)
             on.keep(y)
         else:
-            _need("y", y, q.shape, q.dtype, q.device)
+            need("y", y, q.shape, q.dtype, q.device)
         _native.check("hyena_scan_step", _native.lib().hyena_scan_step(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), state.data_ptr(),
             y.data_ptr(), state_out.data_ptr(), B, D, d_g, code, on.stream.cuda_stream))

@@ -1,6 +1,6 @@
 /*
  * hyena_mixer.h -- C ABI of the operators beside the gated FIR of hyena_conv.h in a mixer layer:
- * the gated linear recurrence (hyena_scan_*).
+ * the gated linear recurrence (hyena_scan_*) and the projections (hyena_proj_*).
  *
  * Status codes, element types and the conventions on streams and buffers are those of
  * hyena_conv.h: DEVICE pointers, row-major contiguous tensors, buffers owned by the caller, no
@@ -81,6 +81,58 @@ int64_t hyena_scan_bwd_workspace_bytes(int64_t B, int64_t L, int64_t D, int d_g,
 int hyena_scan_step(const void *q, const void *k, const void *v, const void *g, const float *s,
                     void *y, float *s_out, int64_t B, int64_t D, int d_g, int dtype,
                     cudaStream_t stream);
+
+enum hyena_act {
+    HYENA_ACT_NONE = 0,
+    HYENA_ACT_GELU = 1,          /* z Phi(z), the exact form (erf) */
+    HYENA_ACT_SILU = 2,          /* z sigmoid(z) */
+    HYENA_ACT_SIGMOID = 3,
+    HYENA_ACT_LOGSIGMOID = 4     /* log sigmoid(z): a log decay for hyena_scan_* */
+};
+
+/*
+ * Projection: a matrix product with bias, activation and residual in its epilogue.
+ *
+ *     z[m][n] = sum_k x[m][k] w[n][k] + bias[n],     y = act(z) + residual
+ *
+ * x: [M, K], w: [N, K], residual, y, z: [M, N], all of `dtype`, 16-byte aligned.  bias: fp32 [N].
+ * bias, residual and z may be NULL; z, where given, receives the value before the activation,
+ * which hyena_proj_bwd wants (rounded to `dtype`).  y may be residual itself.
+ * Any M >= 0, N, K >= 1.  The products run on tensor cores with fp32 accumulation: bf16 operands
+ * as they are (rows that are no multiple of 8 elements are copied into the workspace first); fp32
+ * operands as three bf16 planes each and six products, which keeps fp32's precision (relative to
+ * sum |x| |w|) for finite values; a product with an infinite operand may give NaN in its place.
+ * Bias, activation and residual are fp32, y is rounded once.  Deterministic.
+ * workspace: at least hyena_proj_workspace_bytes(M, N, K, dtype) bytes, 256-byte aligned; NULL
+ * where that is 0.
+ */
+int hyena_proj_fwd(const void *x, const void *w, const float *bias, const void *residual, void *y,
+                   void *z, int64_t M, int64_t N, int64_t K, int act, int dtype, void *workspace,
+                   size_t workspace_bytes, cudaStream_t stream);
+
+/* Host-only: workspace of hyena_proj_fwd (a multiple of 256), or minus HYENA_ERR_INVALID_ARG. */
+int64_t hyena_proj_workspace_bytes(int64_t M, int64_t N, int64_t K, int dtype);
+
+/*
+ * Gradients of hyena_proj_fwd for the upstream gradient dy [M, N] (the residual's is dy itself):
+ *
+ *     dz = dy act'(z),   dx = dz w (+ dx_add),   dw = dz^T x,   db[n] = sum_m dz[m][n]
+ *
+ * z: as the forward left it; NULL for HYENA_ACT_NONE.  dx_add: [M, K] or NULL, a gradient that
+ * reaches x another way (the residual branch, another projection of x); dx may be dx_add itself.
+ * dx [M, K], dw [N, K] of `dtype` and db fp32 [N] are overwritten; each may be NULL (x is not
+ * read without dw, nor w without dx, and may then be NULL).  dz is rounded to `dtype` as an
+ * operand of the products (db is not).  All tensors 16-byte aligned (db 4).  M == 0 zeroes dw and
+ * db.  Deterministic.
+ * workspace: at least hyena_proj_bwd_workspace_bytes(M, N, K, act, dtype) bytes, 256-byte aligned.
+ */
+int hyena_proj_bwd(const void *x, const void *w, const void *z, const void *dy,
+                   const void *dx_add, void *dx, void *dw, float *db, int64_t M, int64_t N,
+                   int64_t K, int act, int dtype, void *workspace, size_t workspace_bytes,
+                   cudaStream_t stream);
+
+/* Host-only: workspace of hyena_proj_bwd (a multiple of 256), or minus HYENA_ERR_INVALID_ARG. */
+int64_t hyena_proj_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int act, int dtype);
 
 #ifdef __cplusplus
 }
