@@ -31,10 +31,11 @@ struct Plan {
   int64_t tiles_m, tiles_n;
 };
 
+// (fp32 sums go on in registers, which hold no more than 128 x 128 outputs.)
 // The tile shape and the number of k cuts with the least estimated time: waves of persistent
 // workers x (k-blocks of one worker's tile x the time of a block + its epilogue), and for cut
 // products a second kernel over the partial sums.
-Plan plan_of(int64_t M, int64_t N, int64_t K, int dtype) {
+Plan find_plan(int64_t M, int64_t N, int64_t K, int dtype) {
   const struct {
     int tm, tn, workers;
     double block, tail;  // ns per k-block of 64, per tile
@@ -43,7 +44,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int dtype) {
   double best_ns = 0;
   const int kb = static_cast<int>((K + pj::kBK - 1) / pj::kBK), pairs = dtype == HYENA_DTYPE_F32 ? 6 : 1;
   const int64_t total = static_cast<int64_t>(kb) * pairs;
-  for (int s = 0; s < 3; ++s) {
+  for (int s = dtype == HYENA_DTYPE_F32 ? kOne128 : kPair256; s <= kOne64; ++s) {
     const int64_t tm = (M + shapes[s].tm - 1) / shapes[s].tm, tn = (N + shapes[s].tn - 1) / shapes[s].tn;
     for (int want = 1; want <= kMaxSplits; ++want) {
       const int64_t per = (total + want - 1) / want;
@@ -59,6 +60,22 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int dtype) {
     }
   }
   return best;
+}
+
+// The same, remembering the last few sizes a thread asked for (a call asks up to four times).
+Plan plan_of(int64_t M, int64_t N, int64_t K, int dtype) {
+  struct Entry {
+    int64_t M, N, K;
+    int dtype;
+    Plan plan;
+  };
+  thread_local Entry seen[8] = {};
+  thread_local unsigned next = 0;
+  for (const Entry &e : seen)
+    if (e.M == M && e.N == N && e.K == K && e.dtype == dtype) return e.plan;
+  Entry &e = seen[next++ % 8];
+  e = Entry{M, N, K, dtype, find_plan(M, N, K, dtype)};
+  return e.plan;
 }
 
 int64_t partial_bytes(int64_t M, int64_t N, int64_t K, int dtype) {
@@ -121,7 +138,8 @@ cudaError_t allow(int *resident) {
 }
 template <typename T, bool kAMn, bool kBMn>
 cudaError_t allow_all(int *resident) {
-  cudaError_t e = allow<T, 2, 256, kAMn, kBMn>(resident);
+  cudaError_t e = cudaSuccess;
+  if constexpr (sizeof(T) == 2) e = allow<T, 2, 256, kAMn, kBMn>(resident);
   if (e == cudaSuccess) e = allow<T, 1, 128, kAMn, kBMn>(nullptr);
   if (e == cudaSuccess) e = allow<T, 1, 64, kAMn, kBMn>(nullptr);
   return e;
@@ -137,10 +155,10 @@ int prepare_device(Device *d) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return HYENA_ERR_CUDA;
   std::call_once(once[dev], [dev]() {
     int r = 0;
-    cudaError_t e = allow_all<float, false, false>(&r);
+    cudaError_t e = allow_all<float, false, false>(nullptr);
     if (e == cudaSuccess) e = allow_all<float, false, true>(nullptr);
     if (e == cudaSuccess) e = allow_all<float, true, true>(nullptr);
-    if (e == cudaSuccess) e = allow_all<__nv_bfloat16, false, false>(nullptr);
+    if (e == cudaSuccess) e = allow_all<__nv_bfloat16, false, false>(&r);
     if (e == cudaSuccess) e = allow_all<__nv_bfloat16, false, true>(nullptr);
     if (e == cudaSuccess) e = allow_all<__nv_bfloat16, true, true>(nullptr);
     err[dev] = e;
@@ -196,7 +214,13 @@ int product(const Operand &a, const Operand &b, int64_t K, pj::Params p, int dty
     return HYENA_ERR_CUDA;
   cudaError_t e;
   switch (pl.shape) {
-    case kPair256: e = launch_shape<T, 2, 256, kAMn, kBMn>(ma, mb, p, d, stream); break;
+    case kPair256:
+      if constexpr (sizeof(T) == 2) {
+        e = launch_shape<T, 2, 256, kAMn, kBMn>(ma, mb, p, d, stream);
+        break;
+      } else {
+        return HYENA_ERR_UNSUPPORTED;  // not planned for fp32
+      }
     case kOne128: e = launch_shape<T, 1, 128, kAMn, kBMn>(ma, mb, p, d, stream); break;
     default: e = launch_shape<T, 1, 64, kAMn, kBMn>(ma, mb, p, d, stream);
   }

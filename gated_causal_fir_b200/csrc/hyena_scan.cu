@@ -125,6 +125,15 @@ cudaError_t allow_smem() {
   return e;
 }
 
+// f(integral constant) for every feed.
+template <typename F>
+void with_feed(F &&f) {
+  f(std::integral_constant<int, sc::kTmaChannel>());
+  f(std::integral_constant<int, sc::kTmaGroup>());
+  f(std::integral_constant<int, sc::kCopyChannel>());
+  f(std::integral_constant<int, sc::kCopyGroup>());
+}
+
 // Per-device one-time opt-in to the kernels' shared memory.
 int prepare_device(hyena::host::DeviceInfo *info) {
   if (hyena::host::device_info(info) != HYENA_OK) return HYENA_ERR_CUDA;
@@ -134,12 +143,11 @@ int prepare_device(hyena::host::DeviceInfo *info) {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return HYENA_ERR_CUDA;
   std::call_once(once[dev], [dev]() {
-    cudaError_t e = allow_smem<float, sc::kFeedChannel>();
-    if (e == cudaSuccess) e = allow_smem<float, sc::kFeedGroup>();
-    if (e == cudaSuccess) e = allow_smem<float, sc::kFeedPlain>();
-    if (e == cudaSuccess) e = allow_smem<__nv_bfloat16, sc::kFeedChannel>();
-    if (e == cudaSuccess) e = allow_smem<__nv_bfloat16, sc::kFeedGroup>();
-    if (e == cudaSuccess) e = allow_smem<__nv_bfloat16, sc::kFeedPlain>();
+    cudaError_t e = cudaSuccess;
+    with_feed([&](auto feed) {
+      if (e == cudaSuccess) e = allow_smem<float, decltype(feed)::value>();
+      if (e == cudaSuccess) e = allow_smem<__nv_bfloat16, decltype(feed)::value>();
+    });
     err[dev] = e;
   });
   return err[dev] == cudaSuccess ? HYENA_OK : HYENA_ERR_CUDA;
@@ -173,8 +181,8 @@ struct Launch {
 };
 template <typename T>
 Launch plan(sc::Params &p, int feed, int streams, int first, int count, int sm_count) {
-  if (feed != sc::kFeedGroup) p.g_box = 0;
-  const int decays = feed == sc::kFeedChannel
+  if (feed != sc::kTmaGroup) p.g_box = 0;
+  const int decays = sc::per_channel(feed)
                          ? sc::stream_bytes<T>()
                          : sc::decay_bytes<T>(p.pieces) +
                                static_cast<int>(round_up(sc::tile_rows<T>() * p.g_box * sizeof(T),
@@ -194,9 +202,9 @@ template <typename T, int kFeed, bool kOut>
 int run_fwd(const Shape &s, sc::Params p, int first, int count, int sms, cudaStream_t stream) {
   const Launch l = plan<T>(p, kFeed, kOut ? 3 : 2, first, count, sms);
   CUtensorMap mk{}, mv{}, mq{}, mg{};
-  if (kFeed != sc::kFeedPlain) {
+  if (sc::by_tma(kFeed)) {
     if (encode(&mk, s, p.k) || encode(&mv, s, p.v) || (kOut && encode(&mq, s, p.q)) ||
-        (kFeed == sc::kFeedChannel && encode(&mg, s, p.g)) ||
+        (kFeed == sc::kTmaChannel && encode(&mg, s, p.g)) ||
         (p.g_box && encode(&mg, s, p.g, s.G(), p.g_box)))
       return HYENA_ERR_CUDA;
   }
@@ -211,9 +219,9 @@ template <typename T, int kFeed, bool kOut>
 int run_bwd(const Shape &s, sc::Params p, int first, int count, int sms, cudaStream_t stream) {
   const Launch l = plan<T>(p, kFeed, kOut ? 4 : 2, first, count, sms);
   CUtensorMap mq{}, mdy{}, mk{}, mv{}, mg{};
-  if (kFeed != sc::kFeedPlain) {
+  if (sc::by_tma(kFeed)) {
     if (encode(&mq, s, p.q) || encode(&mdy, s, p.dy) || (kOut && encode(&mk, s, p.k)) ||
-        (kOut && encode(&mv, s, p.v)) || (kFeed == sc::kFeedChannel && encode(&mg, s, p.g)) ||
+        (kOut && encode(&mv, s, p.v)) || (kFeed == sc::kTmaChannel && encode(&mg, s, p.g)) ||
         (p.g_box && encode(&mg, s, p.g, s.G(), p.g_box)))
       return HYENA_ERR_CUDA;
   }
@@ -274,20 +282,30 @@ int backward(const Shape &s, sc::Params p, void *ws, int sms, cudaStream_t strea
              : HYENA_ERR_CUDA;
 }
 
-// Which feed takes the tensors: TMA needs 16-byte rows and bases.
-int choose_feed(const Shape &s, std::initializer_list<const void *> streams, const void *g) {
-  bool tma = s.D * s.es() % 16 == 0 && s.D * s.es() * s.L < (int64_t{1} << 40);
-  for (const void *t : streams) tma = tma && aligned(t, 16);
-  if (!tma) return sc::kFeedPlain;
-  if (s.d_g > 1) return s.d_g % 2 == 0 ? sc::kFeedGroup : sc::kFeedPlain;
-  return aligned(g, 16) ? sc::kFeedChannel : sc::kFeedPlain;
+// Which feed takes the tensors, from their rows and addresses; sets the copies' and stores' width.
+// TMA needs rows and bases of 16 bytes, and a group's decay for both channels of a pair.
+int choose_feed(const Shape &s, std::initializer_list<const void *> streams,
+                std::initializer_list<const void *> outs, const void *g, sc::Params *p) {
+  uintptr_t bits = static_cast<uintptr_t>(s.D * s.es()), out_bits = bits;
+  for (const void *t : streams) bits |= reinterpret_cast<uintptr_t>(t);
+  if (s.d_g == 1) bits |= reinterpret_cast<uintptr_t>(g);
+  for (const void *t : outs) out_bits |= reinterpret_cast<uintptr_t>(t);
+  const uintptr_t pair = static_cast<uintptr_t>(2 * s.es());
+  p->pair_out = out_bits % pair == 0;
+  p->copy = bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : 0;
+  const bool tma = bits % 16 == 0 && p->pair_out && s.D * s.es() * s.L < (int64_t{1} << 40) &&
+                   (s.d_g == 1 || s.d_g % 2 == 0);
+  return tma ? (s.d_g == 1 ? sc::kTmaChannel : sc::kTmaGroup)
+             : (s.d_g == 1 ? sc::kCopyChannel : sc::kCopyGroup);
 }
 
-template <typename T, typename F>
-int with_feed(int feed, F &&f) {
-  if (feed == sc::kFeedChannel) return f(std::integral_constant<int, sc::kFeedChannel>());
-  if (feed == sc::kFeedGroup) return f(std::integral_constant<int, sc::kFeedGroup>());
-  return f(std::integral_constant<int, sc::kFeedPlain>());
+template <typename F>
+int with_one_feed(int feed, F &&f) {
+  int rc = HYENA_ERR_UNSUPPORTED;
+  with_feed([&](auto one) {
+    if (decltype(one)::value == feed) rc = f(one);
+  });
+  return rc;
 }
 
 // Copies a state (zeros if null) for problems of no tokens.
@@ -378,8 +396,8 @@ int hyena_scan_fwd(const void *q, const void *k, const void *v, const void *g, c
   p.s_out = s_out;
   p.ckpt = ckpt;
   p.y = y;
-  const int feed = choose_feed(s, {q, k, v, y}, g);
-  return with_feed<void>(feed, [&](auto f) {
+  const int feed = choose_feed(s, {q, k, v}, {y}, g, &p);
+  return with_one_feed(feed, [&](auto f) {
     constexpr int kFeed = decltype(f)::value;
     return dtype == HYENA_DTYPE_F32
                ? forward<float, kFeed>(s, p, workspace, info.sm_count, stream)
@@ -428,10 +446,9 @@ int hyena_scan_bwd(const void *q, const void *k, const void *v, const void *g, c
   p.dv = dv;
   p.dg = dg;
   p.ds0 = ds0;
-  const int feed = choose_feed(s, {q, k, v, dy, dq, dk, dv}, g);
-  // the per-channel feed also stores dg in pairs
-  const int use = feed == sc::kFeedChannel && !aligned(dg, 16) ? sc::kFeedPlain : feed;
-  return with_feed<void>(use, [&](auto f) {
+  const int feed = s.d_g == 1 ? choose_feed(s, {q, k, v, dy}, {dq, dk, dv, dg}, g, &p)
+                              : choose_feed(s, {q, k, v, dy}, {dq, dk, dv}, g, &p);
+  return with_one_feed(feed, [&](auto f) {
     constexpr int kFeed = decltype(f)::value;
     return dtype == HYENA_DTYPE_F32
                ? backward<float, kFeed>(s, p, workspace, info.sm_count, stream)

@@ -8,7 +8,10 @@
 //
 // fp32 operands are split into three bf16 planes a = a0 + a1 + a2 (8 bits of the mantissa each),
 // and C is the sum of the six products of planes i + j <= 2, smallest first; the three left out
-// are below 2^-26 of a b.  They run 6 bf16 products, ~4x the rate that fp32 FMA units would give.
+// are below 2^-26 of a b.  The tensor cores' accumulator truncates at every addition, which over
+// thousands of k is a bias above fp32's own rounding: every 256 k the epilogue warps take the
+// accumulator into registers, where the sum goes on with rounding to nearest (error of a
+// 4096-term product against 64 bits: ...).
 //
 // Tiles.  kCG = 2: a pair of CTAs works on 256 x 256 outputs with tcgen05.mma.cta_group::2, each
 // holding 128 rows of A, 128 rows of B and 128 rows of the accumulator.  Each byte staged then
@@ -61,6 +64,9 @@ struct Tile {
   static constexpr int kSmem = kStages * kStage + kFixed;
   static constexpr int kTmemCols = 2 * kBN < 32 ? 32 : 2 * kBN;  // two accumulators
 };
+
+// k-blocks per accumulator when sums go on in registers (fp32 operands).
+constexpr int kFlush = 4;
 
 struct Params {
   int M, N, kb;                 // outputs; k-blocks of one product
@@ -280,6 +286,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     proj_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                 const Params p) {
   using L = Tile<kCG, kBN>;
+  constexpr bool kPromote = sizeof(T) == 4;
+  static_assert(!kPromote || kCG == 1, "the sums of a pair's tile do not fit the registers");
   extern __shared__ uint8_t dynamic[];
   __shared__ uint64_t full[L::kStages], empty[L::kStages], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_at;
@@ -358,30 +366,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------------------- MMA
       constexpr uint32_t id = idesc_bf16(L::kM, L::kN, kAMn, kBMn);
       constexpr uint32_t kStepA = (kAMn ? 16 * 128 : 32) >> 4, kStepB = (kBMn ? 16 * 128 : 32) >> 4;
-      int it = 0, n = 0;
+      int it = 0, n = 0;  // k-blocks; accumulators filled
       bool ok = true;
-      for (int w = first; w < works && ok; w += step, ++n) {
+      for (int w = first; w < works && ok; w += step) {
         const Work k = work_at(p, w);
-        const int acc = n & 1;
-        if (n >= 2 && !mbar_wait(&acc_empty[acc], (n / 2 - 1) & 1, &abort, p.status, kTimeout)) break;
-        tc_fence_after_sync();
-        const uint32_t d = tmem + acc * kBN;
-        for (int kb = k.kb0; kb < k.kb1; ++kb, ++it) {
-          const int st = it % L::kStages;
-          if (!mbar_wait(&full[st], (it / L::kStages) & 1, &abort, p.status, kTimeout)) {
+        for (int kb = k.kb0; kb < k.kb1 && ok; ++n) {
+          const int acc = n & 1, end = kPromote ? min(kb + kFlush, k.kb1) : k.kb1;
+          if (n >= 2 && !mbar_wait(&acc_empty[acc], (n / 2 - 1) & 1, &abort, p.status, kTimeout)) {
             ok = false;
             break;
           }
           tc_fence_after_sync();
-          const uint32_t a = smem_u32(stages + st * L::kStage), b = a + L::kABytes;
-          const uint64_t da = umma_smem_desc(a, kAMn ? 8192 : 16, 1024, 2);
-          const uint64_t db = umma_smem_desc(b, kBMn ? 8192 : 16, 1024, 2);
+          const uint32_t d = tmem + acc * kBN;
+          for (uint32_t more = 0; kb < end; ++kb, ++it) {
+            const int st = it % L::kStages;
+            if (!mbar_wait(&full[st], (it / L::kStages) & 1, &abort, p.status, kTimeout)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after_sync();
+            const uint32_t a = smem_u32(stages + st * L::kStage), b = a + L::kABytes;
+            const uint64_t da = umma_smem_desc(a, kAMn ? 8192 : 16, 1024, 2);
+            const uint64_t db = umma_smem_desc(b, kBMn ? 8192 : 16, 1024, 2);
 #pragma unroll
-          for (int s = 0; s < kBK / 16; ++s)
-            mma<kCG>(d, da + s * kStepA, db + s * kStepB, id, kb > k.kb0 || s > 0);
-          commit<kCG>(&empty[st]);
+            for (int s = 0; s < kBK / 16; ++s) {
+              mma<kCG>(d, da + s * kStepA, db + s * kStepB, id, more);
+              more = 1;
+            }
+            commit<kCG>(&empty[st]);
+          }
+          if (ok) commit<kCG>(&acc_full[acc]);
         }
-        if (ok) commit<kCG>(&acc_full[acc]);
       }
       // MMAs still reading shared memory when a wait gave up: let them finish
       if (!ok || abort) {
@@ -393,35 +408,89 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // --------------------------------------------------------------------------- epilogue
     const int quad = warp % 4;  // the 32 lanes of tensor memory that this warp may read
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     float *out = reinterpret_cast<float *>(stages + L::kStages * L::kStage + (warp - 2) * kStageOut);
+    const auto release = [&](int acc) {  // the accumulator is in registers: the next may start
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (kCG == 2)
+          arrive_at(in_cta(&acc_empty[acc], 0));
+        else
+          mbar_arrive(&acc_empty[acc]);
+      }
+    };
     int n = 0;
-    for (int w = first; w < works; w += step, ++n) {
+    bool ok = true;
+    for (int w = first; w < works && ok; w += step) {
       const Work k = work_at(p, w);
-      const int acc = n & 1;
-      const bool ok = mbar_wait(&acc_full[acc], (n / 2) & 1, &abort, p.status, kTimeout);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after_sync();
       const int row0 = k.m * L::kM + static_cast<int>(rank) * kRows + quad * 32;
-#pragma unroll 1
+      [[maybe_unused]] float sum[kPromote ? kBN : 1];
+      if constexpr (kPromote) {
+#pragma unroll
+        for (int c = 0; c < kBN; ++c) sum[c] = 0.0f;
+        for (int kb = k.kb0; kb < k.kb1 && ok; kb += kFlush, ++n) {
+          const int acc = n & 1;
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait(&acc_full[acc], (n / 2) & 1, &abort, p.status, kTimeout));
+          if (!ok) break;
+          tc_fence_after_sync();
+#pragma unroll
+          for (int c0 = 0; c0 < kBN; c0 += 32) {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(lanes + acc * kBN + c0, r);
+            tmem_wait_ld();
+            reg_fence(r);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) sum[c0 + c] += __uint_as_float(r[c]);
+          }
+          release(acc);
+        }
+      } else {
+        ok = __all_sync(0xffffffffu,
+                        mbar_wait(&acc_full[n & 1], (n / 2) & 1, &abort, p.status, kTimeout));
+        tc_fence_after_sync();
+      }
+      if (!ok) break;
+      constexpr int V = 16 / static_cast<int>(sizeof(T));
+      const bool wide = p.vec && p.splits == 1;
+#pragma unroll(kPromote ? kBN / kChunk : 1)
       for (int c0 = 0; c0 < kBN; c0 += kChunk) {
-        const uint32_t at = tmem + acc * kBN + c0 + (static_cast<uint32_t>(quad * 32) << 16);
-        uint32_t r0[32], r1[32];
-        tmem_ld_32x32b_x32(at, r0);
-        tmem_ld_32x32b_x32(at + 32, r1);
-        tmem_wait_ld();
-        reg_fence(r0);
-        reg_fence(r1);
-        if (c0 + kChunk >= kBN) {  // the accumulator is in registers: the next tile may start
-          tc_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) {
-            if (kCG == 2)
-              arrive_at(in_cta(&acc_empty[acc], 0));
-            else
-              mbar_arrive(&acc_empty[acc]);
+        // phase 2 of this chunk: lane -> rows 4 i + lane / 8, columns col .. col + 7
+        const int col = k.n * L::kN + c0 + (lane % 8) * 8, sub = lane / 8;
+        VecOf<T, 8> res[8];  // the residual, requested before the accumulator is waited for
+        if (wide && p.residual) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = row0 + 4 * i + sub;
+#pragma unroll
+            for (int h = 0; h < 8; h += V)
+              if (row < p.M && col + h < p.N)
+                *reinterpret_cast<VecOf<T, V> *>(&res[i].e[h]) =
+                    *reinterpret_cast<const VecOf<T, V> *>(static_cast<const T *>(p.residual) +
+                                                           static_cast<int64_t>(row) * p.N + col + h);
           }
         }
-        // row `lane`, in 16-byte pieces at positions swizzled by the row
+        float bias[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          bias[e] = p.bias && p.splits == 1 && col + e < p.N ? p.bias[col + e] : 0.0f;
+        // phase 1: row `lane` into shared memory, in 16-byte pieces swizzled by the row
+        uint32_t r0[32], r1[32];
+        if constexpr (kPromote) {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            r0[c] = __float_as_uint(sum[c0 + c]);
+            r1[c] = __float_as_uint(sum[c0 + 32 + c]);
+          }
+        } else {
+          tmem_ld_32x32b_x32(lanes + (n & 1) * kBN + c0, r0);
+          tmem_ld_32x32b_x32(lanes + (n & 1) * kBN + c0 + 32, r1);
+          tmem_wait_ld();
+          reg_fence(r0);
+          reg_fence(r1);
+          if (c0 + kChunk >= kBN) release(n & 1);
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           *reinterpret_cast<uint4 *>(out + lane * kChunk + ((j ^ (lane & 7)) * 4)) =
@@ -430,39 +499,70 @@ __global__ void __launch_bounds__(kThreads, 1)
               make_uint4(r1[4 * j], r1[4 * j + 1], r1[4 * j + 2], r1[4 * j + 3]);
         }
         __syncwarp();
-        const int col = k.n * L::kN + c0 + (lane % 8) * 8;
-        float bias[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          bias[e] = p.bias && p.splits == 1 && col + e < p.N ? p.bias[col + e] : 0.0f;
-#pragma unroll 1
-        for (int i = 0; i < 8; ++i) {  // four rows at a time, eight lanes of eight columns each
-          const int r = i * 4 + lane / 8;
-          const int j = 2 * (lane % 8);
+        const auto staged = [&](int i, float (&c)[8]) {
+          const int r = 4 * i + sub, j = 2 * (lane % 8);
           const float *src = out + r * kChunk + (j & 8) * 4;
           const float4 u = *reinterpret_cast<const float4 *>(src + (((j & 7) ^ (r & 7)) * 4));
           const float4 v = *reinterpret_cast<const float4 *>(src + ((((j & 7) + 1) ^ (r & 7)) * 4));
-          float c[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-          const int64_t row = row0 + r;
-          if (row >= p.M || col >= p.N) continue;
-          if (p.splits > 1) {
+          c[0] = u.x + bias[0], c[1] = u.y + bias[1], c[2] = u.z + bias[2], c[3] = u.w + bias[3];
+          c[4] = v.x + bias[4], c[5] = v.y + bias[5], c[6] = v.z + bias[6], c[7] = v.w + bias[7];
+        };
+        if (wide) {
+          with_act(p.act, [&](auto act) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float c[8];
+              staged(i, c);
+              const int row = row0 + 4 * i + sub;
+              if (row >= p.M) continue;
+              const int64_t at = static_cast<int64_t>(row) * p.N + col;
+#pragma unroll
+              for (int h = 0; h < 8; h += V) {
+                if (col + h >= p.N) break;
+                VecOf<T, V> o;
+                if (p.z) {
+#pragma unroll
+                  for (int e = 0; e < V; ++e) from_f(c[h + e], &o.e[e]);
+                  *reinterpret_cast<VecOf<T, V> *>(static_cast<T *>(p.z) + at + h) = o;
+                }
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                  float y = act_of<T, decltype(act)::value>(c[h + e]);
+                  if (p.residual) y += to_f(res[i].e[h + e]);
+                  from_f(y, &o.e[e]);
+                }
+                *reinterpret_cast<VecOf<T, V> *>(static_cast<T *>(p.y) + at + h) = o;
+              }
+            }
+          });
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i) {
+            float c[8];
+            staged(i, c);
+            const int64_t row = row0 + 4 * i + sub;
+            if (row >= p.M || col >= p.N) continue;
+            if (p.splits == 1) {
+              finish<T, 8>(p, c, row, col);
+              continue;
+            }
             float *to = p.partial + (static_cast<int64_t>(k.split) * p.M + row) * p.N + col;
-            if (p.N % 4 == 0 && col + 8 <= p.N) {
-              *reinterpret_cast<float4 *>(to) = u;
-              *reinterpret_cast<float4 *>(to + 4) = v;
+            if (p.N % 4 == 0) {
+#pragma unroll
+              for (int h = 0; h < 8; h += 4)
+                if (col + h < p.N)
+                  *reinterpret_cast<float4 *>(to + h) =
+                      make_float4(c[h], c[h + 1], c[h + 2], c[h + 3]);
             } else {
 #pragma unroll
               for (int e = 0; e < 8; ++e)
                 if (col + e < p.N) to[e] = c[e];
             }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) c[e] += bias[e];
-            finish<T, 8>(p, c, row, col);
           }
         }
         __syncwarp();
       }
+      if (!kPromote) ++n;
     }
   }
   // Both CTAs' MMAs read each other's shared memory and signal each other's barriers.

@@ -45,14 +45,13 @@ constexpr int kThreads = kComputeThreads + 32 * kHelperWarps;
 constexpr int kMaxStages = 8;
 constexpr unsigned int kTimeout = 1u; // HYENA_DEVICE_TIMEOUT
 
-// How a tile's inputs reach shared memory.
-enum Feed {
-  kFeedChannel = 0,  // TMA, one decay per channel: g is a stream like k and v
-  kFeedGroup = 1,    // TMA for the streams and the groups' g, of which the helper warps form the
-                     // decays (TMA for the streams alone where rows of g are no multiple of 16
-                     // bytes)
-  kFeedPlain = 2     // element loads by the helper warps (rows TMA cannot address), any d_g
-};
+// How a tile's inputs reach shared memory: the streams by TMA, or where their rows are no multiple
+// of 16 bytes by asynchronous 8- or 4-byte copies (single elements where not even those are
+// aligned).  One decay per channel: g is a stream like k and v and the compute warps take its exp.
+// One per group: the helper warps do.
+enum Feed { kTmaChannel = 0, kTmaGroup = 1, kCopyChannel = 2, kCopyGroup = 3 };
+__host__ __device__ constexpr bool by_tma(int feed) { return feed <= kTmaGroup; }
+__host__ __device__ constexpr bool per_channel(int feed) { return feed % 2 == 0; }
 
 // Rows of a tile are 16 R.  The registers of a segment and the bytes of a stage both grow with
 // R; the joining of segments costs 16 steps per tile whatever R is.
@@ -72,7 +71,7 @@ __host__ __device__ constexpr int decay_bytes(int pieces) {
 }
 
 struct Params {
-  const void *q, *k, *v, *g, *dy;   // for kFeedPlain; g also for kFeedGroup
+  const void *q, *k, *v, *g, *dy;
   const float *s0;                  // [B, D] or null
   const float *ds_out;              // [B, D] or null (backward)
   float *s_out;                     // [B, D] or null: the last state
@@ -88,7 +87,9 @@ struct Params {
   int unit_split0, unit_splits;     // the cuts this launch works on
   int n_units;                      // B x unit_splits x n_cb
   int pieces;                       // groups a block of 32 channels touches at most
-  int g_box;                        // groups per row of g's tile (kFeedGroup); 0: element loads
+  int g_box;                        // groups per row of g's tile (kTmaGroup); 0: element loads
+  int copy;                         // bytes per asynchronous copy: 8, 4, or 0 for element loads
+  int pair_out;                     // rows and bases allow stores of two channels
   int stages, stage_bytes;
   int dg_mode;                      // 0: dg itself, 1: one partial per block, 2: per channel
 };
@@ -140,14 +141,9 @@ __device__ __forceinline__ void store_one(float *p, float x) { *p = x; }
 __device__ __forceinline__ float load_one(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
 __device__ __forceinline__ float load_one(const float *p) { return *p; }
 
-// exp(g): one multiply and the hardware's 2^x.  The product's rounding moves the result by
-// |g| 2^-24 of itself, which is small wherever the decay is not (|g| exp(g) < 0.37); 2^x is within
-// 2^-22.  exp(-inf) = 0, and decays below fp32's normal range are 0.
-__device__ __forceinline__ float decay(float g) {
-  float a;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(g * 1.4426950408889634f));
-  return a;
-}
+// exp(g), accurately: a state sums hundreds of products of decays, and the faster 2^x (with its
+// 2^-22) left the states three times as far off, for 4 us of 62 (B=1 L=8192 D=4096 d_g=1).
+__device__ __forceinline__ float decay(float g) { return expf(g); }
 
 __device__ __forceinline__ void compute_barrier() {
   asm volatile("bar.sync 1, %0;" ::"n"(kComputeThreads) : "memory");
@@ -199,15 +195,42 @@ __device__ __forceinline__ void convert_decays(const Params &p, float *as, const
     as[e] = decay(load_one(g + e / p.pieces * p.g_box + first + e % p.pieces));
 }
 
-// Element loads of one stream's tile; zero outside the tensor, as TMA fills.
+// One stream's tile by the helper threads' asynchronous copies; zero outside the tensor, as TMA
+// fills.
+template <typename T, int kBytes>
+__device__ __forceinline__ void copy_tile(const Params &p, T *dst, const void *src, int b, int c0,
+                                          int t0, int thread) {
+  constexpr int E = kBytes / static_cast<int>(sizeof(T)), N = kCh / E;  // elements; copies per row
+  constexpr int kStep = 32 * kHelperWarps / N;                          // rows apart
+  static_assert(E >= 1 && 32 * kHelperWarps % N == 0, "copies of a row");
+  const int c = c0 + thread % N * E, row0 = thread / N;
+  const T *s = static_cast<const T *>(src) + (static_cast<int64_t>(b) * p.L + t0 + row0) * p.D + c;
+  uint32_t d = smem_u32(dst + row0 * kCh + thread % N * E);
+  const int rows = c < p.D ? p.L - t0 : 0;
+  for (int r = row0; r < tile_rows<T>(); r += kStep) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d),
+                 "l"(r < rows ? s : static_cast<const T *>(src)), "n"(kBytes),
+                 "r"(r < rows ? kBytes : 0)
+                 : "memory");
+    s += static_cast<int64_t>(kStep) * p.D;
+    d += kStep * kCh * static_cast<int>(sizeof(T));
+  }
+}
+
 template <typename T>
-__device__ __forceinline__ void fill_plain(const Params &p, T *dst, const void *src, int b, int c0,
-                                           int t0, int thread, int threads) {
+__device__ __forceinline__ void load_elements(const Params &p, T *dst, const void *src, int b,
+                                              int c0, int t0, int thread) {
   const T *s = static_cast<const T *>(src) + static_cast<int64_t>(b) * p.L * p.D;
-  for (int e = thread; e < tile_rows<T>() * kCh; e += threads) {
+  for (int e = thread; e < tile_rows<T>() * kCh; e += 32 * kHelperWarps) {
     const int t = t0 + e / kCh, c = c0 + e % kCh;
     dst[e] = t < p.L && c < p.D ? s[static_cast<int64_t>(t) * p.D + c] : T(0.0f);
   }
+}
+
+// Arrives on `bar` when this thread's asynchronous copies so far have landed.
+__device__ __forceinline__ void arrive_after_copies(uint64_t *bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
 }
 
 // The helper warps: NS streams of every tile of the CTA's units into the ring, in the order the
@@ -217,78 +240,84 @@ __device__ __forceinline__ void feed(const Params &p, Ring &ring, uint8_t *stage
                                      const CUtensorMap *const (&maps)[5],
                                      const void *const (&ptrs)[5]) {
   const int warp = threadIdx.x / 32 - kComputeThreads / 32, lane = threadIdx.x % 32;
-  constexpr int kStreams = NS + (kFeed == kFeedChannel ? 1 : 0);
+  constexpr int kStreams = NS + (per_channel(kFeed) ? 1 : 0);
   constexpr int kBytes = stream_bytes<T>();
   constexpr int kGroups = 16 / static_cast<int>(sizeof(T));  // groups in 16 bytes of g
-  if (kFeed == kFeedChannel && (warp != 0 || lane != 0)) return;
-  if (kFeed == kFeedGroup && warp == 0 && lane != 0) return;
+  const int th = threadIdx.x - kComputeThreads;
+  if (by_tma(kFeed) && warp == 0 && lane != 0) return;
+  if (kFeed == kTmaChannel && warp != 0) return;
   int it = 0, last = 0;
   for (int u = blockIdx.x; u < p.n_units; u += gridDim.x) {
     const Unit un(p, u);
+    const int c0 = un.cb * kCh;
     for (int i = un.tile0; i < un.tile1; ++i, ++it) {
-      const int tile = kReverse ? un.tile1 - 1 - (i - un.tile0) : i;
+      const int tile = kReverse ? un.tile1 - 1 - (i - un.tile0) : i, t0 = tile * tile_rows<T>();
       const int st = it % p.stages, round = it / p.stages;
       uint8_t *buf = stages + st * p.stage_bytes;
+      float *as = reinterpret_cast<float *>(buf + NS * kBytes);  // where decays are formed here
       if (round > 0 && !mbar_wait(&ring.empty[st], (round - 1) & 1, &ring.abort, p.status, kTimeout))
         goto out;
-      if (kFeed != kFeedPlain && warp == 0) {
-        if (kFeed == kFeedGroup && p.g_box) {
-          uint8_t *g_at = buf + NS * kBytes + decay_bytes<T>(p.pieces);
-          const int x = un.cb * kCh / p.d_g / kGroups * kGroups;
+      if (by_tma(kFeed) && warp == 0) {
+        if (kFeed == kTmaGroup && p.g_box) {
           mbar_arrive_expect_tx(&ring.raw[st], tile_rows<T>() * p.g_box * sizeof(T));
-          tma_load_3d(g_at, maps[4], &ring.raw[st], x, tile * tile_rows<T>(), un.b);
+          tma_load_3d(buf + NS * kBytes + decay_bytes<T>(p.pieces), maps[4], &ring.raw[st],
+                      c0 / p.d_g / kGroups * kGroups, t0, un.b);
         }
         mbar_arrive_expect_tx(&ring.full[st], kStreams * kBytes);
 #pragma unroll
         for (int s = 0; s < kStreams; ++s)
-          tma_load_3d(buf + s * kBytes, maps[s], &ring.full[st], un.cb * kCh,
-                      tile * tile_rows<T>(), un.b);
+          tma_load_3d(buf + s * kBytes, maps[s], &ring.full[st], c0, t0, un.b);
         last = it + 1;
       }
-      if (kFeed == kFeedGroup && warp > 0) {
-        const int th = threadIdx.x - kComputeThreads - 32, n = 32 * (kHelperWarps - 1);
-        float *as = reinterpret_cast<float *>(buf + NS * kBytes);
+      if (kFeed == kTmaGroup && warp > 0) {
         if (p.g_box) {
           if (!mbar_wait(&ring.raw[st], round & 1, &ring.abort, p.status, kTimeout)) goto out;
           convert_decays<T>(p, as,
                             reinterpret_cast<const T *>(buf + NS * kBytes +
                                                         decay_bytes<T>(p.pieces)),
-                            un.cb * kCh / p.d_g % kGroups, th, n);
+                            c0 / p.d_g % kGroups, th - 32, 32 * (kHelperWarps - 1));
         } else {
-          fill_decays<T>(p, as, un.b, un.cb * kCh, tile * tile_rows<T>(), th, n);
+          fill_decays<T>(p, as, un.b, c0, t0, th - 32, 32 * (kHelperWarps - 1));
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&ring.full[st]);
       }
-      if (kFeed == kFeedPlain) {
-        const int th = threadIdx.x - kComputeThreads;
+      if (!by_tma(kFeed)) {
 #pragma unroll
-        for (int s = 0; s < NS; ++s)
-          fill_plain<T>(p, reinterpret_cast<T *>(buf + s * kBytes), ptrs[s], un.b, un.cb * kCh,
-                        tile * tile_rows<T>(), th, 32 * kHelperWarps);
-        fill_decays<T>(p, reinterpret_cast<float *>(buf + NS * kBytes), un.b, un.cb * kCh,
-                       tile * tile_rows<T>(), th, 32 * kHelperWarps);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ring.full[st]);
+        for (int s = 0; s < kStreams; ++s) {
+          T *dst = reinterpret_cast<T *>(buf + s * kBytes);
+          if (p.copy == 8)
+            copy_tile<T, 8>(p, dst, ptrs[s], un.b, c0, t0, th);
+          else if (p.copy == 4)
+            copy_tile<T, 4>(p, dst, ptrs[s], un.b, c0, t0, th);
+          else
+            load_elements<T>(p, dst, ptrs[s], un.b, c0, t0, th);
+        }
+        if (!per_channel(kFeed)) fill_decays<T>(p, as, un.b, c0, t0, th, 32 * kHelperWarps);
+        // one arrival for the copies, and one for what the thread stored itself
+        if (p.copy) arrive_after_copies(&ring.full[st]);
+        if (!p.copy || !per_channel(kFeed)) mbar_arrive(&ring.full[st]);
       }
     }
   }
 out:
   // no copy may be in flight when the CTA ends, whatever happened to the readers
-  if (kFeed != kFeedPlain && warp == 0) {
+  if (by_tma(kFeed) && warp == 0) {
     for (int j = max(0, last - p.stages); j < last; ++j) {
       int no_abort = 0;
-      if (kFeed == kFeedGroup && p.g_box)
+      if (kFeed == kTmaGroup && p.g_box)
         mbar_wait(&ring.raw[j % p.stages], (j / p.stages) & 1, &no_abort, p.status, kTimeout);
       mbar_wait(&ring.full[j % p.stages], (j / p.stages) & 1, &no_abort, p.status, kTimeout);
     }
   }
+  if (!by_tma(kFeed)) asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 template <int kFeed>
 __device__ __forceinline__ void ring_init(const Params &p, Ring &ring) {
   if (threadIdx.x == 0) {
-    const int arrivals = kFeed == kFeedChannel ? 1 : kHelperWarps;
+    const int arrivals = by_tma(kFeed) ? (per_channel(kFeed) ? 1 : kHelperWarps)
+                                       : 32 * kHelperWarps * (p.copy && !per_channel(kFeed) ? 2 : 1);
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&ring.full[i], arrivals);
       mbar_init(&ring.empty[i], kComputeThreads / 32);
@@ -301,9 +330,9 @@ __device__ __forceinline__ void ring_init(const Params &p, Ring &ring) {
 }
 
 // A lane's decays in the rows of its segment.
-template <typename T, int kFeed> struct Decays;
-template <typename T>
-struct Decays<T, kFeedChannel> {  // from the lane's pairs of g
+template <typename T, int kFeed, bool kChannel = per_channel(kFeed)> struct Decays;
+template <typename T, int kFeed>
+struct Decays<T, kFeed, true> {  // from the lane's pairs of g
   using Held = F2;
   const uint8_t *at;
   __device__ Decays(const Params &, const uint8_t *tile, int seg, int l, int)
@@ -316,7 +345,7 @@ struct Decays<T, kFeedChannel> {  // from the lane's pairs of g
   __device__ static F2 pair(Held a) { return a; }
 };
 template <typename T>
-struct Decays<T, kFeedGroup> {  // d_g is even: the two channels share one
+struct Decays<T, kTmaGroup, false> {  // d_g is even: the two channels share one
   using Held = float;
   const float *at;
   int step;
@@ -330,7 +359,7 @@ struct Decays<T, kFeedGroup> {  // d_g is even: the two channels share one
   __device__ static F2 pair(Held a) { return pack(a, a); }
 };
 template <typename T>
-struct Decays<T, kFeedPlain> {
+struct Decays<T, kCopyGroup, false> {
   using Held = F2;
   const float *at;
   int step, second;
@@ -351,18 +380,19 @@ struct Out {
   T *at;
   uint32_t stride;  // bytes per row; D is below 2^28
   int live;
-  bool hi;
+  bool hi, pairs;
   __device__ Out(void *base, const Params &p, int b, int t0, int c, bool dead) {
     at = static_cast<T *>(base) + (static_cast<int64_t>(b) * p.L + t0) * p.D + c;
     stride = static_cast<uint32_t>(p.D) * static_cast<uint32_t>(sizeof(T));
     live = dead || c >= p.D ? 0 : p.L - t0;
     hi = c + 1 < p.D;
+    pairs = by_tma(kFeed) || p.pair_out;
   }
   __device__ void put(int r, F2 x) const {
     if (r >= live) return;
     T *to = reinterpret_cast<T *>(reinterpret_cast<uint8_t *>(at) +
                                   static_cast<uint64_t>(stride) * static_cast<uint32_t>(r));
-    if (kFeed != kFeedPlain) {  // rows are a multiple of 16 bytes: a pair is inside or outside
+    if (pairs) {  // D is even: a pair is inside or outside
       Pair<T>::store(to, x);
     } else {
       const float2 v = unpack(x);
@@ -421,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_wait();
   if (threadIdx.x >= kComputeThreads) {
     const CUtensorMap *const maps[5] = {&mk, &mv, kOut ? &mq : &mg, &mg, &mg};
-    const void *const ptrs[5] = {p.k, p.v, p.q, nullptr, nullptr};
+    const void *const ptrs[5] = {p.k, p.v, kOut ? p.q : p.g, p.g, nullptr};
     feed<T, kFeed, false, NS>(p, ring, stages, maps, ptrs);
     return;
   }
@@ -542,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_wait();
   if (threadIdx.x >= kComputeThreads) {
     const CUtensorMap *const maps[5] = {&mq, &mdy, kOut ? &mk : &mg, &mv, &mg};
-    const void *const ptrs[5] = {p.q, p.dy, p.k, p.v, nullptr};
+    const void *const ptrs[5] = {p.q, p.dy, kOut ? p.k : p.g, p.v, p.g};
     feed<T, kFeed, true, NS>(p, ring, stages, maps, ptrs);
     return;
   }
@@ -639,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const F2 d = mul2(w, before[r]);
           dk.put(r, mul2(ut, Pair<T>::f(vr[r])));
           dv.put(r, mul2(ut, Pair<T>::f(kr[r])));
-          if (kFeed == kFeedChannel || (kFeed == kFeedPlain && p.d_g == 1)) {
+          if (per_channel(kFeed)) {
             dg.put(r, d);
           } else if (p.dg_mode == 2) {
             if (r < dg.live)
@@ -649,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             sum[r] = two.x + two.y;
           }
         }
-        if (kFeed != kFeedChannel && p.d_g > 1 && p.dg_mode != 2) {
+        if (!per_channel(kFeed) && p.dg_mode != 2) {
           // groups of 2, 4, ..., 16 channels or whole blocks: sums over neighbouring lanes
           const int64_t row0 = static_cast<int64_t>(un.b) * p.L + t0;
           const int rows = dead ? 0 : min(R, p.L - t0);

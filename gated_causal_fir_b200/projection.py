@@ -7,30 +7,32 @@ CUDA tensors into pointers, sizes and a stream; outputs and workspaces that are 
 from torch.
 """
 from . import _native
-from ._args import On, code as code_of, nbytes, need, ptr, torch_, workspace as workspace_of
+from ._args import (On, code as code_of, cuda_tensor, nbytes, need, ptr, torch_,
+                    workspace as workspace_of)
 from ._native import ACT_CODES, HYENA_DTYPE_BF16
 
 
 def _act(act):
-    if act not in ACT_CODES:
-        raise ValueError("act must be one of %s, got %r" % (", ".join(ACT_CODES), act))
-    return ACT_CODES[act]
+    try:
+        return ACT_CODES[act]
+    except (KeyError, TypeError):
+        raise ValueError("act must be one of %s, got %r" % (", ".join(ACT_CODES), act)) from None
 
 
 def _rows(x, w):
     """(type code, M, N, K) of x [..., K] and w [N, K]."""
-    torch = torch_()
-    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() < 2:
+    cuda_tensor("x", x, "[..., K] tensor")
+    shape = x.shape
+    if len(shape) < 2:
         raise TypeError("x must be a CUDA [..., K] tensor of at least two dimensions")
     code = code_of(x, "x")
-    K = x.shape[-1]
-    need("x", x, x.shape, x.dtype, x.device)
-    if not isinstance(w, torch.Tensor) or w.dim() != 2 or w.shape[1] != K:
-        raise ValueError("w must be a [N, %d] tensor" % K)
-    need("w", w, w.shape, x.dtype, x.device)
+    K = shape[-1]
+    need("x", x, shape, x.dtype, x.device)
+    cuda_tensor("w", w, "[N, K] tensor")
     N = w.shape[0]
     if N < 1 or K < 1:
         raise ValueError("w must not be empty")
+    need("w", w, (N, K), x.dtype, x.device)
     return code, x.numel() // K, N, K
 
 
@@ -53,22 +55,26 @@ def hyena_proj_fwd(x, w, bias=None, act="none", residual=None, y=None, z=None, w
     the current stream of x's device).
     """
     torch = torch_()
+    act = _act(act)
     code, M, N, K = _rows(x, w)
-    shape = tuple(x.shape[:-1]) + (N,)
+    shape = x.shape[:-1] + (N,)
     if bias is not None:
         need("bias", bias, (N,), torch.float32, x.device)
-    for name, t in (("residual", residual), ("y", y), ("z", z)):
-        if t is not None:
-            need(name, t, shape, x.dtype, x.device)
+    if residual is not None:
+        need("residual", residual, shape, x.dtype, x.device)
+    if z is not None:
+        need("z", z, shape, x.dtype, x.device)
     with On(x.device, stream) as on:
         if y is None:
             y = torch.empty(shape, dtype=x.dtype, device=x.device)
             on.keep(y)
+        else:
+            need("y", y, shape, x.dtype, x.device)
         size = nbytes("hyena_proj_workspace_bytes", M, N, K, code)
         ws, nws = workspace_of(workspace, size, x.device, on)
         _native.check("hyena_proj_fwd", _native.lib().hyena_proj_fwd(
             x.data_ptr(), w.data_ptr(), ptr(bias), ptr(residual), y.data_ptr(), ptr(z), M, N, K,
-            _act(act), code, ws, nws, on.stream.cuda_stream))
+            act, code, ws, nws, on.handle))
     return y
 
 
@@ -82,7 +88,7 @@ def hyena_proj_bwd(x, w, dy, z=None, act="none", dx_add=None, grads=None, worksp
     """
     torch = torch_()
     code, M, N, K = _rows(x, w)
-    need("dy", dy, tuple(x.shape[:-1]) + (N,), x.dtype, x.device)
+    need("dy", dy, x.shape[:-1] + (N,), x.dtype, x.device)
     if z is not None:
         need("z", z, dy.shape, x.dtype, x.device)
     elif act != "none":
@@ -104,5 +110,5 @@ def hyena_proj_bwd(x, w, dy, z=None, act="none", dx_add=None, grads=None, worksp
         ws, nws = workspace_of(workspace, size, x.device, on)
         _native.check("hyena_proj_bwd", _native.lib().hyena_proj_bwd(
             x.data_ptr(), w.data_ptr(), ptr(z), dy.data_ptr(), ptr(dx_add), ptr(dx), ptr(dw),
-            ptr(db), M, N, K, _act(act), code, ws, nws, on.stream.cuda_stream))
+            ptr(db), M, N, K, _act(act), code, ws, nws, on.handle))
     return dx, dw, db

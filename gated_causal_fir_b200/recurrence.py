@@ -8,28 +8,31 @@ CUDA tensors into pointers, sizes and a stream; outputs and workspaces that are 
 from torch.
 """
 from . import _native
-from ._args import On, code as code_of, nbytes, need, ptr, torch_, workspace as workspace_of
+from ._args import (On, code as code_of, cuda_tensor, nbytes, need, ptr, torch_,
+                    workspace as workspace_of)
 from ._native import HYENA_DTYPE_BF16
 
 
 def _shapes(q, k, v, g, d_g, dims):
-    torch = torch_()
-    if not isinstance(q, torch.Tensor) or not q.is_cuda or q.dim() != len(dims):
-        raise TypeError("q must be a CUDA [%s] tensor" % ", ".join(dims))
+    """The type code of q [*dims, D], k, v like it and g [*dims, D // d_g]."""
+    cuda_tensor("q", q, "[%s] tensor" % dims)
+    shape, dtype, device = q.shape, q.dtype, q.device
+    if len(shape) != len(dims) // 3 + 1:
+        raise TypeError("q must be a CUDA [%s] tensor" % dims)
     code = code_of(q, "q")
-    D = q.shape[-1]
+    D = shape[-1]
     if not isinstance(d_g, int) or d_g < 1 or D < 1 or D % d_g != 0:
         raise ValueError("d_g = %s must divide D = %d" % (d_g, D))
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        need(name, t, q.shape, q.dtype, q.device)
-    need("g", g, tuple(q.shape[:-1]) + (D // d_g,), q.dtype, q.device)
+    need("q", q, shape, dtype, device)
+    need("k", k, shape, dtype, device)
+    need("v", v, shape, dtype, device)
+    need("g", g, shape if d_g == 1 else shape[:-1] + (D // d_g,), dtype, device)
     return code
 
 
 def _state(name, t, q):
-    torch = torch_()
-    return None if t is None else need(name, t, (q.shape[0], q.shape[-1]), torch.float32,
-                                        q.device)
+    if t is not None:
+        need(name, t, (q.shape[0], q.shape[-1]), torch_().float32, q.device)
 
 
 def hyena_scan_workspace_bytes(B, L, D, d_g, dtype=HYENA_DTYPE_BF16):
@@ -67,7 +70,7 @@ def hyena_scan_fwd(q, k, v, g, d_g, s0=None, y=None, s_out=None, ckpt=None, work
     (default: the current stream of q's device).
     """
     torch = torch_()
-    code = _shapes(q, k, v, g, d_g, ("B", "L", "D"))
+    code = _shapes(q, k, v, g, d_g, "B, L, D")
     B, L, D = q.shape
     _state("s0", s0, q)
     _ckpt(ckpt, q, code)
@@ -83,12 +86,13 @@ def hyena_scan_fwd(q, k, v, g, d_g, s0=None, y=None, s_out=None, ckpt=None, work
     else:
         _state("s_out", s_out, q)
     with On(q.device, stream) as on:
-        on.keep(*made)
+        if made:
+            on.keep(*made)
         size = nbytes("hyena_scan_workspace_bytes", B, L, D, d_g, code)
         ws, nws = workspace_of(workspace, size, q.device, on)
         _native.check("hyena_scan_fwd", _native.lib().hyena_scan_fwd(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), ptr(s0), y.data_ptr(),
-            s_out.data_ptr(), ptr(ckpt), B, L, D, d_g, code, ws, nws, on.stream.cuda_stream))
+            s_out.data_ptr(), ptr(ckpt), B, L, D, d_g, code, ws, nws, on.handle))
     return y, s_out
 
 
@@ -101,7 +105,7 @@ def hyena_scan_bwd(q, k, v, g, dy, d_g, s0=None, ds_out=None, ckpt=None, grads=N
     finds the states again.  grads: optional preallocated (dq, dk, dv, dg, ds0), overwritten.
     """
     torch = torch_()
-    code = _shapes(q, k, v, g, d_g, ("B", "L", "D"))
+    code = _shapes(q, k, v, g, d_g, "B, L, D")
     B, L, D = q.shape
     need("dy", dy, q.shape, q.dtype, q.device)
     _state("s0", s0, q)
@@ -127,7 +131,7 @@ def hyena_scan_bwd(q, k, v, g, dy, d_g, s0=None, ds_out=None, ckpt=None, grads=N
         _native.check("hyena_scan_bwd", _native.lib().hyena_scan_bwd(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), ptr(s0), dy.data_ptr(),
             ptr(ds_out), ptr(ckpt), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(),
-            ds0.data_ptr(), B, L, D, d_g, code, ws, nws, on.stream.cuda_stream))
+            ds0.data_ptr(), B, L, D, d_g, code, ws, nws, on.handle))
     return dq, dk, dv, dg, ds0
 
 
@@ -137,7 +141,7 @@ def hyena_scan_step(q, k, v, g, state, d_g, y=None, state_out=None, stream=None)
     q, k, v: CUDA [B, D]; g: [B, D // d_g]; state: fp32 [B, D].  state_out None advances
     ``state`` in place."""
     torch = torch_()
-    code = _shapes(q, k, v, g, d_g, ("B", "D"))
+    code = _shapes(q, k, v, g, d_g, "B, D")
     B, D = q.shape
     if state is None:
         raise ValueError("state must be an fp32 [B, D] tensor")
@@ -154,5 +158,5 @@ def hyena_scan_step(q, k, v, g, state, d_g, y=None, state_out=None, stream=None)
             need("y", y, q.shape, q.dtype, q.device)
         _native.check("hyena_scan_step", _native.lib().hyena_scan_step(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), state.data_ptr(),
-            y.data_ptr(), state_out.data_ptr(), B, D, d_g, code, on.stream.cuda_stream))
+            y.data_ptr(), state_out.data_ptr(), B, D, d_g, code, on.handle))
     return y, state_out

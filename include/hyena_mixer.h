@@ -33,8 +33,9 @@ extern "C" {
  * would otherwise find again by a pass over k, v and g.
  * The state is fp32 throughout; y is rounded once.  Sums have a fixed order: results are the
  * same in every call on one device.
- * Any B, L, D, d_g dividing D and element-aligned pointers; rows that are a multiple of 16 bytes
- * in 16-byte aligned tensors and d_g 1 or even take the fast path (TMA).  L < 2^31 - 4096,
+ * Any B, L, D, d_g dividing D and element-aligned pointers.  Rows that are a multiple of 16 bytes
+ * in 16-byte aligned tensors with d_g 1 or even are fastest (TMA); rows of 8 or 4 bytes come close;
+ * odd D in bf16, or tensors on 2-byte boundaries, are read element by element.  L < 2^31 - 4096,
  * D <= 2^28.
  * workspace: at least hyena_scan_workspace_bytes(B, L, D, d_g, dtype) bytes, 16-byte aligned;
  * NULL where that is 0.
