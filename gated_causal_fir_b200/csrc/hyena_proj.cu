@@ -26,36 +26,41 @@ int planes(int dtype) { return dtype == HYENA_DTYPE_F32 ? 3 : 1; }
 // ------------------------------------------------------------------------------- plan
 enum Shape { kPair256 = 0, kOne128 = 1, kOne64 = 2 };
 
+struct TileShape {
+  int m, n, workers;
+  double block, tail;  // ns per k-block of 64, and per tile outside its k-blocks
+};
+constexpr TileShape kShapes[] = {
+    {256, 256, kSms / 2, 290, 3000}, {128, 128, kSms, 190, 2000}, {128, 64, kSms, 150, 1500}};
+
 struct Plan {
-  int shape, splits, kb, pairs, per;  // per: blocks per split
-  int64_t tiles_m, tiles_n;
+  int shape, splits, kb, pairs, per;  // per: blocks per cut
+  int64_t tiles_m, tiles_n, whole;
 };
 
-// (fp32 sums go on in registers, which hold no more than 128 x 128 outputs.)
-// The tile shape and the number of k cuts with the least estimated time: waves of persistent
-// workers x (k-blocks of one worker's tile x the time of a block + its epilogue), and for cut
-// products a second kernel over the partial sums.
+// The tile shape and the cuts along k with the least estimated time.  Persistent workers take the
+// tiles in waves; those of an unfinished last wave (or, in a small problem, all) are cut so that
+// the workers finish together, at the price of a second kernel over their partial sums.  fp32
+// sums go on in registers, which hold no more than 128 x 128 outputs.
 Plan find_plan(int64_t M, int64_t N, int64_t K, int dtype) {
-  const struct {
-    int tm, tn, workers;
-    double block, tail;  // ns per k-block of 64, per tile
-  } shapes[] = {{256, 256, kSms / 2, 290, 1500}, {128, 128, kSms, 190, 900}, {128, 64, kSms, 150, 600}};
   Plan best{};
   double best_ns = 0;
   const int kb = static_cast<int>((K + pj::kBK - 1) / pj::kBK), pairs = dtype == HYENA_DTYPE_F32 ? 6 : 1;
   const int64_t total = static_cast<int64_t>(kb) * pairs;
   for (int s = dtype == HYENA_DTYPE_F32 ? kOne128 : kPair256; s <= kOne64; ++s) {
-    const int64_t tm = (M + shapes[s].tm - 1) / shapes[s].tm, tn = (N + shapes[s].tn - 1) / shapes[s].tn;
-    for (int want = 1; want <= kMaxSplits; ++want) {
+    const TileShape &t = kShapes[s];
+    const int64_t tm = (M + t.m - 1) / t.m, tn = (N + t.n - 1) / t.n;
+    const int64_t whole = tm * tn / t.workers * t.workers, rest = tm * tn - whole;
+    for (int want = 1; want <= (rest ? kMaxSplits : 1); ++want) {
       const int64_t per = (total + want - 1) / want;
       const int splits = static_cast<int>((total + per - 1) / per);
-      if (splits != want || (want > 1 && (per < 4 || tm * tn * want > 2 * shapes[s].workers))) continue;
-      const int64_t waves = (tm * tn * splits + shapes[s].workers - 1) / shapes[s].workers;
-      double ns = static_cast<double>(waves) * (static_cast<double>(per) * shapes[s].block + shapes[s].tail);
-      if (splits > 1) ns += 2500 + static_cast<double>(splits) * M * N * 8 / 4000;
+      if (splits != want || (want > 1 && (per < 4 || rest * want > t.workers))) continue;
+      double ns = static_cast<double>(whole / t.workers) * (static_cast<double>(total) * t.block) +
+                  (rest ? static_cast<double>(per) * t.block : 0) + t.tail;
+      if (splits > 1) ns += 3000 + static_cast<double>(rest * splits) * std::min<int64_t>(M, t.m) * t.n * 8 / 4000;
       if (best_ns == 0 || ns < best_ns) {
         best_ns = ns;
-        best = Plan{s, splits, kb, pairs, static_cast<int>(per), tm, tn};
+        best = Plan{s, splits, kb, pairs, static_cast<int>(per), tm, tn, splits > 1 ? whole : tm * tn};
       }
     }
   }
@@ -79,8 +84,9 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int dtype) {
 }
 
 int64_t partial_bytes(int64_t M, int64_t N, int64_t K, int dtype) {
-  const int s = plan_of(M, N, K, dtype).splits;
-  return s > 1 ? round_up(s * M * N * 4, 256) : 0;
+  const Plan p = plan_of(M, N, K, dtype);
+  const int64_t cut = (p.tiles_m * p.tiles_n - p.whole) * p.splits;
+  return cut * kShapes[p.shape].m * kShapes[p.shape].n * 4;  // a multiple of 256
 }
 
 // An operand [rows][cols] in memory: `ptr` with rows of `ld` elements, as bf16 planes.
@@ -172,7 +178,8 @@ template <typename T, int kCG, int kBN, bool kAMn, bool kBMn>
 cudaError_t launch_shape(const CUtensorMap &ma, const CUtensorMap &mb, const pj::Params &p,
                          const Device &d, cudaStream_t stream) {
   using L = pj::Tile<kCG, kBN>;
-  const int64_t works = static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.splits;
+  const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
+  const int64_t works = p.whole + (tiles - p.whole) * p.splits;
   const int64_t workers = std::min<int64_t>(works, kCG == 2 ? d.pairs : d.info.sm_count);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -201,6 +208,7 @@ int product(const Operand &a, const Operand &b, int64_t K, pj::Params p, int dty
   p.pairs = pl.pairs;
   p.tiles_m = static_cast<int>(pl.tiles_m);
   p.tiles_n = static_cast<int>(pl.tiles_n);
+  p.whole = static_cast<int>(pl.whole);
   p.splits = pl.splits;
   p.kb_per_split = pl.per;
   p.group_m = pl.shape == kPair256 ? 8 : 16;
@@ -226,10 +234,11 @@ int product(const Operand &a, const Operand &b, int64_t K, pj::Params p, int dty
   }
   if (e != cudaSuccess) return HYENA_ERR_CUDA;
   if (p.splits == 1) return HYENA_OK;
-  const int64_t n = static_cast<int64_t>(p.M) * ((p.N + 3) / 4);
+  const TileShape &t = kShapes[pl.shape];
+  const int64_t n = (pl.tiles_m * pl.tiles_n - pl.whole) * std::min<int64_t>(t.m, p.M) * (t.n / 4);
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>((n + 255) / 256, 8 * d.info.sm_count));
-  return hyena::host::launch(pj::proj_join_kernel<T>, dim3(grid), dim3(256), 0, stream, p) ==
-                 cudaSuccess
+  return hyena::host::launch(pj::proj_join_kernel<T>, dim3(grid), dim3(256), 0, stream, p, t.m,
+                             t.n) == cudaSuccess
              ? HYENA_OK
              : HYENA_ERR_CUDA;
 }

@@ -17,13 +17,14 @@
 // holding 128 rows of A, 128 rows of B and 128 rows of the accumulator.  Each byte staged then
 // feeds 128 products, twice what a single CTA's 128 x 128 tile gives; at the tensor cores' rate the
 // pair draws 64 bytes per SM and cycle from L2, which L2 can serve, where 96 or 128 bytes starve
-// it.  kCG = 1: 128 x kBN by one CTA, for problems with too few 256 x 256 tiles.  Where even those
-// are few, k is cut (splits) and fp32 partial products are summed, in order, by a second kernel.
+// it.  kCG = 1: 128 x kBN by one CTA, for problems with too few 256 x 256 tiles.  The tiles that do
+// not fill a whole wave of workers (all of them, in a small problem) are cut along k, and their
+// fp32 partial products are summed, in order, by a second kernel.
 //
 // Persistent CTAs: warp 0 streams k-blocks of 64 through a ring of shared-memory stages with TMA
 // (128-byte swizzle; zero fill at the ragged edges), warp 1 issues the MMAs into one of two
-// accumulators in tensor memory, warps 2-5 drain the other: through shared memory, so that global
-// rows are read and written in 128-byte pieces.  Bound: the tensor pipe for large products, the
+// accumulators in tensor memory, warps 2-9 drain the other: through shared memory, so that global
+// rows are read and written in whole sectors.  Bound: the tensor pipe for large products, the
 // bytes of w for a few rows.
 #pragma once
 #include <cuda.h>
@@ -38,9 +39,9 @@ namespace proj {
 
 constexpr int kBK = 64;                        // k per stage: one 128-byte swizzled row
 constexpr int kRows = 128;                     // rows of A (and of the accumulator) per CTA
-constexpr int kEpiWarps = 4;
+constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (2 + kEpiWarps);
-constexpr int kChunk = 64;                     // columns an epilogue warp stages at a time
+constexpr int kChunk = 32;                     // columns an epilogue warp stages at a time
 constexpr int kStageOut = 32 * kChunk * 4;     // its staging bytes
 constexpr int kMaxStages = 8;
 constexpr unsigned int kTimeout = 1u;          // HYENA_DEVICE_TIMEOUT
@@ -71,12 +72,14 @@ constexpr int kFlush = 4;
 struct Params {
   int M, N, kb;                 // outputs; k-blocks of one product
   int pairs;                    // 1 (bf16) or 6 (planes of fp32)
-  int tiles_m, tiles_n, splits, kb_per_split;  // splits cut the pairs * kb blocks
+  int tiles_m, tiles_n;
+  int whole;                    // the first tiles, each one work
+  int splits, kb_per_split;     // cuts of the pairs * kb blocks of the other tiles
   int group_m;                  // tiles of m that run together (their w tiles stay in L2)
   const float *bias;            // [N] or null
   const void *residual;         // [M, N] or null
   void *y, *z;                  // [M, N]; z (before the activation) or null
-  float *partial;               // [splits, M, N] when splits > 1
+  float *partial;               // [other tiles][splits][tile] when splits > 1
   int act;
   int vec;                      // rows of y, z, residual are whole, aligned 16-byte vectors
   unsigned int *status;
@@ -263,19 +266,33 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_
 
 // ------------------------------------------------------------------------------- work
 struct Work {
-  int m, n, split, kb0, kb1;  // tile coordinates; blocks [kb0, kb1) of the pairs * kb
+  int m, n, kb0, kb1;  // tile coordinates; blocks [kb0, kb1) of the pairs * kb
+  int part;            // index of its partial product, or -1
 };
-__device__ __forceinline__ Work work_at(const Params &p, int w) {
-  Work k;
-  const int tiles = p.tiles_m * p.tiles_n, t = w % tiles;
-  k.split = w / tiles;
+__device__ __forceinline__ void tile_at(const Params &p, int t, int *m, int *n) {
   const int per = p.group_m * p.tiles_n, g = t / per, r = t % per;
   const int gm = min(p.group_m, p.tiles_m - g * p.group_m);
-  k.m = g * p.group_m + r % gm;
-  k.n = r / gm;
-  const int total = p.pairs * p.kb;
-  k.kb0 = k.split * p.kb_per_split;
-  k.kb1 = min(k.kb0 + p.kb_per_split, total);
+  *m = g * p.group_m + r % gm;
+  *n = r / gm;
+}
+__device__ __forceinline__ int work_count(const Params &p) {
+  return p.whole + (p.tiles_m * p.tiles_n - p.whole) * p.splits;
+}
+__device__ __forceinline__ Work work_at(const Params &p, int w) {
+  Work k;
+  const int total = p.pairs * p.kb, rest = p.tiles_m * p.tiles_n - p.whole;
+  int tile = w;
+  k.kb0 = 0;
+  k.kb1 = total;
+  k.part = -1;
+  if (w >= p.whole && p.splits > 1) {  // a cut of all the other tiles, then the next cut
+    const int r = w - p.whole, split = r / rest;
+    tile = p.whole + r % rest;
+    k.kb0 = split * p.kb_per_split;
+    k.kb1 = min(k.kb0 + p.kb_per_split, total);
+    k.part = (r % rest) * p.splits + split;
+  }
+  tile_at(p, tile, &k.m, &k.n);
   return k;
 }
 
@@ -313,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (kCG == 2) cluster_sync();
   tc_fence_after_sync();
   const uint32_t tmem = tmem_at;
-  const int works = p.tiles_m * p.tiles_n * p.splits;
+  const int works = work_count(p);
   const int first = blockIdx.x / kCG, step = gridDim.x / kCG;
   griddep_launch_dependents();
   griddep_wait();
@@ -407,8 +424,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // --------------------------------------------------------------------------- epilogue
-    const int quad = warp % 4;  // the 32 lanes of tensor memory that this warp may read
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    const int quad = warp % 4;             // the 32 lanes of tensor memory that this warp may read
+    const int col0 = (warp - 2) / 4 * (kBN / 2);  // its half of the columns
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quad * 32) << 16) + col0;
     float *out = reinterpret_cast<float *>(stages + L::kStages * L::kStage + (warp - 2) * kStageOut);
     const auto release = [&](int acc) {  // the accumulator is in registers: the next may start
       tc_fence_before_sync();
@@ -425,10 +443,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int w = first; w < works && ok; w += step) {
       const Work k = work_at(p, w);
       const int row0 = k.m * L::kM + static_cast<int>(rank) * kRows + quad * 32;
-      [[maybe_unused]] float sum[kPromote ? kBN : 1];
+      [[maybe_unused]] float sum[kPromote ? kBN / 2 : 1];
       if constexpr (kPromote) {
 #pragma unroll
-        for (int c = 0; c < kBN; ++c) sum[c] = 0.0f;
+        for (int c = 0; c < kBN / 2; ++c) sum[c] = 0.0f;
         for (int kb = k.kb0; kb < k.kb1 && ok; kb += kFlush, ++n) {
           const int acc = n & 1;
           ok = __all_sync(0xffffffffu,
@@ -436,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after_sync();
 #pragma unroll
-          for (int c0 = 0; c0 < kBN; c0 += 32) {
+          for (int c0 = 0; c0 < kBN / 2; c0 += 32) {
             uint32_t r[32];
             tmem_ld_32x32b_x32(lanes + acc * kBN + c0, r);
             tmem_wait_ld();
@@ -453,16 +471,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       constexpr int V = 16 / static_cast<int>(sizeof(T));
-      const bool wide = p.vec && p.splits == 1;
-#pragma unroll(kPromote ? kBN / kChunk : 1)
-      for (int c0 = 0; c0 < kBN; c0 += kChunk) {
-        // phase 2 of this chunk: lane -> rows 4 i + lane / 8, columns col .. col + 7
-        const int col = k.n * L::kN + c0 + (lane % 8) * 8, sub = lane / 8;
-        VecOf<T, 8> res[8];  // the residual, requested before the accumulator is waited for
+      const bool wide = p.vec && k.part < 0;
+#pragma unroll(kPromote ? kBN / 2 / kChunk : 1)
+      for (int c0 = 0; c0 < kBN / 2; c0 += kChunk) {
+        // phase 2 of this chunk: lane -> rows 8 i + lane / 4, columns col .. col + 7
+        const int in_tile = col0 + c0 + (lane % 4) * 8, col = k.n * L::kN + in_tile;
+        const int sub = lane / 4;
+        VecOf<T, 8> res[4];  // the residual, requested before the accumulator is waited for
         if (wide && p.residual) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int row = row0 + 4 * i + sub;
+          for (int i = 0; i < 4; ++i) {
+            const int row = row0 + 8 * i + sub;
 #pragma unroll
             for (int h = 0; h < 8; h += V)
               if (row < p.M && col + h < p.N)
@@ -474,46 +493,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         float bias[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          bias[e] = p.bias && p.splits == 1 && col + e < p.N ? p.bias[col + e] : 0.0f;
+          bias[e] = p.bias && k.part < 0 && col + e < p.N ? p.bias[col + e] : 0.0f;
         // phase 1: row `lane` into shared memory, in 16-byte pieces swizzled by the row
-        uint32_t r0[32], r1[32];
+        uint32_t r[32];
         if constexpr (kPromote) {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            r0[c] = __float_as_uint(sum[c0 + c]);
-            r1[c] = __float_as_uint(sum[c0 + 32 + c]);
-          }
+          for (int c = 0; c < 32; ++c) r[c] = __float_as_uint(sum[c0 + c]);
         } else {
-          tmem_ld_32x32b_x32(lanes + (n & 1) * kBN + c0, r0);
-          tmem_ld_32x32b_x32(lanes + (n & 1) * kBN + c0 + 32, r1);
+          tmem_ld_32x32b_x32(lanes + (n & 1) * kBN + c0, r);
           tmem_wait_ld();
-          reg_fence(r0);
-          reg_fence(r1);
-          if (c0 + kChunk >= kBN) release(n & 1);
+          reg_fence(r);
+          if (c0 + kChunk >= kBN / 2) release(n & 1);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 8; ++j)
           *reinterpret_cast<uint4 *>(out + lane * kChunk + ((j ^ (lane & 7)) * 4)) =
-              make_uint4(r0[4 * j], r0[4 * j + 1], r0[4 * j + 2], r0[4 * j + 3]);
-          *reinterpret_cast<uint4 *>(out + lane * kChunk + 32 + ((j ^ (lane & 7)) * 4)) =
-              make_uint4(r1[4 * j], r1[4 * j + 1], r1[4 * j + 2], r1[4 * j + 3]);
-        }
+              make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
         __syncwarp();
         const auto staged = [&](int i, float (&c)[8]) {
-          const int r = 4 * i + sub, j = 2 * (lane % 8);
-          const float *src = out + r * kChunk + (j & 8) * 4;
-          const float4 u = *reinterpret_cast<const float4 *>(src + (((j & 7) ^ (r & 7)) * 4));
-          const float4 v = *reinterpret_cast<const float4 *>(src + ((((j & 7) + 1) ^ (r & 7)) * 4));
+          const int rr = 8 * i + sub, j = 2 * (lane % 4);
+          const float *src = out + rr * kChunk;
+          const float4 u = *reinterpret_cast<const float4 *>(src + ((j ^ (rr & 7)) * 4));
+          const float4 v = *reinterpret_cast<const float4 *>(src + (((j + 1) ^ (rr & 7)) * 4));
           c[0] = u.x + bias[0], c[1] = u.y + bias[1], c[2] = u.z + bias[2], c[3] = u.w + bias[3];
           c[4] = v.x + bias[4], c[5] = v.y + bias[5], c[6] = v.z + bias[6], c[7] = v.w + bias[7];
         };
         if (wide) {
           with_act(p.act, [&](auto act) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 4; ++i) {
               float c[8];
               staged(i, c);
-              const int row = row0 + 4 * i + sub;
+              const int row = row0 + 8 * i + sub;
               if (row >= p.M) continue;
               const int64_t at = static_cast<int64_t>(row) * p.N + col;
 #pragma unroll
@@ -537,26 +548,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           });
         } else {
 #pragma unroll 1
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < 4; ++i) {
             float c[8];
             staged(i, c);
-            const int64_t row = row0 + 4 * i + sub;
+            const int64_t row = row0 + 8 * i + sub;
             if (row >= p.M || col >= p.N) continue;
-            if (p.splits == 1) {
+            if (k.part < 0) {
               finish<T, 8>(p, c, row, col);
-              continue;
-            }
-            float *to = p.partial + (static_cast<int64_t>(k.split) * p.M + row) * p.N + col;
-            if (p.N % 4 == 0) {
-#pragma unroll
-              for (int h = 0; h < 8; h += 4)
-                if (col + h < p.N)
-                  *reinterpret_cast<float4 *>(to + h) =
-                      make_float4(c[h], c[h + 1], c[h + 2], c[h + 3]);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (col + e < p.N) to[e] = c[e];
+            } else {  // whole tiles of fp32: no care at the ragged edge
+              const int in_row = static_cast<int>(rank) * kRows + quad * 32 + 8 * i + sub;
+              float4 *to = reinterpret_cast<float4 *>(
+                  p.partial + (static_cast<int64_t>(k.part) * L::kM + in_row) * kBN + in_tile);
+              to[0] = make_float4(c[0], c[1], c[2], c[3]);
+              to[1] = make_float4(c[4], c[5], c[6], c[7]);
             }
           }
         }
@@ -576,31 +580,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The sum of a product's k cuts, in order, and its epilogue: four columns per thread.
+// The sums of the cut tiles' partial products, in order, and their epilogue: four columns of a row
+// per thread, rows of tile_m x tile_n tiles.
 template <typename T>
-__global__ void __launch_bounds__(256) proj_join_kernel(const Params p) {
+__global__ void __launch_bounds__(256) proj_join_kernel(const Params p, int tile_m, int tile_n) {
   griddep_launch_dependents();
   griddep_wait();
-  const int per_row = (p.N + 3) / 4;
-  const int64_t n = static_cast<int64_t>(p.M) * per_row;
+  // rows of a tile that can be in range at all: a product of few rows fills little of its tiles
+  const int rows = min(tile_m, p.M), per_tile = rows * (tile_n / 4);
+  const int64_t n = static_cast<int64_t>(p.tiles_m * p.tiles_n - p.whole) * per_tile;
   const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) {
-    const int64_t row = i / per_row;
-    const int col = static_cast<int>(i - row * per_row) * 4;
+    const int tile = static_cast<int>(i / per_tile), r = static_cast<int>(i % per_tile);
+    int tm, tn;
+    tile_at(p, p.whole + tile, &tm, &tn);
+    const int in_row = r / (tile_n / 4), in_col = r % (tile_n / 4) * 4;
+    const int64_t row = static_cast<int64_t>(tm) * tile_m + in_row;
+    const int col = tn * tile_n + in_col;
+    if (row >= p.M || col >= p.N) continue;
+    const int64_t size = static_cast<int64_t>(tile_m) * tile_n;
+    const float *from = p.partial + (static_cast<int64_t>(tile) * p.splits) * size + in_row * tile_n + in_col;
     float c[4] = {0.f, 0.f, 0.f, 0.f};
-    const float *from = p.partial + row * p.N + col;
-    for (int s = 0; s < p.splits; ++s, from += static_cast<int64_t>(p.M) * p.N) {
-      if (p.N % 4 == 0) {
-        const float4 v = *reinterpret_cast<const float4 *>(from);
-        c[0] += v.x;
-        c[1] += v.y;
-        c[2] += v.z;
-        c[3] += v.w;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (col + e < p.N) c[e] += from[e];
-      }
+#pragma unroll 4
+    for (int s = 0; s < p.splits; ++s) {
+      const float4 v = *reinterpret_cast<const float4 *>(from + s * size);
+      c[0] += v.x;
+      c[1] += v.y;
+      c[2] += v.z;
+      c[3] += v.w;
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) c[e] += p.bias && col + e < p.N ? p.bias[col + e] : 0.0f;
