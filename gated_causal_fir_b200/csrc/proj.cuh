@@ -210,18 +210,26 @@ __device__ __forceinline__ void load_tile(uint8_t *dst, const CUtensorMap *map, 
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(plane)
         : "memory");
 }
+// One MMA; the descriptors' low words (addresses) change from one to the next, the high do not.
 template <int kCG>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                    uint32_t accumulate) {
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                    uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
   if constexpr (kCG == 2)
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b),
-        "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
         : "memory");
   else
-    umma_f16(d, a, b, idesc, accumulate);
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 // Arrives on `bar` (of every CTA of the group) when the MMAs issued so far are done.
 template <int kCG>
@@ -338,34 +346,50 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------------------------------------------------- TMA
-      int it = 0;
+      // (This thread and the MMA thread run one iteration per k-block of ~300 ns: stages, phases
+      // and planes are counted along, without divisions.)
+      int it = 0, st = 0;
+      uint32_t freed = 1;  // parity of the stage's last release; the first round waits for none
       bool ok = true;
+      const uint32_t full0 = kCG == 2 ? in_cta(&full[0], 0) : smem_u32(&full[0]);
       for (int w = first; w < works && ok; w += step) {
         const Work k = work_at(p, w);
         const int m0 = k.m * L::kM + static_cast<int>(rank) * kRows;
         const int n0 = k.n * L::kN + static_cast<int>(rank) * L::kBRows;
+        int pair = k.kb0 / p.kb, k0 = (k.kb0 - pair * p.kb) * kBK;
+        int pa = p.pairs > 1 ? kPlaneA[pair] : 0, pb = p.pairs > 1 ? kPlaneB[pair] : 0;
         for (int kb = k.kb0; kb < k.kb1; ++kb, ++it) {
-          const int st = it % L::kStages, round = it / L::kStages;
-          if (round > 0 && !mbar_wait(&empty[st], (round - 1) & 1, &abort, p.status, kTimeout)) {
+          if (it >= L::kStages && !mbar_wait(&empty[st], freed, &abort, p.status, kTimeout)) {
             ok = false;
             break;
           }
-          const int pair = kb / p.kb, k0 = (kb - pair * p.kb) * kBK;
-          const int pa = p.pairs > 1 ? kPlaneA[pair] : 0, pb = p.pairs > 1 ? kPlaneB[pair] : 0;
           uint8_t *a = stages + st * L::kStage, *b = a + L::kABytes;
           if (rank == 0) mbar_arrive_expect_tx(&full[st], kCG * L::kStage);
-          const uint32_t bar = kCG == 2 ? in_cta(&full[st], 0) : smem_u32(&full[st]);
+          const uint32_t bar = full0 + 8 * st;
           if (kAMn) {
+#pragma unroll
             for (int h = 0; h < kRows / 64; ++h)
               load_tile<kCG>(a + h * 8192, &ma, bar, m0 + h * 64, k0, pa);
           } else {
             load_tile<kCG>(a, &ma, bar, k0, m0, pa);
           }
           if (kBMn) {
+#pragma unroll
             for (int h = 0; h < L::kBRows / 64; ++h)
               load_tile<kCG>(b + h * 8192, &mb, bar, n0 + h * 64, k0, pb);
           } else {
             load_tile<kCG>(b, &mb, bar, k0, n0, pb);
+          }
+          if (++st == L::kStages) {
+            st = 0;
+            freed ^= 1;
+          }
+          k0 += kBK;
+          if (k0 >= p.kb * kBK && kb + 1 < k.kb1) {  // the next pair of planes
+            k0 = 0;
+            ++pair;
+            pa = kPlaneA[pair];
+            pb = kPlaneB[pair];
           }
         }
       }
@@ -383,7 +407,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------------------- MMA
       constexpr uint32_t id = idesc_bf16(L::kM, L::kN, kAMn, kBMn);
       constexpr uint32_t kStepA = (kAMn ? 16 * 128 : 32) >> 4, kStepB = (kBMn ? 16 * 128 : 32) >> 4;
-      int it = 0, n = 0;  // k-blocks; accumulators filled
+      const uint32_t s0 = smem_u32(stages);
+      const uint64_t da0 = umma_smem_desc(s0, kAMn ? 8192 : 16, 1024, 2);
+      const uint64_t db0 = umma_smem_desc(s0 + L::kABytes, kBMn ? 8192 : 16, 1024, 2);
+      const uint32_t a_hi = static_cast<uint32_t>(da0 >> 32), b_hi = static_cast<uint32_t>(db0 >> 32);
+      uint32_t a_lo = static_cast<uint32_t>(da0), b_lo = static_cast<uint32_t>(db0);
+      int it = 0, n = 0, st = 0;  // k-blocks; accumulators filled; stage
+      uint32_t filled = 0;        // parity of the stage's next fill
       bool ok = true;
       for (int w = first; w < works && ok; w += step) {
         const Work k = work_at(p, w);
@@ -396,21 +426,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after_sync();
           const uint32_t d = tmem + acc * kBN;
           for (uint32_t more = 0; kb < end; ++kb, ++it) {
-            const int st = it % L::kStages;
-            if (!mbar_wait(&full[st], (it / L::kStages) & 1, &abort, p.status, kTimeout)) {
+            if (!mbar_wait(&full[st], filled, &abort, p.status, kTimeout)) {
               ok = false;
               break;
             }
             tc_fence_after_sync();
-            const uint32_t a = smem_u32(stages + st * L::kStage), b = a + L::kABytes;
-            const uint64_t da = umma_smem_desc(a, kAMn ? 8192 : 16, 1024, 2);
-            const uint64_t db = umma_smem_desc(b, kBMn ? 8192 : 16, 1024, 2);
 #pragma unroll
-            for (int s = 0; s < kBK / 16; ++s) {
-              mma<kCG>(d, da + s * kStepA, db + s * kStepB, id, more);
-              more = 1;
-            }
+            for (int s = 0; s < kBK / 16; ++s)
+              mma<kCG>(d, a_lo + s * kStepA, a_hi, b_lo + s * kStepB, b_hi, id, s > 0 ? 1u : more);
+            more = 1;
             commit<kCG>(&empty[st]);
+            a_lo += L::kStage >> 4;
+            b_lo += L::kStage >> 4;
+            if (++st == L::kStages) {
+              st = 0;
+              filled ^= 1;
+              a_lo = static_cast<uint32_t>(da0);
+              b_lo = static_cast<uint32_t>(db0);
+            }
           }
           if (ok) commit<kCG>(&acc_full[acc]);
         }
