@@ -184,6 +184,13 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
+// One lane of the (whole) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(p));
+  return p != 0;
+}
 // The address of this CTA's shared variable in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t in_cta(const void *p, uint32_t rank) {
   uint32_t a;
@@ -318,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t tmem_at;
   __shared__ int abort;
   uint8_t *stages = dynamic + (1024 - smem_u32(dynamic) % 1024) % 1024;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const uint32_t rank = kCG == 2 ? cluster_rank() : 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::kStages; ++i) {
@@ -343,29 +350,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
   griddep_wait();
 
+  // A wait of the whole warp, with one answer for all of it.
+  const auto wait = [&](uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, &abort, p.status, kTimeout)) != 0;
+  };
+  // The TMA and MMA warps run their loops as a whole and only the instruction itself in one lane:
+  // descriptors and coordinates then stay in uniform registers.  With the loops inside one lane,
+  // moving every operand there took 0.3 us per k-block (a cuBLAS block: 0.08).
   if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------------------------- TMA
-      // (This thread and the MMA thread run one iteration per k-block of ~300 ns: stages, phases
-      // and planes are counted along, without divisions.)
-      int it = 0, st = 0;
-      uint32_t freed = 1;  // parity of the stage's last release; the first round waits for none
-      bool ok = true;
-      const uint32_t full0 = kCG == 2 ? in_cta(&full[0], 0) : smem_u32(&full[0]);
-      for (int w = first; w < works && ok; w += step) {
-        const Work k = work_at(p, w);
-        const int m0 = k.m * L::kM + static_cast<int>(rank) * kRows;
-        const int n0 = k.n * L::kN + static_cast<int>(rank) * L::kBRows;
-        int pair = k.kb0 / p.kb, k0 = (k.kb0 - pair * p.kb) * kBK;
-        int pa = p.pairs > 1 ? kPlaneA[pair] : 0, pb = p.pairs > 1 ? kPlaneB[pair] : 0;
-        for (int kb = k.kb0; kb < k.kb1; ++kb, ++it) {
-          if (it >= L::kStages && !mbar_wait(&empty[st], freed, &abort, p.status, kTimeout)) {
-            ok = false;
-            break;
-          }
-          uint8_t *a = stages + st * L::kStage, *b = a + L::kABytes;
+    // --------------------------------------------------------------------------- TMA
+    const bool lead = elect_one();
+    int it = 0, st = 0;
+    uint32_t freed = 1;  // parity of the stage's last release; the first round waits for none
+    bool ok = true;
+    const uint32_t full0 = kCG == 2 ? in_cta(&full[0], 0) : smem_u32(&full[0]);
+    for (int w = first; w < works && ok; w += step) {
+      const Work k = work_at(p, w);
+      const int m0 = k.m * L::kM + static_cast<int>(rank) * kRows;
+      const int n0 = k.n * L::kN + static_cast<int>(rank) * L::kBRows;
+      int pair = k.kb0 / p.kb, k0 = (k.kb0 - pair * p.kb) * kBK;
+      int pa = p.pairs > 1 ? kPlaneA[pair] : 0, pb = p.pairs > 1 ? kPlaneB[pair] : 0;
+      for (int kb = k.kb0; kb < k.kb1; ++kb, ++it) {
+        if (it >= L::kStages && !wait(&empty[st], freed)) {
+          ok = false;
+          break;
+        }
+        uint8_t *a = stages + st * L::kStage, *b = a + L::kABytes;
+        const uint32_t bar = full0 + 8 * st;
+        if (lead) {
           if (rank == 0) mbar_arrive_expect_tx(&full[st], kCG * L::kStage);
-          const uint32_t bar = full0 + 8 * st;
           if (kAMn) {
 #pragma unroll
             for (int h = 0; h < kRows / 64; ++h)
@@ -380,33 +393,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             load_tile<kCG>(b, &mb, bar, k0, n0, pb);
           }
-          if (++st == L::kStages) {
-            st = 0;
-            freed ^= 1;
-          }
-          k0 += kBK;
-          if (k0 >= p.kb * kBK && kb + 1 < k.kb1) {  // the next pair of planes
-            k0 = 0;
-            ++pair;
-            pa = kPlaneA[pair];
-            pb = kPlaneB[pair];
-          }
+        }
+        if (++st == L::kStages) {
+          st = 0;
+          freed ^= 1;
+        }
+        k0 += kBK;
+        if (k0 >= p.kb * kBK && kb + 1 < k.kb1) {  // the next pair of planes
+          k0 = 0;
+          ++pair;
+          pa = kPlaneA[pair];
+          pb = kPlaneB[pair];
         }
       }
-      // Before the CTA ends every copy has landed and every release of a stage has arrived.  In
-      // the leader `full` covers both CTAs' copies.
-      for (int j = it > L::kStages ? it - L::kStages : 0; j < it; ++j) {
-        const int st = j % L::kStages, parity = (j / L::kStages) & 1;
-        int no_abort = 0;
-        if (!mbar_wait(&empty[st], parity, &abort, p.status, kTimeout) && rank == 0)
-          mbar_wait(&full[st], parity, &no_abort, p.status, kTimeout);
-      }
+    }
+    // Before the CTA ends every copy has landed and every release of a stage has arrived.  In
+    // the leader `full` covers both CTAs' copies.
+    for (int j = it > L::kStages ? it - L::kStages : 0; j < it; ++j) {
+      const int s = j % L::kStages, parity = (j / L::kStages) & 1;
+      int no_abort = 0;
+      if (!wait(&empty[s], parity) && rank == 0)
+        mbar_wait(&full[s], parity, &no_abort, p.status, kTimeout);
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       // ------------------------------------------------------------------------- MMA
       constexpr uint32_t id = idesc_bf16(L::kM, L::kN, kAMn, kBMn);
       constexpr uint32_t kStepA = (kAMn ? 16 * 128 : 32) >> 4, kStepB = (kBMn ? 16 * 128 : 32) >> 4;
+      const bool lead = elect_one();
       const uint32_t s0 = smem_u32(stages);
       const uint64_t da0 = umma_smem_desc(s0, kAMn ? 8192 : 16, 1024, 2);
       const uint64_t db0 = umma_smem_desc(s0 + L::kABytes, kBMn ? 8192 : 16, 1024, 2);
@@ -419,23 +433,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Work k = work_at(p, w);
         for (int kb = k.kb0; kb < k.kb1 && ok; ++n) {
           const int acc = n & 1, end = kPromote ? min(kb + kFlush, k.kb1) : k.kb1;
-          if (n >= 2 && !mbar_wait(&acc_empty[acc], (n / 2 - 1) & 1, &abort, p.status, kTimeout)) {
+          if (n >= 2 && !wait(&acc_empty[acc], (n / 2 - 1) & 1)) {
             ok = false;
             break;
           }
           tc_fence_after_sync();
           const uint32_t d = tmem + acc * kBN;
           for (uint32_t more = 0; kb < end; ++kb, ++it) {
-            if (!mbar_wait(&full[st], filled, &abort, p.status, kTimeout)) {
+            if (!wait(&full[st], filled)) {
               ok = false;
               break;
             }
             tc_fence_after_sync();
+            if (lead) {
 #pragma unroll
-            for (int s = 0; s < kBK / 16; ++s)
-              mma<kCG>(d, a_lo + s * kStepA, a_hi, b_lo + s * kStepB, b_hi, id, s > 0 ? 1u : more);
+              for (int s = 0; s < kBK / 16; ++s)
+                mma<kCG>(d, a_lo + s * kStepA, a_hi, b_lo + s * kStepB, b_hi, id, s > 0 ? 1u : more);
+              commit<kCG>(&empty[st]);
+            }
             more = 1;
-            commit<kCG>(&empty[st]);
             a_lo += L::kStage >> 4;
             b_lo += L::kStage >> 4;
             if (++st == L::kStages) {
@@ -445,7 +461,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               b_lo = static_cast<uint32_t>(db0);
             }
           }
-          if (ok) commit<kCG>(&acc_full[acc]);
+          if (ok && lead) commit<kCG>(&acc_full[acc]);
+          __syncwarp();
         }
       }
       // MMAs still reading shared memory when a wait gave up: let them finish
@@ -482,8 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < kBN / 2; ++c) sum[c] = 0.0f;
         for (int kb = k.kb0; kb < k.kb1 && ok; kb += kFlush, ++n) {
           const int acc = n & 1;
-          ok = __all_sync(0xffffffffu,
-                          mbar_wait(&acc_full[acc], (n / 2) & 1, &abort, p.status, kTimeout));
+          ok = wait(&acc_full[acc], (n / 2) & 1);
           if (!ok) break;
           tc_fence_after_sync();
 #pragma unroll
@@ -498,8 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           release(acc);
         }
       } else {
-        ok = __all_sync(0xffffffffu,
-                        mbar_wait(&acc_full[n & 1], (n / 2) & 1, &abort, p.status, kTimeout));
+        ok = wait(&acc_full[n & 1], (n / 2) & 1);
         tc_fence_after_sync();
       }
       if (!ok) break;
