@@ -30,8 +30,8 @@ struct TileShape {
   int m, n, workers;
   double block, tail;  // ns per k-block of 64, and per tile outside its k-blocks
 };
-constexpr TileShape kShapes[] = {
-    {256, 256, kSms / 2, 290, 3000}, {128, 128, kSms, 190, 2000}, {128, 64, kSms, 150, 1500}};
+constexpr TileShape kShapes[] = {  // times measured on products of 16..8192 rows and columns
+    {256, 256, kSms / 2, 340, 5000}, {128, 128, kSms, 230, 3200}, {128, 64, kSms, 185, 2600}};
 
 struct Plan {
   int shape, splits, kb, pairs, per;  // per: blocks per cut
@@ -57,7 +57,8 @@ Plan find_plan(int64_t M, int64_t N, int64_t K, int dtype) {
       if (splits != want || (want > 1 && (per < 4 || rest * want > t.workers))) continue;
       double ns = static_cast<double>(whole / t.workers) * (static_cast<double>(total) * t.block) +
                   (rest ? static_cast<double>(per) * t.block : 0) + t.tail;
-      if (splits > 1) ns += 3000 + static_cast<double>(rest * splits) * std::min<int64_t>(M, t.m) * t.n * 8 / 4000;
+      if (splits > 1)  // the second kernel, and the partial sums' way to it and back
+        ns += 3000 + static_cast<double>(rest * splits) * std::min<int64_t>(M, t.m) * t.n * 4 / 4500;
       if (best_ns == 0 || ns < best_ns) {
         best_ns = ns;
         best = Plan{s, splits, kb, pairs, static_cast<int>(per), tm, tn, splits > 1 ? whole : tm * tn};
