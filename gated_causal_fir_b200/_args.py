@@ -10,6 +10,7 @@ from ._native import HYENA_DTYPE_BF16, HYENA_DTYPE_F32
 
 _TORCH = None
 _CODES = {}
+_FUNCTIONS = {}
 
 
 def torch_():
@@ -56,46 +57,46 @@ def ptr(t):
     return None if t is None else t.data_ptr()
 
 
-class On:
-    """The launch context of a call: the tensors' device made current, and the stream (by default
-    that device's current one).  ``keep`` marks buffers made here as in use on a given stream."""
-    __slots__ = ("given", "handle", "guard")
-
-    def __init__(self, device, stream):
-        torch = torch_()
-        self.given = stream
-        self.handle = (torch._C._cuda_getCurrentRawStream(device.index) if stream is None
-                       else stream.cuda_stream)
-        self.guard = (None if device.index == torch._C._cuda_getDevice()
-                      else torch.cuda.device(device))
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-    def keep(self, *tensors):
-        if self.given is not None:
-            for t in tensors:
-                t.record_stream(self.given)
+def stream_handle(device, stream):
+    """The raw handle of ``stream``, by default the current one of ``device``."""
+    return (torch_()._C._cuda_getCurrentRawStream(device.index) if stream is None
+            else stream.cuda_stream)
 
 
-def workspace(given, size, device, on):
-    """(pointer, bytes) of the workspace: the caller's, or one made here; (None, 0) for none."""
+def keep(stream, *tensors):
+    """Marks buffers made for a call as in use on the stream that the caller gave."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
+def run(name, device, *args):
+    """Calls a function of the library with the tensors' device current; raises on an error."""
+    torch = torch_()
+    fn = _FUNCTIONS.get(name)
+    if fn is None:
+        fn = _FUNCTIONS[name] = getattr(_native.lib(), name)
+    if device.index == torch._C._cuda_getDevice():
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args)
+    if rc:
+        _native.check(name, rc)
+
+
+def workspace(given, size, device, stream):
+    """(pointer, bytes, buffer) of the workspace: the caller's, or one made here; none for 0."""
     if given is None:
         if size == 0:
-            return None, 0
+            return None, 0, None
         ws = torch_().empty(size, dtype=torch_().uint8, device=device)
-        on.keep(ws)
-        return ws.data_ptr(), size
+        keep(stream, ws)
+        return ws.data_ptr(), size, ws
     if not isinstance(given, torch_().Tensor) or given.device != device \
             or not given.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on the inputs' device")
-    return given.data_ptr(), given.numel() * given.element_size()
+    return given.data_ptr(), given.numel() * given.element_size(), given
 
 
 @functools.lru_cache(maxsize=4096)

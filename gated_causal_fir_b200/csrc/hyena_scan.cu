@@ -44,14 +44,19 @@ int check_shape(const Shape &s) {
   return HYENA_OK;
 }
 
-// Cuts of the time axis.  A CTA streams ~50 GB/s at best, so fewer than ~100 columns of 32
-// channels leave HBM idle; every cut but one costs a second read of k, v and g, and a launch.
-// Each keeps at least two tiles.
+// Cuts of the time axis.  A CTA streams ~50 GB/s at best (a tile in ~0.8 us), so fewer than ~100
+// columns of 32 channels leave HBM idle; but every cut except one costs a second read of k, v and
+// g, and all of them a launch.  Cut where that saves at least 6 us.
 int64_t split_count(const Shape &s) {
   constexpr int64_t kCtas = 148;
-  const int64_t blocks = s.B * s.n_cb();
+  constexpr double kTileUs = 0.8, kAggregateUs = 0.5, kLaunchUs = 6.0;
+  const int64_t blocks = s.B * s.n_cb(), tiles = s.n_tiles();
   if (blocks * 2 > kCtas) return 1;
-  return std::max<int64_t>(1, std::min(kCtas / blocks, s.n_tiles() / 2));
+  const int64_t n = std::min(kCtas / blocks, tiles / 2);
+  if (n < 2) return 1;
+  const double whole = static_cast<double>(tiles) * kTileUs;
+  const double cut = static_cast<double>(tiles) / static_cast<double>(n) * (kTileUs + kAggregateUs);
+  return cut + kLaunchUs < whole ? n : 1;
 }
 
 // What `blocks` CTAs' worth of cuts leaves after rounding to whole tiles per cut.

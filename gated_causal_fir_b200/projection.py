@@ -6,9 +6,8 @@ x: CUDA [..., K], w: [N, K], all bf16 or all fp32; bias fp32 [N].  The functions
 CUDA tensors into pointers, sizes and a stream; outputs and workspaces that are not given come
 from torch.
 """
-from . import _native
-from ._args import (On, code as code_of, cuda_tensor, nbytes, need, ptr, torch_,
-                    workspace as workspace_of)
+from ._args import (code as code_of, cuda_tensor, keep, nbytes, need, ptr, run, stream_handle,
+                    torch_, workspace as workspace_of)
 from ._native import ACT_CODES, HYENA_DTYPE_BF16
 
 
@@ -64,17 +63,15 @@ def hyena_proj_fwd(x, w, bias=None, act="none", residual=None, y=None, z=None, w
         need("residual", residual, shape, x.dtype, x.device)
     if z is not None:
         need("z", z, shape, x.dtype, x.device)
-    with On(x.device, stream) as on:
-        if y is None:
-            y = torch.empty(shape, dtype=x.dtype, device=x.device)
-            on.keep(y)
-        else:
-            need("y", y, shape, x.dtype, x.device)
-        size = nbytes("hyena_proj_workspace_bytes", M, N, K, code)
-        ws, nws = workspace_of(workspace, size, x.device, on)
-        _native.check("hyena_proj_fwd", _native.lib().hyena_proj_fwd(
-            x.data_ptr(), w.data_ptr(), ptr(bias), ptr(residual), y.data_ptr(), ptr(z), M, N, K,
-            act, code, ws, nws, on.handle))
+    if y is None:
+        y = x.new_empty(shape)
+        keep(stream, y)
+    else:
+        need("y", y, shape, x.dtype, x.device)
+    size = nbytes("hyena_proj_workspace_bytes", M, N, K, code)
+    ws, nws, _buf = workspace_of(workspace, size, x.device, stream)
+    run("hyena_proj_fwd", x.device, x.data_ptr(), w.data_ptr(), ptr(bias), ptr(residual),
+        y.data_ptr(), ptr(z), M, N, K, act, code, ws, nws, stream_handle(x.device, stream))
     return y
 
 
@@ -88,6 +85,8 @@ def hyena_proj_bwd(x, w, dy, z=None, act="none", dx_add=None, grads=None, worksp
     """
     torch = torch_()
     code, M, N, K = _rows(x, w)
+    if act not in ACT_CODES:
+        _act(act)
     need("dy", dy, x.shape[:-1] + (N,), x.dtype, x.device)
     if z is not None:
         need("z", z, dy.shape, x.dtype, x.device)
@@ -104,11 +103,11 @@ def hyena_proj_bwd(x, w, dy, z=None, act="none", dx_add=None, grads=None, worksp
                               ("db", db, (N,), torch.float32)):
         if t is not None:
             need(name, t, like, dt, x.device)
-    with On(x.device, stream) as on:
-        on.keep(*made)
-        size = nbytes("hyena_proj_bwd_workspace_bytes", M, N, K, _act(act), code)
-        ws, nws = workspace_of(workspace, size, x.device, on)
-        _native.check("hyena_proj_bwd", _native.lib().hyena_proj_bwd(
-            x.data_ptr(), w.data_ptr(), ptr(z), dy.data_ptr(), ptr(dx_add), ptr(dx), ptr(dw),
-            ptr(db), M, N, K, _act(act), code, ws, nws, on.handle))
+    keep(stream, *made)
+    act = _act(act)
+    size = nbytes("hyena_proj_bwd_workspace_bytes", M, N, K, act, code)
+    ws, nws, _buf = workspace_of(workspace, size, x.device, stream)
+    run("hyena_proj_bwd", x.device, x.data_ptr(), w.data_ptr(), ptr(z), dy.data_ptr(),
+        ptr(dx_add), ptr(dx), ptr(dw), ptr(db), M, N, K, act, code, ws, nws,
+        stream_handle(x.device, stream))
     return dx, dw, db

@@ -7,9 +7,8 @@ gates of the FIR operator around a state that the data lets decay.  The function
 CUDA tensors into pointers, sizes and a stream; outputs and workspaces that are not given come
 from torch.
 """
-from . import _native
-from ._args import (On, code as code_of, cuda_tensor, nbytes, need, ptr, torch_,
-                    workspace as workspace_of)
+from ._args import (code as code_of, cuda_tensor, keep, nbytes, need, ptr, run, stream_handle,
+                    torch_, workspace as workspace_of)
 from ._native import HYENA_DTYPE_BF16
 
 
@@ -69,30 +68,26 @@ def hyena_scan_fwd(q, k, v, g, d_g, s0=None, y=None, s_out=None, ckpt=None, work
     tensor of hyena_scan_ckpt(q), filled for hyena_scan_bwd.  Runs asynchronously on ``stream``
     (default: the current stream of q's device).
     """
-    torch = torch_()
     code = _shapes(q, k, v, g, d_g, "B, L, D")
     B, L, D = q.shape
+    device = q.device
     _state("s0", s0, q)
     _ckpt(ckpt, q, code)
-    made = []
     if y is None:
-        y = torch.empty_like(q)
-        made.append(y)
+        y = torch_().empty_like(q)
+        keep(stream, y)
     else:
-        need("y", y, q.shape, q.dtype, q.device)
+        need("y", y, q.shape, q.dtype, device)
     if s_out is None:
-        s_out = torch.empty((B, D), dtype=torch.float32, device=q.device)
-        made.append(s_out)
+        s_out = torch_().empty((B, D), dtype=torch_().float32, device=device)
+        keep(stream, s_out)
     else:
         _state("s_out", s_out, q)
-    with On(q.device, stream) as on:
-        if made:
-            on.keep(*made)
-        size = nbytes("hyena_scan_workspace_bytes", B, L, D, d_g, code)
-        ws, nws = workspace_of(workspace, size, q.device, on)
-        _native.check("hyena_scan_fwd", _native.lib().hyena_scan_fwd(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), ptr(s0), y.data_ptr(),
-            s_out.data_ptr(), ptr(ckpt), B, L, D, d_g, code, ws, nws, on.handle))
+    size = nbytes("hyena_scan_workspace_bytes", B, L, D, d_g, code)
+    ws, nws, _buf = workspace_of(workspace, size, device, stream)
+    run("hyena_scan_fwd", device, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), ptr(s0),
+        y.data_ptr(), s_out.data_ptr(), ptr(ckpt), B, L, D, d_g, code, ws, nws,
+        stream_handle(device, stream))
     return y, s_out
 
 
@@ -124,14 +119,13 @@ def hyena_scan_bwd(q, k, v, g, dy, d_g, s0=None, ds_out=None, ckpt=None, grads=N
         if ds0 is None:
             raise ValueError("ds0 must be an fp32 [B, D] tensor")
         _state("ds0", ds0, q)
-    with On(q.device, stream) as on:
-        on.keep(*made)
-        size = nbytes("hyena_scan_bwd_workspace_bytes", B, L, D, d_g, code, int(ckpt is not None))
-        ws, nws = workspace_of(workspace, size, q.device, on)
-        _native.check("hyena_scan_bwd", _native.lib().hyena_scan_bwd(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), ptr(s0), dy.data_ptr(),
-            ptr(ds_out), ptr(ckpt), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dg.data_ptr(),
-            ds0.data_ptr(), B, L, D, d_g, code, ws, nws, on.handle))
+    size = nbytes("hyena_scan_bwd_workspace_bytes", B, L, D, d_g, code, int(ckpt is not None))
+    ws, nws, _buf = workspace_of(workspace, size, q.device, stream)
+    keep(stream, *made)
+    run("hyena_scan_bwd", q.device, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+        ptr(s0), dy.data_ptr(), ptr(ds_out), ptr(ckpt), dq.data_ptr(), dk.data_ptr(),
+        dv.data_ptr(), dg.data_ptr(), ds0.data_ptr(), B, L, D, d_g, code, ws, nws,
+        stream_handle(q.device, stream))
     return dq, dk, dv, dg, ds0
 
 
@@ -140,7 +134,6 @@ def hyena_scan_step(q, k, v, g, state, d_g, y=None, state_out=None, stream=None)
 
     q, k, v: CUDA [B, D]; g: [B, D // d_g]; state: fp32 [B, D].  state_out None advances
     ``state`` in place."""
-    torch = torch_()
     code = _shapes(q, k, v, g, d_g, "B, D")
     B, D = q.shape
     if state is None:
@@ -150,13 +143,12 @@ def hyena_scan_step(q, k, v, g, state, d_g, y=None, state_out=None, stream=None)
         state_out = state
     else:
         _state("state_out", state_out, q)
-    with On(q.device, stream) as on:
-        if y is None:
-            y = torch.empty_like(q)
-            on.keep(y)
-        else:
-            need("y", y, q.shape, q.dtype, q.device)
-        _native.check("hyena_scan_step", _native.lib().hyena_scan_step(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), state.data_ptr(),
-            y.data_ptr(), state_out.data_ptr(), B, D, d_g, code, on.handle))
+    if y is None:
+        y = torch_().empty_like(q)
+        keep(stream, y)
+    else:
+        need("y", y, q.shape, q.dtype, q.device)
+    run("hyena_scan_step", q.device, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
+        state.data_ptr(), y.data_ptr(), state_out.data_ptr(), B, D, d_g, code,
+        stream_handle(q.device, stream))
     return y, state_out
