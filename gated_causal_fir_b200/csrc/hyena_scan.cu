@@ -17,17 +17,21 @@ using hyena::host::overlap;
 using hyena::host::round_up;
 
 constexpr int kSmemMax = 227 * 1024;
+constexpr int kCopySmem = 148 * 1024;   // where tiles come by copies (see plan)
 constexpr int kStaticSmem = 16 * 1024;  // bound on a kernel's static shared memory
 constexpr int64_t kI32 = std::numeric_limits<int32_t>::max();
 
 struct Shape {
   int64_t B, L, D;
   int d_g, dtype;
+  bool train = false;  // the backward's tiles (checkpoints)
   int64_t es() const { return dtype == HYENA_DTYPE_F32 ? 4 : 2; }
   int64_t G() const { return D / d_g; }
   int64_t n_cb() const { return (D + sc::kCh - 1) / sc::kCh; }
   int64_t rows() const {
-    return dtype == HYENA_DTYPE_F32 ? sc::tile_rows<float>() : sc::tile_rows<__nv_bfloat16>();
+    return dtype == HYENA_DTYPE_F32 ? sc::tile_rows<sc::F32>()
+           : train                  ? sc::tile_rows<sc::Bf16Train>()
+                                    : sc::tile_rows<sc::Bf16>();
   }
   int64_t n_tiles() const { return (L + rows() - 1) / rows(); }
   int64_t numel() const { return B * L * D; }
@@ -116,18 +120,20 @@ int encode(CUtensorMap *m, const Shape &s, const void *ptr) {
   return encode(m, s, ptr, s.D, sc::kCh);
 }
 
-template <typename T, int kFeed>
-cudaError_t allow_smem() {
-  cudaError_t e = cudaSuccess;
-  const void *fns[] = {reinterpret_cast<const void *>(sc::scan_fwd_kernel<T, kFeed, true>),
-                       reinterpret_cast<const void *>(sc::scan_fwd_kernel<T, kFeed, false>),
-                       reinterpret_cast<const void *>(sc::scan_bwd_kernel<T, kFeed, true>),
-                       reinterpret_cast<const void *>(sc::scan_bwd_kernel<T, kFeed, false>)};
-  for (const void *f : fns)
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               kSmemMax - kStaticSmem);
-  return e;
+template <typename F>
+void allow(F *kernel, cudaError_t *e) {
+  if (*e == cudaSuccess)
+    *e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax - kStaticSmem);
+}
+template <typename C, int kFeed, bool kBackward>
+void allow_smem(cudaError_t *e) {
+  allow(sc::scan_fwd_kernel<C, kFeed, true>, e);
+  allow(sc::scan_fwd_kernel<C, kFeed, false>, e);
+  if constexpr (kBackward && kFeed != sc::kTmaRaw) {
+    allow(sc::scan_bwd_kernel<C, kFeed, true>, e);
+    allow(sc::scan_bwd_kernel<C, kFeed, false>, e);
+  }
 }
 
 // f(integral constant) for every feed.
@@ -137,6 +143,7 @@ void with_feed(F &&f) {
   f(std::integral_constant<int, sc::kTmaGroup>());
   f(std::integral_constant<int, sc::kCopyChannel>());
   f(std::integral_constant<int, sc::kCopyGroup>());
+  f(std::integral_constant<int, sc::kTmaRaw>());
 }
 
 // Per-device one-time opt-in to the kernels' shared memory.
@@ -150,8 +157,9 @@ int prepare_device(hyena::host::DeviceInfo *info) {
   std::call_once(once[dev], [dev]() {
     cudaError_t e = cudaSuccess;
     with_feed([&](auto feed) {
-      if (e == cudaSuccess) e = allow_smem<float, decltype(feed)::value>();
-      if (e == cudaSuccess) e = allow_smem<__nv_bfloat16, decltype(feed)::value>();
+      allow_smem<sc::F32, decltype(feed)::value, true>(&e);
+      allow_smem<sc::Bf16Train, decltype(feed)::value, true>(&e);
+      allow_smem<sc::Bf16, decltype(feed)::value, false>(&e);
     });
     err[dev] = e;
   });
@@ -174,6 +182,7 @@ sc::Params base_params(const Shape &s, const void *g, const hyena::host::DeviceI
   p.pieces = s.d_g % sc::kCh == 0   ? 1
              : sc::kCh % s.d_g == 0 ? sc::kCh / s.d_g
                                     : (sc::kCh + s.d_g - 2) / s.d_g + 1;
+  while ((1 << p.piece_bits) < p.pieces) ++p.piece_bits;
   p.dg_mode = dg_mode(s);
   p.g_box = g_box(s, g, p.pieces);
   return p;
@@ -184,16 +193,20 @@ struct Launch {
   unsigned grid;
   size_t smem;
 };
-template <typename T>
+template <typename C>
 Launch plan(sc::Params &p, int feed, int streams, int first, int count, int sm_count) {
-  if (feed != sc::kTmaGroup) p.g_box = 0;
+  if (feed != sc::kTmaGroup && feed != sc::kTmaRaw) p.g_box = 0;
   const int decays = sc::per_channel(feed)
-                         ? sc::stream_bytes<T>()
-                         : sc::decay_bytes<T>(p.pieces) +
-                               static_cast<int>(round_up(sc::tile_rows<T>() * p.g_box * sizeof(T),
+                         ? sc::stream_bytes<C>()
+                         : (feed == sc::kTmaRaw ? 0 : sc::decay_bytes<C>(p.pieces)) +
+                               static_cast<int>(round_up(sc::tile_rows<C>() * p.g_box * sizeof(typename C::T),
                                                          sc::kStageAlign));
-  p.stage_bytes = streams * sc::stream_bytes<T>() + decays;
-  p.stages = std::min(sc::kMaxStages, (kSmemMax - kStaticSmem - sc::kStageAlign) / p.stage_bytes);
+  p.stage_bytes = streams * sc::stream_bytes<C>() + decays;
+  // Copies on their way to shared memory hold lines of the L1 cache, which shares its memory: with
+  // all of it given to the ring ~9 KB were in flight and the forward of L = 65536, D = 500 took
+  // 236 us; with rings of 80 to 180 KB 118 us (D = 496, by TMA: 105).
+  const int room = (sc::by_tma(feed) ? kSmemMax : kCopySmem) - kStaticSmem - sc::kStageAlign;
+  p.stages = std::max(2, std::min(sc::kMaxStages, room / p.stage_bytes));
   p.unit_split0 = first;
   p.unit_splits = count;
   p.n_units = p.B * count * p.n_cb;
@@ -203,9 +216,9 @@ Launch plan(sc::Params &p, int feed, int streams, int first, int count, int sm_c
   return l;
 }
 
-template <typename T, int kFeed, bool kOut>
+template <typename C, int kFeed, bool kOut>
 int run_fwd(const Shape &s, sc::Params p, int first, int count, int sms, cudaStream_t stream) {
-  const Launch l = plan<T>(p, kFeed, kOut ? 3 : 2, first, count, sms);
+  const Launch l = plan<C>(p, kFeed, kOut ? 3 : 2, first, count, sms);
   CUtensorMap mk{}, mv{}, mq{}, mg{};
   if (sc::by_tma(kFeed)) {
     if (encode(&mk, s, p.k) || encode(&mv, s, p.v) || (kOut && encode(&mq, s, p.q)) ||
@@ -213,16 +226,16 @@ int run_fwd(const Shape &s, sc::Params p, int first, int count, int sms, cudaStr
         (p.g_box && encode(&mg, s, p.g, s.G(), p.g_box)))
       return HYENA_ERR_CUDA;
   }
-  return hyena::host::launch(sc::scan_fwd_kernel<T, kFeed, kOut>, dim3(l.grid),
+  return hyena::host::launch(sc::scan_fwd_kernel<C, kFeed, kOut>, dim3(l.grid),
                              dim3(sc::kThreads), l.smem, stream, mk, mv, mq, mg,
                              p) == cudaSuccess
              ? HYENA_OK
              : HYENA_ERR_CUDA;
 }
 
-template <typename T, int kFeed, bool kOut>
+template <typename C, int kFeed, bool kOut>
 int run_bwd(const Shape &s, sc::Params p, int first, int count, int sms, cudaStream_t stream) {
-  const Launch l = plan<T>(p, kFeed, kOut ? 4 : 2, first, count, sms);
+  const Launch l = plan<C>(p, kFeed, kOut ? 4 : 2, first, count, sms);
   CUtensorMap mq{}, mdy{}, mk{}, mv{}, mg{};
   if (sc::by_tma(kFeed)) {
     if (encode(&mq, s, p.q) || encode(&mdy, s, p.dy) || (kOut && encode(&mk, s, p.k)) ||
@@ -230,7 +243,7 @@ int run_bwd(const Shape &s, sc::Params p, int first, int count, int sms, cudaStr
         (p.g_box && encode(&mg, s, p.g, s.G(), p.g_box)))
       return HYENA_ERR_CUDA;
   }
-  return hyena::host::launch(sc::scan_bwd_kernel<T, kFeed, kOut>, dim3(l.grid),
+  return hyena::host::launch(sc::scan_bwd_kernel<C, kFeed, kOut>, dim3(l.grid),
                              dim3(sc::kThreads), l.smem, stream, mq, mdy, mk, mv, mg,
                              p) == cudaSuccess
              ? HYENA_OK
@@ -238,26 +251,26 @@ int run_bwd(const Shape &s, sc::Params p, int first, int count, int sms, cudaStr
 }
 
 // The states pass over the whole problem: y and the last state, or (kOut = false) checkpoints.
-template <typename T, int kFeed, bool kOut>
+template <typename C, int kFeed, bool kOut>
 int states(const Shape &s, sc::Params p, float2 *agg, int sms, cudaStream_t stream) {
   if (p.splits > 1) {
     sc::Params a = p;
     a.agg = agg;
     a.ckpt = nullptr;
     a.s_out = nullptr;
-    const int rc = run_fwd<T, kFeed, false>(s, a, 0, p.splits - 1, sms, stream);
+    const int rc = run_fwd<C, kFeed, false>(s, a, 0, p.splits - 1, sms, stream);
     if (rc != HYENA_OK) return rc;
     p.agg = agg;
   }
-  return run_fwd<T, kFeed, kOut>(s, p, 0, p.splits, sms, stream);
+  return run_fwd<C, kFeed, kOut>(s, p, 0, p.splits, sms, stream);
 }
 
-template <typename T, int kFeed>
+template <typename C, int kFeed>
 int forward(const Shape &s, const sc::Params &p, void *ws, int sms, cudaStream_t stream) {
-  return states<T, kFeed, true>(s, p, static_cast<float2 *>(ws), sms, stream);
+  return states<C, kFeed, true>(s, p, static_cast<float2 *>(ws), sms, stream);
 }
 
-template <typename T, int kFeed>
+template <typename C, int kFeed>
 int backward(const Shape &s, sc::Params p, void *ws, int sms, cudaStream_t stream) {
   uint8_t *at = static_cast<uint8_t *>(ws);
   float2 *agg = reinterpret_cast<float2 *>(at);
@@ -267,30 +280,32 @@ int backward(const Shape &s, sc::Params p, void *ws, int sms, cudaStream_t strea
   int rc = HYENA_OK;
   if (!p.ckpt) {
     p.ckpt = reinterpret_cast<float *>(at);
-    rc = states<T, kFeed, false>(s, p, agg, sms, stream);
+    rc = states<C, kFeed, false>(s, p, agg, sms, stream);
     if (rc != HYENA_OK) return rc;
   }
   if (p.splits > 1) {
     p.agg = agg;
-    rc = run_bwd<T, kFeed, false>(s, p, 1, p.splits - 1, sms, stream);
+    rc = run_bwd<C, kFeed, false>(s, p, 1, p.splits - 1, sms, stream);
     if (rc != HYENA_OK) return rc;
   }
-  rc = run_bwd<T, kFeed, true>(s, p, 0, p.splits, sms, stream);
+  rc = run_bwd<C, kFeed, true>(s, p, 0, p.splits, sms, stream);
   if (rc != HYENA_OK || p.dg_mode == 0) return rc;
   const int64_t n = s.B * s.L * s.G();
   const int width = p.dg_mode == 1 ? s.d_g / sc::kCh : s.d_g;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>((n + 255) / 256, 16 * sms));
-  return hyena::host::launch(sc::scan_dg_kernel<T>, dim3(grid), dim3(256), 0, stream,
-                             static_cast<const float *>(p.dg_part), static_cast<T *>(p.dg), n,
+  return hyena::host::launch(sc::scan_dg_kernel<typename C::T>, dim3(grid), dim3(256), 0, stream,
+                             static_cast<const float *>(p.dg_part), static_cast<typename C::T *>(p.dg), n,
                              width) == cudaSuccess
              ? HYENA_OK
              : HYENA_ERR_CUDA;
 }
 
 // Which feed takes the tensors, from their rows and addresses; sets the copies' and stores' width.
-// TMA needs rows and bases of 16 bytes, and a group's decay for both channels of a pair.
+// TMA needs rows and bases of 16 bytes, and a group's decay for both channels of a pair.  raw:
+// whether groups of 2 and 4 take their exps in the compute warps (the backward's have no time for
+// them: 175 us against 147 at L = 8192, D = 4096, d_g = 2).
 int choose_feed(const Shape &s, std::initializer_list<const void *> streams,
-                std::initializer_list<const void *> outs, const void *g, sc::Params *p) {
+                std::initializer_list<const void *> outs, const void *g, bool raw, sc::Params *p) {
   uintptr_t bits = static_cast<uintptr_t>(s.D * s.es()), out_bits = bits;
   for (const void *t : streams) bits |= reinterpret_cast<uintptr_t>(t);
   if (s.d_g == 1) bits |= reinterpret_cast<uintptr_t>(g);
@@ -300,7 +315,9 @@ int choose_feed(const Shape &s, std::initializer_list<const void *> streams,
   p->copy = bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : 0;
   const bool tma = bits % 16 == 0 && p->pair_out && s.D * s.es() * s.L < (int64_t{1} << 40) &&
                    (s.d_g == 1 || s.d_g % 2 == 0);
-  return tma ? (s.d_g == 1 ? sc::kTmaChannel : sc::kTmaGroup)
+  return tma ? (s.d_g == 1                  ? sc::kTmaChannel
+                : raw && s.d_g <= 4 && p->g_box > 0 ? sc::kTmaRaw
+                                             : sc::kTmaGroup)
              : (s.d_g == 1 ? sc::kCopyChannel : sc::kCopyGroup);
 }
 
@@ -348,20 +365,20 @@ bool misaligned(uintptr_t a, std::initializer_list<const void *> ptrs) {
 extern "C" {
 
 int64_t hyena_scan_ckpt_tiles(int64_t L, int dtype) {
-  const Shape s{1, L, 1, 1, dtype};
+  const Shape s{1, L, 1, 1, dtype, true};
   if (check_shape(s) != HYENA_OK) return -HYENA_ERR_INVALID_ARG;
   return s.n_tiles();
 }
 
 int64_t hyena_scan_workspace_bytes(int64_t B, int64_t L, int64_t D, int d_g, int dtype) {
-  const Shape s{B, L, D, d_g, dtype};
+  const Shape s{B, L, D, d_g, dtype}, t{B, L, D, d_g, dtype, true};
   if (check_shape(s) != HYENA_OK) return -HYENA_ERR_INVALID_ARG;
-  return B == 0 || L == 0 ? 0 : agg_bytes(s);
+  return B == 0 || L == 0 ? 0 : std::max(agg_bytes(s), agg_bytes(t));
 }
 
 int64_t hyena_scan_bwd_workspace_bytes(int64_t B, int64_t L, int64_t D, int d_g, int dtype,
                                        int have_ckpt) {
-  const Shape s{B, L, D, d_g, dtype};
+  const Shape s{B, L, D, d_g, dtype, true};
   if (check_shape(s) != HYENA_OK) return -HYENA_ERR_INVALID_ARG;
   if (B == 0 || L == 0) return 0;
   return agg_bytes(s) + dg_bytes(s) + (have_ckpt ? 0 : ckpt_bytes(s));
@@ -370,7 +387,7 @@ int64_t hyena_scan_bwd_workspace_bytes(int64_t B, int64_t L, int64_t D, int d_g,
 int hyena_scan_fwd(const void *q, const void *k, const void *v, const void *g, const float *s0,
                    void *y, float *s_out, float *ckpt, int64_t B, int64_t L, int64_t D, int d_g,
                    int dtype, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
-  const Shape s{B, L, D, d_g, dtype};
+  const Shape s{B, L, D, d_g, dtype, ckpt != nullptr};
   int rc = check_shape(s);
   if (rc != HYENA_OK) return rc;
   if (misaligned(4, {s0, s_out, ckpt})) return HYENA_ERR_MISALIGNED;
@@ -401,12 +418,13 @@ int hyena_scan_fwd(const void *q, const void *k, const void *v, const void *g, c
   p.s_out = s_out;
   p.ckpt = ckpt;
   p.y = y;
-  const int feed = choose_feed(s, {q, k, v}, {y}, g, &p);
+  const int feed = choose_feed(s, {q, k, v}, {y}, g, true, &p);
   return with_one_feed(feed, [&](auto f) {
     constexpr int kFeed = decltype(f)::value;
-    return dtype == HYENA_DTYPE_F32
-               ? forward<float, kFeed>(s, p, workspace, info.sm_count, stream)
-               : forward<__nv_bfloat16, kFeed>(s, p, workspace, info.sm_count, stream);
+    if (dtype == HYENA_DTYPE_F32)
+      return forward<sc::F32, kFeed>(s, p, workspace, info.sm_count, stream);
+    return s.train ? forward<sc::Bf16Train, kFeed>(s, p, workspace, info.sm_count, stream)
+                   : forward<sc::Bf16, kFeed>(s, p, workspace, info.sm_count, stream);
   });
 }
 
@@ -414,7 +432,7 @@ int hyena_scan_bwd(const void *q, const void *k, const void *v, const void *g, c
                    const void *dy, const float *ds_out, const float *ckpt, void *dq, void *dk,
                    void *dv, void *dg, float *ds0, int64_t B, int64_t L, int64_t D, int d_g,
                    int dtype, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
-  const Shape s{B, L, D, d_g, dtype};
+  const Shape s{B, L, D, d_g, dtype, true};
   int rc = check_shape(s);
   if (rc != HYENA_OK) return rc;
   if (misaligned(4, {s0, ds_out, ckpt, ds0})) return HYENA_ERR_MISALIGNED;
@@ -451,13 +469,16 @@ int hyena_scan_bwd(const void *q, const void *k, const void *v, const void *g, c
   p.dv = dv;
   p.dg = dg;
   p.ds0 = ds0;
-  const int feed = s.d_g == 1 ? choose_feed(s, {q, k, v, dy}, {dq, dk, dv, dg}, g, &p)
-                              : choose_feed(s, {q, k, v, dy}, {dq, dk, dv}, g, &p);
+  const int feed = s.d_g == 1 ? choose_feed(s, {q, k, v, dy}, {dq, dk, dv, dg}, g, false, &p)
+                              : choose_feed(s, {q, k, v, dy}, {dq, dk, dv}, g, false, &p);
   return with_one_feed(feed, [&](auto f) {
     constexpr int kFeed = decltype(f)::value;
-    return dtype == HYENA_DTYPE_F32
-               ? backward<float, kFeed>(s, p, workspace, info.sm_count, stream)
-               : backward<__nv_bfloat16, kFeed>(s, p, workspace, info.sm_count, stream);
+    if constexpr (kFeed == sc::kTmaRaw)
+      return static_cast<int>(HYENA_ERR_UNSUPPORTED);  // not chosen here
+    else
+      return dtype == HYENA_DTYPE_F32
+                 ? backward<sc::F32, kFeed>(s, p, workspace, info.sm_count, stream)
+                 : backward<sc::Bf16Train, kFeed>(s, p, workspace, info.sm_count, stream);
   });
 }
 

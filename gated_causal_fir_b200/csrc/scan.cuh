@@ -48,26 +48,45 @@ constexpr unsigned int kTimeout = 1u; // HYENA_DEVICE_TIMEOUT
 // How a tile's inputs reach shared memory: the streams by TMA, or where their rows are no multiple
 // of 16 bytes by asynchronous 8- or 4-byte copies (single elements where not even those are
 // aligned).  One decay per channel: g is a stream like k and v and the compute warps take its exp.
-// One per group: the helper warps do.
-enum Feed { kTmaChannel = 0, kTmaGroup = 1, kCopyChannel = 2, kCopyGroup = 3 };
-__host__ __device__ constexpr bool by_tma(int feed) { return feed <= kTmaGroup; }
-__host__ __device__ constexpr bool per_channel(int feed) { return feed % 2 == 0; }
+// One per group: the helper warps do, except for groups of 2 and 4 channels (kTmaRaw), whose many
+// exps are quicker where they are used (L = 8192, D = 4096, d_g = 2: 99 us by the helpers).
+enum Feed { kTmaChannel = 0, kTmaGroup = 1, kCopyChannel = 2, kCopyGroup = 3, kTmaRaw = 4 };
+__host__ __device__ constexpr bool by_tma(int feed) {
+  return feed == kTmaChannel || feed == kTmaGroup || feed == kTmaRaw;
+}
+__host__ __device__ constexpr bool per_channel(int feed) {
+  return feed == kTmaChannel || feed == kCopyChannel;
+}
+// One warp feeds all of a tile.
+__host__ __device__ constexpr bool one_feeder(int feed) {
+  return feed == kTmaChannel || feed == kTmaRaw;
+}
 
-// Rows of a tile are 16 R.  The registers of a segment and the bytes of a stage both grow with
-// R; the joining of segments costs 16 steps per tile whatever R is.
-template <typename T> struct Rows;
-template <> struct Rows<__nv_bfloat16> { static constexpr int R = 11; };
-template <> struct Rows<float> { static constexpr int R = 7; };
+// An element type with R, the rows of a segment (a tile has 16 R).  The joining of segments costs
+// the same per tile whatever R is, so the forward takes as many as its registers allow (B=1 L=8192
+// D=4096 d_g=64 bf16: 48 us with 11, 55 with 9); the backward, which holds five values a row where
+// the forward holds three, runs out of them earlier (162 us with 11 and spills, 121 with 9, 133
+// with 7).  Checkpoints tie a training forward to the backward's tiles.
+template <typename E, int kRows>
+struct Cfg {
+  using T = E;
+  static constexpr int R = kRows;
+};
+using Bf16 = Cfg<__nv_bfloat16, 11>;
+using Bf16Train = Cfg<__nv_bfloat16, 9>;
+using F32 = Cfg<float, 7>;
 
-template <typename T>
-__host__ __device__ constexpr int tile_rows() { return kSegs * Rows<T>::R; }
-template <typename T>
-__host__ __device__ constexpr int stream_bytes() { return tile_rows<T>() * kCh * static_cast<int>(sizeof(T)); }
+template <typename C>
+__host__ __device__ constexpr int tile_rows() { return kSegs * C::R; }
+template <typename C>
+__host__ __device__ constexpr int stream_bytes() {
+  return tile_rows<C>() * kCh * static_cast<int>(sizeof(typename C::T));
+}
 
 // fp32 decays of a tile's rows and groups, rounded up to keep what follows them aligned.
-template <typename T>
+template <typename C>
 __host__ __device__ constexpr int decay_bytes(int pieces) {
-  return (tile_rows<T>() * pieces * 4 + 127) / 128 * 128;
+  return (tile_rows<C>() * pieces * 4 + 127) / 128 * 128;
 }
 
 struct Params {
@@ -86,7 +105,8 @@ struct Params {
   int n_cb, n_tiles, splits, tiles_per_split;
   int unit_split0, unit_splits;     // the cuts this launch works on
   int n_units;                      // B x unit_splits x n_cb
-  int pieces;                       // groups a block of 32 channels touches at most
+  int pieces, piece_bits;           // groups a block of 32 channels touches at most; and the
+                                    // least power of two that holds them
   int g_box;                        // groups per row of g's tile (kTmaGroup); 0: element loads
   int copy;                         // bytes per asynchronous copy: 8, 4, or 0 for element loads
   int pair_out;                     // rows and bases allow stores of two channels
@@ -174,54 +194,101 @@ struct Unit {
   }
 };
 
-template <typename T>
-__device__ __forceinline__ void fill_decays(const Params &p, float *as, int b, int c0, int t0,
-                                            int thread, int threads) {
-  const T *g = static_cast<const T *>(p.g) + static_cast<int64_t>(b) * p.L * p.G;
-  const int g0 = c0 / p.d_g;
-  for (int e = thread; e < tile_rows<T>() * p.pieces; e += threads) {
-    const int row = e / p.pieces, t = t0 + row, gi = g0 + e % p.pieces;
-    // rows past the end leave the state as it is
-    as[e] = t < p.L && gi < p.G ? decay(load_one(g + static_cast<int64_t>(t) * p.G + gi)) : 1.0f;
+// One decay per row and group of the block by the warps [0, warps): lanes take groups first, in a
+// power of two of columns (p.piece_bits), so that no index is divided; g_at(row, group) is the log
+// decay, and 0 past the end, where rows leave the state as it is.
+template <typename C, int kBatch, typename F>  // kBatch: loads in flight per thread
+__device__ __forceinline__ void form_batches(const Params &p, float *as, int warp, int warps,
+                                             F &&g_at) {
+  const int lane = threadIdx.x % 32, per = 32 >> p.piece_bits;  // rows a warp takes at a time
+  const int gi = lane & ((1 << p.piece_bits) - 1);
+  if (gi >= p.pieces) return;
+  const int step = warps * per;
+  for (int row = warp * per + (lane >> p.piece_bits); row < tile_rows<C>(); row += kBatch * step) {
+    float v[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      v[i] = row + i * step < tile_rows<C>() ? g_at(row + i * step, gi) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if (row + i * step < tile_rows<C>()) as[(row + i * step) * p.pieces + gi] = decay(v[i]);
   }
 }
+template <typename C, typename F>
+__device__ __forceinline__ void form_decays(const Params &p, float *as, int warp, int warps,
+                                            F &&g_at) {
+  if (p.piece_bits <= 1)
+    form_batches<C, 4>(p, as, warp, warps, g_at);
+  else
+    form_batches<C, 24>(p, as, warp, warps, g_at);
+}
 
-// The decays of a tile from its rows of g in shared memory (rows past the end were filled with 0
-// and decay by 1).
-template <typename T>
-__device__ __forceinline__ void convert_decays(const Params &p, float *as, const T *g, int first,
-                                               int thread, int threads) {
-  for (int e = thread; e < tile_rows<T>() * p.pieces; e += threads)
-    as[e] = decay(load_one(g + e / p.pieces * p.g_box + first + e % p.pieces));
+// From global memory.
+template <typename C>
+__device__ __forceinline__ void fill_decays(const Params &p, float *as, int b, int c0, int t0,
+                                            int warp, int warps) {
+  using T = typename C::T;
+  const int g0 = c0 / p.d_g, rows = p.L - t0, groups = p.G - g0;
+  const T *g = static_cast<const T *>(p.g) + (static_cast<int64_t>(b) * p.L + t0) * p.G + g0;
+  form_decays<C>(p, as, warp, warps, [&](int row, int gi) {
+    return row < rows && gi < groups ? load_one(g + static_cast<int64_t>(row) * p.G + gi) : 0.0f;
+  });
+}
+
+// From the tile of g's rows in shared memory (zeros past the end).
+template <typename C>
+__device__ __forceinline__ void convert_decays(const Params &p, float *as,
+                                               const typename C::T *g, int first, int warp,
+                                               int warps) {
+  form_decays<C>(p, as, warp, warps,
+                 [&](int row, int gi) { return load_one(g + row * p.g_box + first + gi); });
 }
 
 // One stream's tile by the helper threads' asynchronous copies; zero outside the tensor, as TMA
 // fills.
-template <typename T, int kBytes>
-__device__ __forceinline__ void copy_tile(const Params &p, T *dst, const void *src, int b, int c0,
-                                          int t0, int thread) {
+template <typename C, int kBytes>
+__device__ __forceinline__ void copy_tile(const Params &p, typename C::T *dst, const void *src,
+                                          int b, int c0, int t0, int thread) {
+  using T = typename C::T;
   constexpr int E = kBytes / static_cast<int>(sizeof(T)), N = kCh / E;  // elements; copies per row
   constexpr int kStep = 32 * kHelperWarps / N;                          // rows apart
   static_assert(E >= 1 && 32 * kHelperWarps % N == 0, "copies of a row");
+  constexpr int kCopies = tile_rows<C>() / kStep;
+  static_assert(kCopies * kStep == tile_rows<C>(), "copies of a column");
   const int c = c0 + thread % N * E, row0 = thread / N;
-  const T *s = static_cast<const T *>(src) + (static_cast<int64_t>(b) * p.L + t0 + row0) * p.D + c;
-  uint32_t d = smem_u32(dst + row0 * kCh + thread % N * E);
-  const int rows = c < p.D ? p.L - t0 : 0;
-  for (int r = row0; r < tile_rows<T>(); r += kStep) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(d),
-                 "l"(r < rows ? s : static_cast<const T *>(src)), "n"(kBytes),
-                 "r"(r < rows ? kBytes : 0)
-                 : "memory");
-    s += static_cast<int64_t>(kStep) * p.D;
-    d += kStep * kCh * static_cast<int>(sizeof(T));
+  const bool inside = c < p.D;
+  const uint8_t *s = static_cast<const uint8_t *>(src);
+  if (inside)
+    s += ((static_cast<int64_t>(b) * p.L + t0 + row0) * p.D + c) * static_cast<int64_t>(sizeof(T));
+  const int64_t step = inside ? static_cast<int64_t>(kStep) * p.D * static_cast<int64_t>(sizeof(T)) : 0;
+  const uint32_t d = smem_u32(dst + row0 * kCh + thread % N * E);
+  const int rows = inside ? p.L - t0 - row0 : 0;  // rows of this thread's, and between, to read
+  if (p.L - t0 >= tile_rows<C>()) {
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i, s += step)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(
+                       d + i * kStep * kCh * static_cast<int>(sizeof(T))),
+                   "l"(s), "n"(kBytes), "r"(inside ? kBytes : 0)
+                   : "memory");
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < kCopies; ++i) {
+      const bool live = i * kStep < rows;
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(
+                       d + i * kStep * kCh * static_cast<int>(sizeof(T))),
+                   "l"(live ? s + i * step : static_cast<const uint8_t *>(src)), "n"(kBytes),
+                   "r"(live ? kBytes : 0)
+                   : "memory");
+    }
   }
 }
 
-template <typename T>
-__device__ __forceinline__ void load_elements(const Params &p, T *dst, const void *src, int b,
-                                              int c0, int t0, int thread) {
+template <typename C>
+__device__ __forceinline__ void load_elements(const Params &p, typename C::T *dst,
+                                              const void *src, int b, int c0, int t0, int thread) {
+  using T = typename C::T;
   const T *s = static_cast<const T *>(src) + static_cast<int64_t>(b) * p.L * p.D;
-  for (int e = thread; e < tile_rows<T>() * kCh; e += 32 * kHelperWarps) {
+  for (int e = thread; e < tile_rows<C>() * kCh; e += 32 * kHelperWarps) {
     const int t = t0 + e / kCh, c = c0 + e % kCh;
     dst[e] = t < p.L && c < p.D ? s[static_cast<int64_t>(t) * p.D + c] : T(0.0f);
   }
@@ -235,23 +302,24 @@ __device__ __forceinline__ void arrive_after_copies(uint64_t *bar) {
 
 // The helper warps: NS streams of every tile of the CTA's units into the ring, in the order the
 // compute warps take them (kReverse: last tile first).
-template <typename T, int kFeed, bool kReverse, int NS>
+template <typename C, int kFeed, bool kReverse, int NS>
 __device__ __forceinline__ void feed(const Params &p, Ring &ring, uint8_t *stages,
                                      const CUtensorMap *const (&maps)[5],
                                      const void *const (&ptrs)[5]) {
+  using T = typename C::T;
   const int warp = threadIdx.x / 32 - kComputeThreads / 32, lane = threadIdx.x % 32;
   constexpr int kStreams = NS + (per_channel(kFeed) ? 1 : 0);
-  constexpr int kBytes = stream_bytes<T>();
+  constexpr int kBytes = stream_bytes<C>();
   constexpr int kGroups = 16 / static_cast<int>(sizeof(T));  // groups in 16 bytes of g
   const int th = threadIdx.x - kComputeThreads;
   if (by_tma(kFeed) && warp == 0 && lane != 0) return;
-  if (kFeed == kTmaChannel && warp != 0) return;
+  if (one_feeder(kFeed) && warp != 0) return;
   int it = 0, last = 0;
   for (int u = blockIdx.x; u < p.n_units; u += gridDim.x) {
     const Unit un(p, u);
     const int c0 = un.cb * kCh;
     for (int i = un.tile0; i < un.tile1; ++i, ++it) {
-      const int tile = kReverse ? un.tile1 - 1 - (i - un.tile0) : i, t0 = tile * tile_rows<T>();
+      const int tile = kReverse ? un.tile1 - 1 - (i - un.tile0) : i, t0 = tile * tile_rows<C>();
       const int st = it % p.stages, round = it / p.stages;
       uint8_t *buf = stages + st * p.stage_bytes;
       float *as = reinterpret_cast<float *>(buf + NS * kBytes);  // where decays are formed here
@@ -259,11 +327,15 @@ __device__ __forceinline__ void feed(const Params &p, Ring &ring, uint8_t *stage
         goto out;
       if (by_tma(kFeed) && warp == 0) {
         if (kFeed == kTmaGroup && p.g_box) {
-          mbar_arrive_expect_tx(&ring.raw[st], tile_rows<T>() * p.g_box * sizeof(T));
-          tma_load_3d(buf + NS * kBytes + decay_bytes<T>(p.pieces), maps[4], &ring.raw[st],
+          mbar_arrive_expect_tx(&ring.raw[st], tile_rows<C>() * p.g_box * sizeof(T));
+          tma_load_3d(buf + NS * kBytes + decay_bytes<C>(p.pieces), maps[4], &ring.raw[st],
                       c0 / p.d_g / kGroups * kGroups, t0, un.b);
         }
-        mbar_arrive_expect_tx(&ring.full[st], kStreams * kBytes);
+        const int raw = kFeed == kTmaRaw ? tile_rows<C>() * p.g_box * static_cast<int>(sizeof(T)) : 0;
+        mbar_arrive_expect_tx(&ring.full[st], kStreams * kBytes + raw);
+        if (kFeed == kTmaRaw)
+          tma_load_3d(buf + NS * kBytes, maps[4], &ring.full[st], c0 / p.d_g / kGroups * kGroups,
+                      t0, un.b);
 #pragma unroll
         for (int s = 0; s < kStreams; ++s)
           tma_load_3d(buf + s * kBytes, maps[s], &ring.full[st], c0, t0, un.b);
@@ -272,12 +344,12 @@ __device__ __forceinline__ void feed(const Params &p, Ring &ring, uint8_t *stage
       if (kFeed == kTmaGroup && warp > 0) {
         if (p.g_box) {
           if (!mbar_wait(&ring.raw[st], round & 1, &ring.abort, p.status, kTimeout)) goto out;
-          convert_decays<T>(p, as,
+          convert_decays<C>(p, as,
                             reinterpret_cast<const T *>(buf + NS * kBytes +
-                                                        decay_bytes<T>(p.pieces)),
-                            c0 / p.d_g % kGroups, th - 32, 32 * (kHelperWarps - 1));
+                                                        decay_bytes<C>(p.pieces)),
+                            c0 / p.d_g % kGroups, warp - 1, kHelperWarps - 1);
         } else {
-          fill_decays<T>(p, as, un.b, c0, t0, th - 32, 32 * (kHelperWarps - 1));
+          fill_decays<C>(p, as, un.b, c0, t0, warp - 1, kHelperWarps - 1);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&ring.full[st]);
@@ -287,13 +359,13 @@ __device__ __forceinline__ void feed(const Params &p, Ring &ring, uint8_t *stage
         for (int s = 0; s < kStreams; ++s) {
           T *dst = reinterpret_cast<T *>(buf + s * kBytes);
           if (p.copy == 8)
-            copy_tile<T, 8>(p, dst, ptrs[s], un.b, c0, t0, th);
+            copy_tile<C, 8>(p, dst, ptrs[s], un.b, c0, t0, th);
           else if (p.copy == 4)
-            copy_tile<T, 4>(p, dst, ptrs[s], un.b, c0, t0, th);
+            copy_tile<C, 4>(p, dst, ptrs[s], un.b, c0, t0, th);
           else
-            load_elements<T>(p, dst, ptrs[s], un.b, c0, t0, th);
+            load_elements<C>(p, dst, ptrs[s], un.b, c0, t0, th);
         }
-        if (!per_channel(kFeed)) fill_decays<T>(p, as, un.b, c0, t0, th, 32 * kHelperWarps);
+        if (!per_channel(kFeed)) fill_decays<C>(p, as, un.b, c0, t0, warp, kHelperWarps);
         // one arrival for the copies, and one for what the thread stored itself
         if (p.copy) arrive_after_copies(&ring.full[st]);
         if (!p.copy || !per_channel(kFeed)) mbar_arrive(&ring.full[st]);
@@ -316,7 +388,7 @@ out:
 template <int kFeed>
 __device__ __forceinline__ void ring_init(const Params &p, Ring &ring) {
   if (threadIdx.x == 0) {
-    const int arrivals = by_tma(kFeed) ? (per_channel(kFeed) ? 1 : kHelperWarps)
+    const int arrivals = by_tma(kFeed) ? (one_feeder(kFeed) ? 1 : kHelperWarps)
                                        : 32 * kHelperWarps * (p.copy && !per_channel(kFeed) ? 2 : 1);
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&ring.full[i], arrivals);
@@ -330,13 +402,14 @@ __device__ __forceinline__ void ring_init(const Params &p, Ring &ring) {
 }
 
 // A lane's decays in the rows of its segment.
-template <typename T, int kFeed, bool kChannel = per_channel(kFeed)> struct Decays;
-template <typename T, int kFeed>
-struct Decays<T, kFeed, true> {  // from the lane's pairs of g
+template <typename C, int kFeed, bool kChannel = per_channel(kFeed)> struct Decays;
+template <typename C, int kFeed>
+struct Decays<C, kFeed, true> {  // from the lane's pairs of g
+  using T = typename C::T;
   using Held = F2;
   const uint8_t *at;
   __device__ Decays(const Params &, const uint8_t *tile, int seg, int l, int)
-      : at(tile + (seg * Rows<T>::R * kCh + 2 * l) * static_cast<int>(sizeof(T))) {}
+      : at(tile + (seg * C::R * kCh + 2 * l) * static_cast<int>(sizeof(T))) {}
   __device__ Held load(int r) const {
     const float2 g = unpack(Pair<T>::f(*reinterpret_cast<const typename Pair<T>::Raw *>(
         at + r * kCh * static_cast<int>(sizeof(T)))));
@@ -344,28 +417,44 @@ struct Decays<T, kFeed, true> {  // from the lane's pairs of g
   }
   __device__ static F2 pair(Held a) { return a; }
 };
-template <typename T>
-struct Decays<T, kTmaGroup, false> {  // d_g is even: the two channels share one
+template <typename C>
+struct Decays<C, kTmaGroup, false> {  // d_g is even: the two channels share one
   using Held = float;
   const float *at;
   int step;
   __device__ Decays(const Params &p, const uint8_t *tile, int seg, int l, int c0) {
     const int c = min(c0 + 2 * l, p.D - 1);
-    at = reinterpret_cast<const float *>(tile) + seg * Rows<T>::R * p.pieces + c / p.d_g -
+    at = reinterpret_cast<const float *>(tile) + seg * C::R * p.pieces + c / p.d_g -
          c0 / p.d_g;
     step = p.pieces;
   }
   __device__ Held load(int r) const { return at[r * step]; }
   __device__ static F2 pair(Held a) { return pack(a, a); }
 };
-template <typename T>
-struct Decays<T, kCopyGroup, false> {
+template <typename C>
+struct Decays<C, kTmaRaw, false> {  // the same, from the tile of g's rows
+  using T = typename C::T;
+  using Held = float;
+  const T *at;
+  int step;
+  __device__ Decays(const Params &p, const uint8_t *tile, int seg, int l, int c0) {
+    constexpr int kGroups = 16 / static_cast<int>(sizeof(T));
+    const int c = min(c0 + 2 * l, p.D - 1), g0 = c0 / p.d_g;
+    at = reinterpret_cast<const T *>(tile) + seg * C::R * p.g_box + g0 % kGroups + c / p.d_g -
+         g0;
+    step = p.g_box;
+  }
+  __device__ Held load(int r) const { return decay(load_one(at + r * step)); }
+  __device__ static F2 pair(Held a) { return pack(a, a); }
+};
+template <typename C>
+struct Decays<C, kCopyGroup, false> {
   using Held = F2;
   const float *at;
   int step, second;
   __device__ Decays(const Params &p, const uint8_t *tile, int seg, int l, int c0) {
     const int g0 = c0 / p.d_g, i0 = min(c0 + 2 * l, p.D - 1) / p.d_g - g0;
-    at = reinterpret_cast<const float *>(tile) + seg * Rows<T>::R * p.pieces + i0;
+    at = reinterpret_cast<const float *>(tile) + seg * C::R * p.pieces + i0;
     second = min(c0 + 2 * l + 1, p.D - 1) / p.d_g - g0 - i0;
     step = p.pieces;
   }
@@ -434,7 +523,7 @@ __device__ __forceinline__ F2 from_other_half(F2 x) { return __shfl_xor_sync(0xf
 // ---------------------------------------------------------------------------- forward
 // kOut: y and the last state (streams k, v, q); otherwise only states: checkpoints, or the (A, S)
 // of the unit's time cut from a zero state (streams k, v).
-template <typename T, int kFeed, bool kOut>
+template <typename C, int kFeed, bool kOut>
 __global__ void __launch_bounds__(kThreads, 1)
     scan_fwd_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                     const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg,
@@ -443,16 +532,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *stages = align_stage(dynamic);
   __shared__ Ring ring;
   __shared__ ulonglong2 joint[2][kWarps][kCh / 2];  // (A, S) of a warp's rows
-  constexpr int R = Rows<T>::R, NS = kOut ? 3 : 2, kBytes = stream_bytes<T>();
+  using T = typename C::T;
+  constexpr int R = C::R, NS = kOut ? 3 : 2, kBytes = stream_bytes<C>();
   using Raw = typename Pair<T>::Raw;
-  using Dec = Decays<T, kFeed>;
+  using Dec = Decays<C, kFeed>;
   ring_init<kFeed>(p, ring);
   griddep_launch_dependents();
   griddep_wait();
   if (threadIdx.x >= kComputeThreads) {
     const CUtensorMap *const maps[5] = {&mk, &mv, kOut ? &mq : &mg, &mg, &mg};
     const void *const ptrs[5] = {p.k, p.v, kOut ? p.q : p.g, p.g, nullptr};
-    feed<T, kFeed, false, NS>(p, ring, stages, maps, ptrs);
+    feed<C, kFeed, false, NS>(p, ring, stages, maps, ptrs);
     return;
   }
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, l = lane % 16;
@@ -513,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (kOut) {
         if (second) s = fma2(Ao, s, So);
-        const Out<T, kFeed> y(p.y, p, un.b, tile * tile_rows<T>() + seg * R, c, dead);
+        const Out<T, kFeed> y(p.y, p, un.b, tile * tile_rows<C>() + seg * R, c, dead);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           s = fma2(Dec::pair(a[r]), s, x[r]);
@@ -554,7 +644,7 @@ __device__ __forceinline__ void sum_groups(const float (&v)[R], int l, F &&put) 
 
 // kOut: the gradients (streams q, dy, k, v and the checkpoints); otherwise the (A, W) of the
 // unit's time cut from w = 0 (streams q, dy).
-template <typename T, int kFeed, bool kOut>
+template <typename C, int kFeed, bool kOut>
 __global__ void __launch_bounds__(kThreads, 1)
     scan_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mdy,
                     const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
@@ -564,16 +654,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Ring ring;
   __shared__ ulonglong2 joint[2][kWarps][kCh / 2];  // (A, S) of a warp's rows
   __shared__ F2 joint_w[2][kWarps][kCh / 2];
-  constexpr int R = Rows<T>::R, NS = kOut ? 4 : 2, kBytes = stream_bytes<T>();
+  using T = typename C::T;
+  constexpr int R = C::R, NS = kOut ? 4 : 2, kBytes = stream_bytes<C>();
   using Raw = typename Pair<T>::Raw;
-  using Dec = Decays<T, kFeed>;
+  using Dec = Decays<C, kFeed>;
   ring_init<kFeed>(p, ring);
   griddep_launch_dependents();
   griddep_wait();
   if (threadIdx.x >= kComputeThreads) {
     const CUtensorMap *const maps[5] = {&mq, &mdy, kOut ? &mk : &mg, &mv, &mg};
     const void *const ptrs[5] = {p.q, p.dy, kOut ? p.k : p.g, p.v, p.g};
-    feed<T, kFeed, true, NS>(p, ring, stages, maps, ptrs);
+    feed<C, kFeed, true, NS>(p, ring, stages, maps, ptrs);
     return;
   }
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, l = lane % 16;
@@ -591,11 +682,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = p.splits - 1; j > un.split; --j)
         w_in = through_cut(agg + static_cast<int64_t>(j) * p.D, c, p.D, w_in);
     }
+    const int64_t ckpt0 = static_cast<int64_t>(un.b) * p.n_tiles;
+    F2 start = 0;  // the state before the tile, requested a tile ahead
+    if (kOut) start = get_state(p.ckpt, ckpt0 + un.tile1 - 1, c, p.D);
     for (int tile = un.tile1 - 1; tile >= un.tile0; --tile, ++it) {
       const int st = it % p.stages;
       const uint8_t *buf = stages + st * p.stage_bytes;
-      F2 s = 0;
-      if (kOut) s = get_state(p.ckpt, static_cast<int64_t>(un.b) * p.n_tiles + tile, c, p.D);
+      F2 s = start;
+      if (kOut && tile > un.tile0) start = get_state(p.ckpt, ckpt0 + tile - 1, c, p.D);
       if (!mbar_wait(&ring.full[st], (it / p.stages) & 1, &ring.abort, p.status, kTimeout))
         dead = true;
       Raw qr[R], dyr[R], kr[R], vr[R];
@@ -650,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           s = fma2(Ao, s, So);
         else
           w = fma2(Ao, w, Wo);
-        const int t0 = tile * tile_rows<T>() + seg * R;
+        const int t0 = tile * tile_rows<C>() + seg * R;
         F2 before[R];  // s_{t-1}
         const Out<T, kFeed> dq(p.dq, p, un.b, t0, c, dead);
 #pragma unroll
