@@ -9,6 +9,10 @@ streams, nothing else.  There is no CPU path: without a CUDA device or the built
 call raises.
 
 Importing the package does not load the library; the first call does.
+
+Beside the FIR (``include/hyena_mixer.h``): the gated linear recurrence (``hyena_scan_*``), the
+projections around a mixer (``hyena_proj_*``), and whole mixer layers over them
+(``hyena_mixer_*``).
 """
 import ctypes
 
@@ -18,6 +22,7 @@ from ._native import (HYENA_ALGO_AUTO, HYENA_ALGO_DIRECT, HYENA_ALGO_FFT, HYENA_
                       HYENA_DTYPE_BF16, HYENA_DTYPE_F32, ALGO_NAMES, HyenaError)
 from ._native import (HYENA_ACT_GELU, HYENA_ACT_LOGSIGMOID, HYENA_ACT_NONE, HYENA_ACT_SIGMOID,
                       HYENA_ACT_SILU)
+from .mixer import Linear, MixerParams, hyena_mixer_bwd, hyena_mixer_fwd, hyena_mixer_step
 from .projection import (hyena_proj_bwd, hyena_proj_bwd_workspace_bytes, hyena_proj_fwd,
                          hyena_proj_workspace_bytes)
 from .recurrence import (hyena_scan_bwd, hyena_scan_bwd_workspace_bytes, hyena_scan_ckpt,
@@ -39,7 +44,8 @@ __all__ = [
     "hyena_scan_workspace_bytes", "hyena_scan_bwd_workspace_bytes",
     "hyena_proj_fwd", "hyena_proj_bwd", "hyena_proj_workspace_bytes",
     "hyena_proj_bwd_workspace_bytes", "HYENA_ACT_NONE", "HYENA_ACT_GELU", "HYENA_ACT_SILU",
-    "HYENA_ACT_SIGMOID", "HYENA_ACT_LOGSIGMOID",
+    "HYENA_ACT_SIGMOID", "HYENA_ACT_LOGSIGMOID", "Linear", "MixerParams", "hyena_mixer_fwd",
+    "hyena_mixer_bwd", "hyena_mixer_step",
 ]
 
 
