@@ -88,13 +88,19 @@ int64_t dg_bytes(const Shape &s) {
   return m == 0 ? 0 : round_up(s.B * s.L * (m == 1 ? s.n_cb() : s.D) * 4, 256);
 }
 
-// Groups per row of g's tile: from a 16-byte boundary at or before a block's first group to its
-// last.  0 where TMA cannot take g's rows.
-int g_box(const Shape &s, const void *g, int pieces) {
-  const int64_t per = 16 / s.es();
-  if (s.G() % per != 0 || !aligned(g, 16)) return 0;
-  const bool whole = s.d_g % sc::kCh == 0 || sc::kCh % s.d_g == 0;  // blocks start at their groups
-  return static_cast<int>(round_up(whole ? pieces : pieces + per - 1, per));
+// How the groups' rows of g arrive: a tile from a multiple of g_align groups at or before a block's
+// first group to its last.
+void choose_groups(const Shape &s, const void *g, sc::Params *p) {
+  const int per16 = static_cast<int>(16 / s.es()), per4 = static_cast<int>(4 / s.es());
+  p->g_feed = s.G() % per16 == 0 && aligned(g, 16) ? sc::kGroupsTma
+              : s.G() % per4 == 0 && aligned(g, 4) ? sc::kGroupsCopy
+                                                   : sc::kGroupsElement;
+  p->g_align = p->g_feed == sc::kGroupsTma ? per16 : p->g_feed == sc::kGroupsCopy ? per4 : 1;
+  // blocks of 32 channels start at every pieces-th group where those are whole
+  const bool whole = s.d_g % sc::kCh == 0 || sc::kCh % s.d_g == 0;
+  const bool fits = whole && (p->pieces % p->g_align == 0 || p->g_align % p->pieces == 0);
+  p->g_box = static_cast<int>(round_up(fits ? p->pieces : p->pieces + p->g_align - 1, p->g_align));
+  while ((1 << p->copy_bits) * per4 < p->g_box) ++p->copy_bits;
 }
 
 // One tensor [B, L, width] as boxes of `box_w` columns and one tile's rows.
@@ -184,7 +190,7 @@ sc::Params base_params(const Shape &s, const void *g, const hyena::host::DeviceI
                                     : (sc::kCh + s.d_g - 2) / s.d_g + 1;
   while ((1 << p.piece_bits) < p.pieces) ++p.piece_bits;
   p.dg_mode = dg_mode(s);
-  p.g_box = g_box(s, g, p.pieces);
+  if (s.d_g > 1) choose_groups(s, g, &p);
   return p;
 }
 
@@ -195,17 +201,19 @@ struct Launch {
 };
 template <typename C>
 Launch plan(sc::Params &p, int feed, int streams, int first, int count, int sm_count) {
-  if (feed != sc::kTmaGroup && feed != sc::kTmaRaw) p.g_box = 0;
-  const int decays = sc::per_channel(feed)
-                         ? sc::stream_bytes<C>()
-                         : (feed == sc::kTmaRaw ? 0 : sc::decay_bytes<C>(p.pieces)) +
-                               static_cast<int>(round_up(sc::tile_rows<C>() * p.g_box * sizeof(typename C::T),
-                                                         sc::kStageAlign));
+  int decays = sc::stream_bytes<C>();  // a stream of g, or decays and the groups' rows of g
+  if (!sc::per_channel(feed)) {
+    decays = feed == sc::kTmaGroup ? sc::decay_bytes<C>(p.pieces) : 0;
+    if (feed != sc::kTmaGroup || p.g_feed != sc::kGroupsElement)
+      decays += static_cast<int>(round_up(
+          sc::tile_rows<C>() * p.g_box * static_cast<int64_t>(sizeof(typename C::T)), sc::kStageAlign));
+  }
   p.stage_bytes = streams * sc::stream_bytes<C>() + decays;
   // Copies on their way to shared memory hold lines of the L1 cache, which shares its memory: with
   // all of it given to the ring ~9 KB were in flight and the forward of L = 65536, D = 500 took
   // 236 us; with rings of 80 to 180 KB 118 us (D = 496, by TMA: 105).
-  const int room = (sc::by_tma(feed) ? kSmemMax : kCopySmem) - kStaticSmem - sc::kStageAlign;
+  const bool all_tma = sc::by_tma(feed) && (sc::per_channel(feed) || p.g_feed == sc::kGroupsTma);
+  const int room = (all_tma ? kSmemMax : kCopySmem) - kStaticSmem - sc::kStageAlign;
   p.stages = std::max(2, std::min(sc::kMaxStages, room / p.stage_bytes));
   p.unit_split0 = first;
   p.unit_splits = count;
@@ -223,7 +231,7 @@ int run_fwd(const Shape &s, sc::Params p, int first, int count, int sms, cudaStr
   if (sc::by_tma(kFeed)) {
     if (encode(&mk, s, p.k) || encode(&mv, s, p.v) || (kOut && encode(&mq, s, p.q)) ||
         (kFeed == sc::kTmaChannel && encode(&mg, s, p.g)) ||
-        (p.g_box && encode(&mg, s, p.g, s.G(), p.g_box)))
+        (s.d_g > 1 && p.g_feed == sc::kGroupsTma && encode(&mg, s, p.g, s.G(), p.g_box)))
       return HYENA_ERR_CUDA;
   }
   return hyena::host::launch(sc::scan_fwd_kernel<C, kFeed, kOut>, dim3(l.grid),
@@ -240,7 +248,7 @@ int run_bwd(const Shape &s, sc::Params p, int first, int count, int sms, cudaStr
   if (sc::by_tma(kFeed)) {
     if (encode(&mq, s, p.q) || encode(&mdy, s, p.dy) || (kOut && encode(&mk, s, p.k)) ||
         (kOut && encode(&mv, s, p.v)) || (kFeed == sc::kTmaChannel && encode(&mg, s, p.g)) ||
-        (p.g_box && encode(&mg, s, p.g, s.G(), p.g_box)))
+        (s.d_g > 1 && p.g_feed == sc::kGroupsTma && encode(&mg, s, p.g, s.G(), p.g_box)))
       return HYENA_ERR_CUDA;
   }
   return hyena::host::launch(sc::scan_bwd_kernel<C, kFeed, kOut>, dim3(l.grid),
@@ -316,7 +324,7 @@ int choose_feed(const Shape &s, std::initializer_list<const void *> streams,
   const bool tma = bits % 16 == 0 && p->pair_out && s.D * s.es() * s.L < (int64_t{1} << 40) &&
                    (s.d_g == 1 || s.d_g % 2 == 0);
   return tma ? (s.d_g == 1                  ? sc::kTmaChannel
-                : raw && s.d_g <= 4 && p->g_box > 0 ? sc::kTmaRaw
+                : raw && s.d_g <= 4 && p->g_feed != sc::kGroupsElement ? sc::kTmaRaw
                                              : sc::kTmaGroup)
              : (s.d_g == 1 ? sc::kCopyChannel : sc::kCopyGroup);
 }

@@ -57,10 +57,9 @@ __host__ __device__ constexpr bool by_tma(int feed) {
 __host__ __device__ constexpr bool per_channel(int feed) {
   return feed == kTmaChannel || feed == kCopyChannel;
 }
-// One warp feeds all of a tile.
-__host__ __device__ constexpr bool one_feeder(int feed) {
-  return feed == kTmaChannel || feed == kTmaRaw;
-}
+// Groups' rows of g: a tile by TMA; by 4-byte copies where their rows are no multiple of 16 bytes;
+// or element loads (odd numbers of groups in bf16).
+enum GroupFeed { kGroupsElement = 0, kGroupsTma = 1, kGroupsCopy = 2 };
 
 // An element type with R, the rows of a segment (a tile has 16 R).  The joining of segments costs
 // the same per tile whatever R is, so the forward takes as many as its registers allow (B=1 L=8192
@@ -107,7 +106,9 @@ struct Params {
   int n_units;                      // B x unit_splits x n_cb
   int pieces, piece_bits;           // groups a block of 32 channels touches at most; and the
                                     // least power of two that holds them
-  int g_box;                        // groups per row of g's tile (kTmaGroup); 0: element loads
+  int g_feed;                       // how the groups' rows of g arrive (GroupFeed)
+  int copy_bits;                    // least power of two of copies per row of theirs
+  int g_align, g_box;               // their tile starts at a multiple of g_align groups, g_box wide
   int copy;                         // bytes per asynchronous copy: 8, 4, or 0 for element loads
   int pair_out;                     // rows and bases allow stores of two channels
   int stages, stage_bytes;
@@ -294,10 +295,65 @@ __device__ __forceinline__ void load_elements(const Params &p, typename C::T *ds
   }
 }
 
+// The tile of the groups' rows of g by the warps [0, warps): 4-byte copies, or element loads; zeros
+// past the end.
+template <typename C>
+__device__ __forceinline__ void groups_tile(const Params &p, typename C::T *dst, int b, int c0,
+                                            int t0, int warp, int warps) {
+  using T = typename C::T;
+  constexpr int E = 4 / static_cast<int>(sizeof(T));  // groups per copy
+  const int lane = threadIdx.x % 32, x = c0 / p.d_g / p.g_align * p.g_align;
+  const T *g = static_cast<const T *>(p.g) + (static_cast<int64_t>(b) * p.L + t0) * p.G + x;
+  const int rows = p.L - t0;
+  if (p.g_feed == kGroupsCopy) {
+    const int n = p.g_box / E, bits = min(p.copy_bits, 5), per = warps * (32 >> bits);
+    for (int col = lane & ((1 << bits) - 1); col < n; col += 32) {
+      const bool inside = x + col * E < p.G;
+      int row = warp * (32 >> bits) + (lane >> bits);
+      const T *from = g + static_cast<int64_t>(row) * p.G + col * E;
+      uint32_t to = smem_u32(dst + row * p.g_box + col * E);
+      const int64_t step = static_cast<int64_t>(per) * p.G;
+      const uint32_t to_step = per * p.g_box * static_cast<uint32_t>(sizeof(T));
+#pragma unroll 4
+      for (; row < tile_rows<C>(); row += per, from += step, to += to_step) {
+        const bool live = inside && row < rows;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to),
+                     "l"(live ? from : static_cast<const T *>(p.g)), "r"(live ? 4 : 0)
+                     : "memory");
+      }
+    }
+  } else {
+    constexpr int kBatch = 16;  // loads in flight per thread
+    for (int e0 = warp * 32 + lane; e0 < tile_rows<C>() * p.g_box; e0 += kBatch * warps * 32) {
+      T v[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int row = (e0 + i * warps * 32) / p.g_box, gi = e0 + i * warps * 32 - row * p.g_box;
+        v[i] = row < tile_rows<C>() && row < rows && x + gi < p.G
+                   ? g[static_cast<int64_t>(row) * p.G + gi]
+                   : T(0.0f);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (e0 + i * warps * 32 < tile_rows<C>() * p.g_box) dst[e0 + i * warps * 32] = v[i];
+    }
+  }
+}
+
 // Arrives on `bar` when this thread's asynchronous copies so far have landed.
 __device__ __forceinline__ void arrive_after_copies(uint64_t *bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
+}
+
+// Which arrivals a helper thread of a copying feed makes on a tile's barrier.
+template <int kFeed>
+__device__ __forceinline__ bool copy_arrivals(const Params &p) {
+  return p.copy || (!per_channel(kFeed) && p.g_feed == kGroupsCopy);
+}
+template <int kFeed>
+__device__ __forceinline__ bool store_arrivals(const Params &p) {
+  return !p.copy || (!per_channel(kFeed) && p.g_feed == kGroupsElement);
 }
 
 // The helper warps: NS streams of every tile of the CTA's units into the ring, in the order the
@@ -310,10 +366,16 @@ __device__ __forceinline__ void feed(const Params &p, Ring &ring, uint8_t *stage
   const int warp = threadIdx.x / 32 - kComputeThreads / 32, lane = threadIdx.x % 32;
   constexpr int kStreams = NS + (per_channel(kFeed) ? 1 : 0);
   constexpr int kBytes = stream_bytes<C>();
-  constexpr int kGroups = 16 / static_cast<int>(sizeof(T));  // groups in 16 bytes of g
   const int th = threadIdx.x - kComputeThreads;
+  // the groups' warps in a TMA feed: where their rows are copied, warp 1 copies and the rest of the
+  // helpers form decays; all of them copy where the compute warps take the exps
+  const bool copies = p.g_feed == kGroupsCopy;
+  const int converters = kFeed == kTmaGroup ? kHelperWarps - (copies ? 2 : 1) : 0;
+  const int copiers = copies ? kHelperWarps - 1 - converters : 0;
+  const bool converter = warp >= kHelperWarps - converters;
   if (by_tma(kFeed) && warp == 0 && lane != 0) return;
-  if (one_feeder(kFeed) && warp != 0) return;
+  if (kFeed == kTmaChannel && warp != 0) return;
+  if (kFeed == kTmaRaw && warp != 0 && !copies) return;
   int it = 0, last = 0;
   for (int u = blockIdx.x; u < p.n_units; u += gridDim.x) {
     const Unit un(p, u);
@@ -322,39 +384,42 @@ __device__ __forceinline__ void feed(const Params &p, Ring &ring, uint8_t *stage
       const int tile = kReverse ? un.tile1 - 1 - (i - un.tile0) : i, t0 = tile * tile_rows<C>();
       const int st = it % p.stages, round = it / p.stages;
       uint8_t *buf = stages + st * p.stage_bytes;
-      float *as = reinterpret_cast<float *>(buf + NS * kBytes);  // where decays are formed here
+      float *as = reinterpret_cast<float *>(buf + NS * kBytes);  // decays (kTmaGroup)
+      T *graw = reinterpret_cast<T *>(
+          buf + NS * kBytes + (kFeed == kTmaGroup ? decay_bytes<C>(p.pieces) : 0));
+      uint64_t *graw_full = kFeed == kTmaGroup ? &ring.raw[st] : &ring.full[st];
       if (round > 0 && !mbar_wait(&ring.empty[st], (round - 1) & 1, &ring.abort, p.status, kTimeout))
         goto out;
       if (by_tma(kFeed) && warp == 0) {
-        if (kFeed == kTmaGroup && p.g_box) {
-          mbar_arrive_expect_tx(&ring.raw[st], tile_rows<C>() * p.g_box * sizeof(T));
-          tma_load_3d(buf + NS * kBytes + decay_bytes<C>(p.pieces), maps[4], &ring.raw[st],
-                      c0 / p.d_g / kGroups * kGroups, t0, un.b);
+        int bytes = kStreams * kBytes;
+        if (!per_channel(kFeed) && p.g_feed == kGroupsTma) {
+          const int graw_bytes = tile_rows<C>() * p.g_box * static_cast<int>(sizeof(T));
+          if (kFeed == kTmaGroup)
+            mbar_arrive_expect_tx(graw_full, graw_bytes);
+          else
+            bytes += graw_bytes;
         }
-        const int raw = kFeed == kTmaRaw ? tile_rows<C>() * p.g_box * static_cast<int>(sizeof(T)) : 0;
-        mbar_arrive_expect_tx(&ring.full[st], kStreams * kBytes + raw);
-        if (kFeed == kTmaRaw)
-          tma_load_3d(buf + NS * kBytes, maps[4], &ring.full[st], c0 / p.d_g / kGroups * kGroups,
-                      t0, un.b);
+        mbar_arrive_expect_tx(&ring.full[st], bytes);
+        if (!per_channel(kFeed) && p.g_feed == kGroupsTma)
+          tma_load_3d(graw, maps[4], graw_full, c0 / p.d_g / p.g_align * p.g_align, t0, un.b);
 #pragma unroll
         for (int s = 0; s < kStreams; ++s)
           tma_load_3d(buf + s * kBytes, maps[s], &ring.full[st], c0, t0, un.b);
         last = it + 1;
-      }
-      if (kFeed == kTmaGroup && warp > 0) {
-        if (p.g_box) {
-          if (!mbar_wait(&ring.raw[st], round & 1, &ring.abort, p.status, kTimeout)) goto out;
-          convert_decays<C>(p, as,
-                            reinterpret_cast<const T *>(buf + NS * kBytes +
-                                                        decay_bytes<C>(p.pieces)),
-                            c0 / p.d_g % kGroups, warp - 1, kHelperWarps - 1);
+      } else if (by_tma(kFeed) && !per_channel(kFeed) && warp <= copiers) {
+        groups_tile<C>(p, graw, un.b, c0, t0, warp - 1, copiers);
+        arrive_after_copies(graw_full);
+      } else if (kFeed == kTmaGroup && converter) {
+        const int w = warp - (kHelperWarps - converters);
+        if (p.g_feed == kGroupsElement) {
+          fill_decays<C>(p, as, un.b, c0, t0, w, converters);
         } else {
-          fill_decays<C>(p, as, un.b, c0, t0, warp - 1, kHelperWarps - 1);
+          if (!mbar_wait(&ring.raw[st], round & 1, &ring.abort, p.status, kTimeout)) goto out;
+          convert_decays<C>(p, as, graw, c0 / p.d_g % p.g_align, w, converters);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&ring.full[st]);
-      }
-      if (!by_tma(kFeed)) {
+      } else if (!by_tma(kFeed)) {
 #pragma unroll
         for (int s = 0; s < kStreams; ++s) {
           T *dst = reinterpret_cast<T *>(buf + s * kBytes);
@@ -365,10 +430,10 @@ __device__ __forceinline__ void feed(const Params &p, Ring &ring, uint8_t *stage
           else
             load_elements<C>(p, dst, ptrs[s], un.b, c0, t0, th);
         }
-        if (!per_channel(kFeed)) fill_decays<C>(p, as, un.b, c0, t0, warp, kHelperWarps);
+        if (!per_channel(kFeed)) groups_tile<C>(p, graw, un.b, c0, t0, warp, kHelperWarps);
         // one arrival for the copies, and one for what the thread stored itself
-        if (p.copy) arrive_after_copies(&ring.full[st]);
-        if (!p.copy || !per_channel(kFeed)) mbar_arrive(&ring.full[st]);
+        if (copy_arrivals<kFeed>(p)) arrive_after_copies(&ring.full[st]);
+        if (store_arrivals<kFeed>(p)) mbar_arrive(&ring.full[st]);
       }
     }
   }
@@ -377,23 +442,27 @@ out:
   if (by_tma(kFeed) && warp == 0) {
     for (int j = max(0, last - p.stages); j < last; ++j) {
       int no_abort = 0;
-      if (kFeed == kTmaGroup && p.g_box)
+      if (kFeed == kTmaGroup && p.g_feed == kGroupsTma)
         mbar_wait(&ring.raw[j % p.stages], (j / p.stages) & 1, &no_abort, p.status, kTimeout);
       mbar_wait(&ring.full[j % p.stages], (j / p.stages) & 1, &no_abort, p.status, kTimeout);
     }
   }
-  if (!by_tma(kFeed)) asm volatile("cp.async.wait_all;" ::: "memory");
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 template <int kFeed>
 __device__ __forceinline__ void ring_init(const Params &p, Ring &ring) {
   if (threadIdx.x == 0) {
-    const int arrivals = by_tma(kFeed) ? (one_feeder(kFeed) ? 1 : kHelperWarps)
-                                       : 32 * kHelperWarps * (p.copy && !per_channel(kFeed) ? 2 : 1);
+    const bool copies = p.g_feed == kGroupsCopy;
+    int arrivals = 1;  // the TMA warp
+    if (kFeed == kTmaGroup) arrivals += kHelperWarps - (copies ? 2 : 1);
+    if (kFeed == kTmaRaw && copies) arrivals += 32 * (kHelperWarps - 1);
+    if (!by_tma(kFeed))
+      arrivals = 32 * kHelperWarps * (copy_arrivals<kFeed>(p) + store_arrivals<kFeed>(p));
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&ring.full[i], arrivals);
       mbar_init(&ring.empty[i], kComputeThreads / 32);
-      mbar_init(&ring.raw[i], 1);
+      mbar_init(&ring.raw[i], copies ? 32 : 1);
     }
     ring.abort = 0;
     fence_mbar_init();
@@ -438,9 +507,8 @@ struct Decays<C, kTmaRaw, false> {  // the same, from the tile of g's rows
   const T *at;
   int step;
   __device__ Decays(const Params &p, const uint8_t *tile, int seg, int l, int c0) {
-    constexpr int kGroups = 16 / static_cast<int>(sizeof(T));
     const int c = min(c0 + 2 * l, p.D - 1), g0 = c0 / p.d_g;
-    at = reinterpret_cast<const T *>(tile) + seg * C::R * p.g_box + g0 % kGroups + c / p.d_g -
+    at = reinterpret_cast<const T *>(tile) + seg * C::R * p.g_box + g0 % p.g_align + c / p.d_g -
          g0;
     step = p.g_box;
   }
@@ -448,17 +516,21 @@ struct Decays<C, kTmaRaw, false> {  // the same, from the tile of g's rows
   __device__ static F2 pair(Held a) { return pack(a, a); }
 };
 template <typename C>
-struct Decays<C, kCopyGroup, false> {
+struct Decays<C, kCopyGroup, false> {  // any d_g
+  using T = typename C::T;
   using Held = F2;
-  const float *at;
+  const T *at;
   int step, second;
   __device__ Decays(const Params &p, const uint8_t *tile, int seg, int l, int c0) {
     const int g0 = c0 / p.d_g, i0 = min(c0 + 2 * l, p.D - 1) / p.d_g - g0;
-    at = reinterpret_cast<const float *>(tile) + seg * C::R * p.pieces + i0;
+    at = reinterpret_cast<const T *>(tile) + seg * C::R * p.g_box + g0 % p.g_align + i0;
     second = min(c0 + 2 * l + 1, p.D - 1) / p.d_g - g0 - i0;
-    step = p.pieces;
+    step = p.g_box;
   }
-  __device__ Held load(int r) const { return pack(at[r * step], at[r * step + second]); }
+  __device__ Held load(int r) const {
+    const float a = decay(load_one(at + r * step));
+    return pack(a, second ? decay(load_one(at + r * step + second)) : a);
+  }
   __device__ static F2 pair(Held a) { return a; }
 };
 

@@ -42,7 +42,9 @@ SHAPES = [
     (2, 177, 64, 64), (1, 111, 96, 96), (1, 112, 128, 128), (2, 113, 72, 2), (1, 353, 200, 8),
     (2, 1000, 96, 48), (1, 700, 36, 3), (1, 401, 33, 1), (2, 333, 35, 5), (1, 260, 7, 7),
     (1, 300, 1, 1), (1, 143, 64, 4), (2, 144, 64, 2), (1, 145, 128, 32), (1, 289, 264, 4),
-    (2, 300, 66, 2), (1, 700, 100, 2), (1, 5000, 32, 1), (1, 4000, 72, 24), (5, 190, 1024, 1), (160, 3, 64, 32),
+    (2, 300, 66, 2), (1, 700, 100, 2),
+    (2, 200, 1732, 2), (1, 310, 440, 8), (1, 300, 488, 8), (1, 200, 272, 16), (2, 180, 192, 96),
+    (1, 200, 208, 4), (1, 150, 24, 2), (1, 330, 50, 10), (1, 5000, 32, 1), (1, 4000, 72, 24), (5, 190, 1024, 1), (160, 3, 64, 32),
 ]
 
 
