@@ -244,22 +244,27 @@ int product(const Operand &a, const Operand &b, int64_t K, pj::Params p, int dty
              : HYENA_ERR_CUDA;
 }
 
-// An input as a product's operand: itself, or (`at` advances) bf16 planes in the workspace.
+// Up to two inputs of one row length as operands: themselves, or (`at` advances) bf16 planes in
+// the workspace.  Rows 0: none.
 template <typename T>
-int operand(Operand *o, const void *ptr, int64_t rows, int64_t cols, int dtype, uint8_t *&at,
-            const Device &d, cudaStream_t stream) {
-  if (!needs_pack(cols, dtype)) {
-    *o = Operand{ptr, rows, cols, cols};
-    return HYENA_OK;
-  }
-  const int64_t ld = round_up(cols, 8), n = rows * (ld / 8);
-  *o = Operand{at, rows, cols, ld};
+int operands(Operand *a, const void *pa, int64_t ra, Operand *b, const void *pb, int64_t rb,
+             int64_t cols, int dtype, uint8_t *&at, const Device &d, cudaStream_t stream) {
+  *a = Operand{pa, ra, cols, cols};
+  *b = Operand{pb, rb, cols, cols};
+  if (!needs_pack(cols, dtype)) return HYENA_OK;
+  const int64_t ld = round_up(cols, 8), n = (ra + rb) * (ld / 8);
+  const auto place = [&](Operand *o, const void *ptr, int64_t rows) {
+    const pj::Pack<T> p{static_cast<const T *>(ptr), reinterpret_cast<__nv_bfloat16 *>(at), rows};
+    *o = Operand{at, rows, cols, ld};
+    at += pack_bytes(rows, cols, dtype);
+    return p;
+  };
+  const pj::Pack<T> ka = place(a, pa, ra), kb = place(b, pb, rb);
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>((n + 255) / 256, 16 * d.info.sm_count));
-  const cudaError_t e = hyena::host::launch(
-      pj::proj_pack_kernel<T>, dim3(grid), dim3(256), 0, stream, static_cast<const T *>(ptr),
-      reinterpret_cast<__nv_bfloat16 *>(at), rows, static_cast<int>(cols), static_cast<int>(ld));
-  at += pack_bytes(rows, cols, dtype);
-  return e == cudaSuccess ? HYENA_OK : HYENA_ERR_CUDA;
+  return hyena::host::launch(pj::proj_pack_kernel<T>, dim3(grid), dim3(256), 0, stream, ka, kb,
+                             static_cast<int>(cols), static_cast<int>(ld)) == cudaSuccess
+             ? HYENA_OK
+             : HYENA_ERR_CUDA;
 }
 
 int check_shape(int64_t M, int64_t N, int64_t K, int dtype) {
@@ -287,26 +292,30 @@ template <typename T>
 int forward(const void *x, const void *w, const pj::Params &p, int64_t K, int dtype, uint8_t *ws,
             const Device &d, cudaStream_t stream) {
   Operand a, b;
-  int rc = operand<T>(&a, x, p.M, K, dtype, ws, d, stream);
-  if (rc == HYENA_OK) rc = operand<T>(&b, w, p.N, K, dtype, ws, d, stream);
+  const int rc = operands<T>(&a, x, p.M, &b, w, p.N, K, dtype, ws, d, stream);
   if (rc != HYENA_OK) return rc;
   return product<T, false, false>(a, b, K, p, dtype, reinterpret_cast<float *>(ws), d, stream);
 }
+
+// Rows whose sum a CTA of the dz kernel leaves: all of them where they are few, which spares the
+// kernel that adds up the blocks.
+int64_t db_rows(int64_t M) { return M <= 512 ? 512 : 128; }
+int64_t db_blocks(int64_t M) { return (M + db_rows(M) - 1) / db_rows(M); }
 
 template <typename T, int kAct>
 cudaError_t launch_dz(const void *dy, const void *z, __nv_bfloat16 *dz, float *part, int64_t M,
                       int64_t N, int64_t ld, int vec, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>((ld + pj::kDbCols - 1) / pj::kDbCols),
-                  static_cast<unsigned>((M + pj::kDbRows - 1) / pj::kDbRows));
+                  static_cast<unsigned>(db_blocks(M)));
   return hyena::host::launch(pj::proj_dz_kernel<T, kAct>, grid, dim3(256), 0, stream,
                              static_cast<const T *>(dy), static_cast<const T *>(z), dz, part, M,
-                             static_cast<int>(N), static_cast<int>(ld), vec);
+                             static_cast<int>(N), static_cast<int>(ld), vec,
+                             static_cast<int>(db_rows(M)));
 }
 
 bool needs_dz(int64_t N, int act, int dtype) {
   return act != HYENA_ACT_NONE || needs_pack(N, dtype);
 }
-int64_t db_blocks(int64_t M) { return (M + pj::kDbRows - 1) / pj::kDbRows; }
 
 template <typename T>
 int backward(const void *x, const void *w, const void *z, const void *dy, const void *dx_add,
@@ -324,7 +333,7 @@ int backward(const void *x, const void *w, const void *z, const void *dy, const 
     }
     float *part = nullptr;
     if (db) {
-      part = reinterpret_cast<float *>(ws);
+      part = db_blocks(M) > 1 ? reinterpret_cast<float *>(ws) : db;
       ws += round_up(db_blocks(M) * N * 4, 256);
     }
     const int vec = N % (16 / elem(dtype)) == 0 ? 1 : 0;
@@ -340,7 +349,7 @@ int backward(const void *x, const void *w, const void *z, const void *dy, const 
         break;
       default: e = launch_dz<T, pj::kNone>(dy, z, dz, part, M, N, ld, vec, stream);
     }
-    if (e == cudaSuccess && db)
+    if (e == cudaSuccess && db && db_blocks(M) > 1)
       e = hyena::host::launch(pj::proj_db_kernel, dim3(static_cast<unsigned>((N + 31) / 32)),
                               dim3(256), 0, stream, static_cast<const float *>(part), db,
                               static_cast<int>(db_blocks(M)), static_cast<int>(N));
@@ -350,28 +359,25 @@ int backward(const void *x, const void *w, const void *z, const void *dy, const 
   p.status = d.info.status;
   p.act = pj::kNone;
   int rc = HYENA_OK;
-  if (dx) {  // [M, K] = dz [M, N] w [N, K]
-    Operand wo;
-    uint8_t *at = ws;
-    rc = operand<T>(&wo, w, N, K, dtype, at, d, stream);
+  Operand xo, wo;
+  if (dx || dw) {
+    rc = operands<T>(&xo, x, dw ? M : 0, &wo, w, dx ? N : 0, K, dtype, ws, d, stream);
     if (rc != HYENA_OK) return rc;
+  }
+  if (dx) {  // [M, K] = dz [M, N] w [N, K]
     p.M = static_cast<int>(M);
     p.N = static_cast<int>(K);
     p.residual = dx_add;
     p.y = dx;
-    rc = product<T, false, true>(dzo, wo, N, p, dtype, reinterpret_cast<float *>(at), d, stream);
+    rc = product<T, false, true>(dzo, wo, N, p, dtype, reinterpret_cast<float *>(ws), d, stream);
     if (rc != HYENA_OK) return rc;
   }
   if (dw) {  // [N, K] = dz^T [N, M] x [M, K]
-    Operand xo;
-    uint8_t *at = ws;
-    rc = operand<T>(&xo, x, M, K, dtype, at, d, stream);
-    if (rc != HYENA_OK) return rc;
     p.M = static_cast<int>(N);
     p.N = static_cast<int>(K);
     p.residual = nullptr;
     p.y = dw;
-    rc = product<T, true, true>(dzo, xo, M, p, dtype, reinterpret_cast<float *>(at), d, stream);
+    rc = product<T, true, true>(dzo, xo, M, p, dtype, reinterpret_cast<float *>(ws), d, stream);
   }
   return rc;
 }
@@ -400,11 +406,9 @@ int64_t hyena_proj_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int act,
   if (M == 0) return 0;
   int64_t n = round_up(db_blocks(M) * N * 4, 256);
   if (needs_dz(N, act, dtype)) n += pack_bytes(M, N, dtype);
-  // the two products run one after the other in the same room
-  const bool pack = needs_pack(K, dtype);
-  const int64_t for_dx = (pack ? pack_bytes(N, K, dtype) : 0) + partial_bytes(M, K, N, dtype);
-  const int64_t for_dw = (pack ? pack_bytes(M, K, dtype) : 0) + partial_bytes(N, K, M, dtype);
-  return n + std::max(for_dx, for_dw);
+  if (needs_pack(K, dtype)) n += pack_bytes(M, K, dtype) + pack_bytes(N, K, dtype);
+  // the two products run one after the other and share the room for partial sums
+  return n + std::max(partial_bytes(M, K, N, dtype), partial_bytes(N, K, M, dtype));
 }
 
 int hyena_proj_fwd(const void *x, const void *w, const float *bias, const void *residual, void *y,

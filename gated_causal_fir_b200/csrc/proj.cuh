@@ -97,9 +97,35 @@ template <typename T> __device__ __forceinline__ float sigmoid_of(float z) {
   return ratio<T>(1.0f, 1.0f + exp_of<T>(-z));
 }
 
+// 1 - Phi(|z|), times 2, from the exponential e = exp(-z^2 / 2): the rational approximation 7.1.26 of
+// Abramowitz and Stegun's handbook (1964) to erf, within 1.5e-7.  For bf16 results: half the
+// instructions of erff, which bound the epilogue of products over few k.
+__device__ __forceinline__ float erfc_of(float z, float e) {
+  const float t = __fdividef(1.0f, fmaf(0.3275911f * 0.70710678f, fabsf(z), 1.0f));
+  float p = fmaf(1.061405429f, t, -1.453152027f);
+  p = fmaf(p, t, 1.421413741f);
+  p = fmaf(p, t, -0.284496736f);
+  p = fmaf(p, t, 0.254829592f);
+  return p * t * e;
+}
+template <typename T>
+__device__ __forceinline__ float gelu_of(float z) {
+  if constexpr (sizeof(T) == 4) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
+  const float half = 0.5f * z * erfc_of(z, __expf(-0.5f * z * z));  // z (1 - Phi(|z|))
+  return z > 0.0f ? z - half : half;
+}
+template <typename T>
+__device__ __forceinline__ float gelu_slope(float z) {
+  const float e = exp_of<T>(-0.5f * z * z);
+  if constexpr (sizeof(T) == 4)
+    return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * 0.39894228f * e;
+  const float tail = 0.5f * erfc_of(z, e);
+  return fmaf(z * 0.39894228f, e, z > 0.0f ? 1.0f - tail : tail);
+}
+
 template <typename T, int kAct>
 __device__ __forceinline__ float act_of(float z) {
-  if constexpr (kAct == kGelu) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
+  if constexpr (kAct == kGelu) return gelu_of<T>(z);
   if constexpr (kAct == kSilu) return ratio<T>(z, 1.0f + exp_of<T>(-z));
   if constexpr (kAct == kSigmoid) return sigmoid_of<T>(z);
   if constexpr (kAct == kLogSigmoid) return fminf(z, 0.0f) - log1pf(exp_of<T>(-fabsf(z)));
@@ -108,8 +134,7 @@ __device__ __forceinline__ float act_of(float z) {
 
 template <typename T, int kAct>
 __device__ __forceinline__ float act_slope(float z) {
-  if constexpr (kAct == kGelu)
-    return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * 0.39894228f * exp_of<T>(-0.5f * z * z);
+  if constexpr (kAct == kGelu) return gelu_slope<T>(z);
   if constexpr (kAct == kSilu) {
     const float p = sigmoid_of<T>(z);
     return p * (1.0f + z * (1.0f - p));
@@ -703,49 +728,62 @@ __device__ __forceinline__ void planes_of(float x, __nv_bfloat16 (&o)[kPlanes]) 
 }
 
 // Rows of `cols` elements as rows of `ld` bf16 (a multiple of 8, zero past cols): one plane for
-// bf16, three for fp32.  Eight elements of a row per thread.
+// bf16, three for fp32.  Eight elements of a row per thread; one launch for up to two operands of
+// the same row length.
+template <typename T>
+struct Pack {
+  const T *src;
+  __nv_bfloat16 *dst;
+  int64_t rows;
+};
 template <typename T>
 __global__ void __launch_bounds__(256)
-    proj_pack_kernel(const T *src, __nv_bfloat16 *dst, int64_t rows, int cols, int ld) {
+    proj_pack_kernel(const Pack<T> a, const Pack<T> b, int cols, int ld) {
   constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
   griddep_launch_dependents();
   griddep_wait();
   const int per_row = ld / 8;
-  const int64_t n = rows * per_row, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  const int64_t n = (a.rows + b.rows) * per_row, step = static_cast<int64_t>(gridDim.x) * blockDim.x;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) {
-    const int64_t row = i / per_row;
+    int64_t row = i / per_row;
     const int col = static_cast<int>(i - row * per_row) * 8;
-    VecOf<__nv_bfloat16, 8> o[kPlanes];
+    const bool second = row >= a.rows;
+    const Pack<T> &o = second ? b : a;
+    if (second) row -= a.rows;
+    VecOf<__nv_bfloat16, 8> out[kPlanes];
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = col + e < cols ? to_f(o.src[row * cols + col + e]) : 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       __nv_bfloat16 pl[kPlanes];
-      planes_of<kPlanes>(col + e < cols ? to_f(src[row * cols + col + e]) : 0.0f, pl);
+      planes_of<kPlanes>(v[e], pl);
 #pragma unroll
-      for (int q = 0; q < kPlanes; ++q) o[q].e[e] = pl[q];
+      for (int q = 0; q < kPlanes; ++q) out[q].e[e] = pl[q];
     }
 #pragma unroll
     for (int q = 0; q < kPlanes; ++q)
-      *reinterpret_cast<VecOf<__nv_bfloat16, 8> *>(dst + (q * rows + row) * ld + col) = o[q];
+      *reinterpret_cast<VecOf<__nv_bfloat16, 8> *>(o.dst + (q * o.rows + row) * ld + col) = out[q];
   }
 }
 
 // dz = dy act'(z) as a product's operand (planes and row length as above; null where dy itself
-// serves) and its column sums over kDbRows rows, part[row block][N].  A CTA takes 64 columns:
-// 8 threads of 8 columns x 32 rows at a time.
-constexpr int kDbRows = 128, kDbCols = 64;
+// serves) and its column sums over `block_rows` rows, part[row block][N] (db itself where there is
+// one block).  A CTA takes 64 columns: 8 threads of 8 columns x 32 rows at a time.
+constexpr int kDbCols = 64;
 template <typename T, int kAct>
 __global__ void __launch_bounds__(256)
     proj_dz_kernel(const T *dy, const T *z, __nv_bfloat16 *dz, float *part, int64_t M, int N,
-                   int ld, int vec) {
+                   int ld, int vec, int block_rows) {
   constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1, V = 16 / static_cast<int>(sizeof(T));
   __shared__ float sums[32][kDbCols + 1];
   griddep_launch_dependents();
   griddep_wait();
   const int c8 = threadIdx.x % 8, rr = threadIdx.x / 8;
   const int col = blockIdx.x * kDbCols + c8 * 8;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.y) * kDbRows;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.y) * block_rows;
   float sum[8] = {};
-  for (int r = rr; r < kDbRows; r += 32) {
+  for (int r = rr; r < block_rows; r += 32) {
     const int64_t row = row0 + r;
     if (row >= M || col >= ld) break;
     float d[8];
