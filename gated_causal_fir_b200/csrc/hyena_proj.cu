@@ -28,10 +28,12 @@ enum Shape { kPair256 = 0, kOne128 = 1, kOne64 = 2 };
 
 struct TileShape {
   int m, n, workers;
-  double block, tail;  // ns per k-block of 64, and per tile outside its k-blocks
+  double block, tail, epi;  // ns per k-block of 64; outside the k-blocks; per tile's epilogue
 };
 constexpr TileShape kShapes[] = {  // times measured on products of 16..8192 rows and columns
-    {256, 256, kSms / 2, 340, 5000}, {128, 128, kSms, 230, 3200}, {128, 64, kSms, 185, 2600}};
+    {256, 256, kSms / 2, 340, 5000, 3000},
+    {128, 128, kSms, 230, 3200, 1500},
+    {128, 64, kSms, 185, 2600, 900}};
 
 struct Plan {
   int shape, splits, kb, pairs, per;  // per: blocks per cut
@@ -55,8 +57,9 @@ Plan find_plan(int64_t M, int64_t N, int64_t K, int dtype) {
       const int64_t per = (total + want - 1) / want;
       const int splits = static_cast<int>((total + per - 1) / per);
       if (splits != want || (want > 1 && (per < 4 || rest * want > t.workers))) continue;
-      double ns = static_cast<double>(whole / t.workers) * (static_cast<double>(total) * t.block) +
-                  (rest ? static_cast<double>(per) * t.block : 0) + t.tail;
+      // a tile's k-blocks run beside the epilogue of the one before it
+      double ns = static_cast<double>(whole / t.workers) * std::max(static_cast<double>(total) * t.block, t.epi) +
+                  (rest ? std::max(static_cast<double>(per) * t.block, whole ? t.epi : 0.0) : 0) + t.tail;
       if (splits > 1)  // the second kernel, and the partial sums' way to it and back
         ns += 3000 + static_cast<double>(rest * splits) * std::min<int64_t>(M, t.m) * t.n * 4 / 4500;
       if (best_ns == 0 || ns < best_ns) {
@@ -113,6 +116,20 @@ int encode(CUtensorMap *m, const Operand &o, int n_planes, int box_rows) {
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(o.ptr), dims, strides, box,
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? HYENA_OK
+             : HYENA_ERR_CUDA;
+}
+
+// An output (or residual) [M, N] of bf16 as the epilogue's chunks of 32 x 32.
+int encode_out(CUtensorMap *m, const void *ptr, int64_t M, int64_t N) {
+  hyena::host::EncodeTiledFn enc = hyena::host::encode_tiled();
+  if (!enc) return HYENA_ERR_CUDA;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M), 1};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(N) * 2, static_cast<cuuint64_t>(M * N) * 2};
+  const cuuint32_t box[3] = {pj::kChunk, 32, 1}, estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? HYENA_OK
              : HYENA_ERR_CUDA;
 }
@@ -176,8 +193,8 @@ int prepare_device(Device *d) {
 }
 
 template <typename T, int kCG, int kBN, bool kAMn, bool kBMn>
-cudaError_t launch_shape(const CUtensorMap &ma, const CUtensorMap &mb, const pj::Params &p,
-                         const Device &d, cudaStream_t stream) {
+cudaError_t launch_shape(const CUtensorMap (&m)[5], const pj::Params &p, const Device &d,
+                         cudaStream_t stream) {
   using L = pj::Tile<kCG, kBN>;
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
   const int64_t works = p.whole + (tiles - p.whole) * p.splits;
@@ -194,7 +211,8 @@ cudaError_t launch_shape(const CUtensorMap &ma, const CUtensorMap &mb, const pj:
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = kCG == 2 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, pj::proj_kernel<T, kCG, kBN, kAMn, kBMn>, ma, mb, p);
+  return cudaLaunchKernelEx(&cfg, pj::proj_kernel<T, kCG, kBN, kAMn, kBMn>, m[0], m[1], m[2], m[3],
+                            m[4], p);
 }
 
 // C = A B^T with its epilogue.  p: outputs, epilogue and status; K: the reduced dimension.  a, b:
@@ -216,22 +234,27 @@ int product(const Operand &a, const Operand &b, int64_t K, pj::Params p, int dty
   p.partial = partial;
   const int64_t per16 = 16 / elem(dtype);
   p.vec = p.N % per16 == 0 && aligned(p.y, 16) && aligned(p.z, 16) && aligned(p.residual, 16);
-  CUtensorMap ma, mb;
+  p.bias_vec = aligned(p.bias, 16);
+  p.tma = sizeof(T) == 2 && p.vec && p.whole > 0 && !(p.z && p.residual);
+  CUtensorMap m[5] = {};  // A, B, y, z, residual
   const int b_rows = pl.shape == kOne64 ? 64 : 128;
-  if (encode(&ma, a, planes(dtype), kAMn ? 64 : pj::kRows) ||
-      encode(&mb, b, planes(dtype), kBMn ? 64 : b_rows))
+  if (encode(&m[0], a, planes(dtype), kAMn ? 64 : pj::kRows) ||
+      encode(&m[1], b, planes(dtype), kBMn ? 64 : b_rows) ||
+      (p.tma && encode_out(&m[2], p.y, p.M, p.N)) ||
+      (p.tma && p.z && encode_out(&m[3], p.z, p.M, p.N)) ||
+      (p.tma && p.residual && encode_out(&m[4], p.residual, p.M, p.N)))
     return HYENA_ERR_CUDA;
   cudaError_t e;
   switch (pl.shape) {
     case kPair256:
       if constexpr (sizeof(T) == 2) {
-        e = launch_shape<T, 2, 256, kAMn, kBMn>(ma, mb, p, d, stream);
+        e = launch_shape<T, 2, 256, kAMn, kBMn>(m, p, d, stream);
         break;
       } else {
         return HYENA_ERR_UNSUPPORTED;  // not planned for fp32
       }
-    case kOne128: e = launch_shape<T, 1, 128, kAMn, kBMn>(ma, mb, p, d, stream); break;
-    default: e = launch_shape<T, 1, 64, kAMn, kBMn>(ma, mb, p, d, stream);
+    case kOne128: e = launch_shape<T, 1, 128, kAMn, kBMn>(m, p, d, stream); break;
+    default: e = launch_shape<T, 1, 64, kAMn, kBMn>(m, p, d, stream);
   }
   if (e != cudaSuccess) return HYENA_ERR_CUDA;
   if (p.splits == 1) return HYENA_OK;

@@ -81,6 +81,8 @@ struct Params {
   void *y, *z;                  // [M, N]; z (before the activation) or null
   float *partial;               // [other tiles][splits][tile] when splits > 1
   int act;
+  int tma;                      // whole tiles leave by TMA
+  int bias_vec;                 // bias is 16-byte aligned
   int vec;                      // rows of y, z, residual are whole, aligned 16-byte vectors
   unsigned int *status;
 };
@@ -367,12 +369,14 @@ __device__ __forceinline__ Work work_at(const Params &p, int w) {
 template <typename T, int kCG, int kBN, bool kAMn, bool kBMn>
 __global__ void __launch_bounds__(kThreads, 1)
     proj_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
-                const Params p) {
+                const __grid_constant__ CUtensorMap my, const __grid_constant__ CUtensorMap mz,
+                const __grid_constant__ CUtensorMap mr, const Params p) {
   using L = Tile<kCG, kBN>;
   constexpr bool kPromote = sizeof(T) == 4;
   static_assert(!kPromote || kCG == 1, "the sums of a pair's tile do not fit the registers");
   extern __shared__ uint8_t dynamic[];
   __shared__ uint64_t full[L::kStages], empty[L::kStages], acc_full[2], acc_empty[2];
+  __shared__ uint64_t res_full[kEpiWarps];
   __shared__ uint32_t tmem_at;
   __shared__ int abort;
   uint8_t *stages = dynamic + (1024 - smem_u32(dynamic) % 1024) % 1024;
@@ -387,6 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], kEpiWarps * kCG);
     }
+    for (int i = 0; i < kEpiWarps; ++i) mbar_init(&res_full[i], 1);
     abort = 0;
     fence_mbar_init();
   }
@@ -539,6 +544,64 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&acc_empty[acc]);
       }
     };
+    // Whole bf16 tiles leave by TMA: a chunk of 32 x 32 outputs is finished in registers (a lane
+    // has a row), written to one of two buffers in the layout of the 64-byte swizzle and stored from
+    // there; a residual comes into the buffer the same way, a chunk ahead, and is overwritten in
+    // place.  (Through fp32 staging and plain stores the epilogue took three times as long, which
+    // is what products over few k are bound by.)
+    uint8_t *bufs = reinterpret_cast<uint8_t *>(out);
+    uint64_t *res_bar = &res_full[warp - 2];
+    [[maybe_unused]] uint64_t once = 0;  // L2 policy of what is read or written once
+    [[maybe_unused]] uint32_t writes = 0, res_seen = 0;
+    if constexpr (!kPromote)
+      asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
+    // Requests the residual of the chunk at column c0 of work k into the buffer of write `at`; the
+    // stores so far have read their buffers.
+    const auto request = [&](const Work &k, int c0, uint32_t at) {
+      if (lane == 0) {
+        mbar_arrive_expect_tx(res_bar, 2048);
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(
+                smem_u32(bufs + (at & 1) * 2048)),
+            "l"(reinterpret_cast<uint64_t>(&mr)), "r"(smem_u32(res_bar)),
+            "r"(k.n * L::kN + col0 + c0),
+            "r"(k.m * L::kM + static_cast<int>(rank) * kRows + quad * 32), "r"(0), "l"(once)
+            : "memory");
+      }
+    };
+    // Stores the rows that the lanes hold at (row0, col) from the buffer of the next write.
+    const auto store = [&](const CUtensorMap *map, const float (&v)[32], int row0, int col) {
+      uint8_t *buf = bufs + (writes & 1) * 2048;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * j + 2 * e], v[8 * j + 2 * e + 1]);
+          o[e] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+        *reinterpret_cast<uint4 *>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) * 16)) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (col < p.N && row0 < p.M)
+          asm volatile(
+              "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group.L2::cache_hint"
+              " [%0, {%2, %3, %4}], [%1], %5;" ::"l"(reinterpret_cast<uint64_t>(map)),
+              "r"(smem_u32(buf)), "r"(col), "r"(row0), "r"(0), "l"(once)
+              : "memory");
+        bulk_commit_group();
+      }
+      ++writes;
+    };
+    const bool ahead = p.tma && p.residual;  // residuals are requested a chunk ahead
+    if (!kPromote && ahead && first < works) {
+      const Work k = work_at(p, first);
+      if (k.part < 0) request(k, 0, 0);
+    }
     int n = 0;
     bool ok = true;
     for (int w = first; w < works && ok; w += step) {
@@ -569,24 +632,97 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after_sync();
       }
       if (!ok) break;
-      constexpr int V = 16 / static_cast<int>(sizeof(T));
-      const bool wide = p.vec && k.part < 0;
+      if constexpr (!kPromote) {
+        if (p.tma && k.part < 0) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < kBN / 2 && ok; c0 += kChunk) {
+            const bool last = c0 + kChunk >= kBN / 2;
+            const int col = k.n * L::kN + col0 + c0;
+            float v[32];
+            {
+              uint32_t r[32];
+              tmem_ld_32x32b_x32(lanes + (n & 1) * kBN + c0, r);
+              tmem_wait_ld();
+              reg_fence(r);
+              if (last) release(n & 1);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]);
+            }
+            if (p.bias) {  // N is a multiple of 8: pieces of 4 are inside or outside
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                if (col + e >= p.N) break;
+                if (p.bias_vec) {
+                  const float4 b = *reinterpret_cast<const float4 *>(p.bias + col + e);
+                  v[e] += b.x, v[e + 1] += b.y, v[e + 2] += b.z, v[e + 3] += b.w;
+                } else {
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) v[e + i] += p.bias[col + e + i];
+                }
+              }
+            }
+            if (p.z) {  // (never with a residual here: the buffers are the stores' alone)
+              if (lane == 0) bulk_wait_group_read<1>();
+              __syncwarp();
+              store(&mz, v, row0, col);
+            }
+            with_act(p.act, [&](auto act) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] = act_of<T, decltype(act)::value>(v[e]);
+            });
+            if (p.residual) {
+              ok = wait(res_bar, res_seen++ & 1);
+              const uint8_t *buf = bufs + (writes & 1) * 2048;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint4 u =
+                    *reinterpret_cast<const uint4 *>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) * 16));
+                const uint32_t word[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  v[8 * j + 2 * e] += __uint_as_float(word[e] << 16);
+                  v[8 * j + 2 * e + 1] += __uint_as_float(word[e] & 0xffff0000u);
+                }
+              }
+              if (lane == 0) bulk_wait_group_read<0>();
+              __syncwarp();
+              if (!last) {
+                request(k, c0 + kChunk, writes + 1);
+              } else if (w + step < works) {
+                const Work next = work_at(p, w + step);
+                if (next.part < 0) request(next, 0, writes + 1);
+              }
+            } else {
+              if (lane == 0) bulk_wait_group_read<1>();
+              __syncwarp();
+            }
+            if (ok) store(&my, v, row0, col);
+          }
+          ++n;
+          continue;
+        }
+        // the staging below takes both buffers
+        if (lane == 0) bulk_wait_group_read<0>();
+        __syncwarp();
+      }
+      const bool wide = kPromote && p.vec && k.part < 0;
 #pragma unroll(kPromote ? kBN / 2 / kChunk : 1)
       for (int c0 = 0; c0 < kBN / 2; c0 += kChunk) {
-        // phase 2 of this chunk: lane -> rows 8 i + lane / 4, columns col .. col + 7
+        // phase 2: lane -> rows 8 i + lane / 4, columns col .. col + 7 of the warp's 32 rows
         const int in_tile = col0 + c0 + (lane % 4) * 8, col = k.n * L::kN + in_tile;
+        const bool last = c0 + kChunk >= kBN / 2;
+        constexpr int V = 16 / static_cast<int>(sizeof(T));
         const int sub = lane / 4;
-        VecOf<T, 8> res[4];  // the residual, requested before the accumulator is waited for
+        [[maybe_unused]] VecOf<T, 8> res[4];  // requested before the accumulator is touched
         if (wide && p.residual) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = row0 + 8 * i + sub;
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int h = 0; h < 8; h += V)
-              if (row < p.M && col + h < p.N)
-                *reinterpret_cast<VecOf<T, V> *>(&res[i].e[h]) = load_once<T, V>(
-                    static_cast<const T *>(p.residual) + static_cast<int64_t>(row) * p.N + col + h);
-          }
+              if (row0 + 8 * i + sub < p.M && col + h < p.N)
+                *reinterpret_cast<VecOf<T, V> *>(&res[i].e[h]) =
+                    load_once<T, V>(static_cast<const T *>(p.residual) +
+                                    static_cast<int64_t>(row0 + 8 * i + sub) * p.N + col + h);
         }
         float bias[8];
 #pragma unroll
@@ -601,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_32x32b_x32(lanes + (n & 1) * kBN + c0, r);
           tmem_wait_ld();
           reg_fence(r);
-          if (c0 + kChunk >= kBN / 2) release(n & 1);
+          if (last) release(n & 1);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -616,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           c[0] = u.x + bias[0], c[1] = u.y + bias[1], c[2] = u.z + bias[2], c[3] = u.w + bias[3];
           c[4] = v.x + bias[4], c[5] = v.y + bias[5], c[6] = v.z + bias[6], c[7] = v.w + bias[7];
         };
-        if (wide) {
+        if (kPromote && wide) {
           with_act(p.act, [&](auto act) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -665,6 +801,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       if (!kPromote) ++n;
+    }
+    if constexpr (!kPromote) {
+      if (lane == 0) {
+        bulk_wait_group<0>();
+        // a residual requested for a chunk that a failed wait kept from being read
+        int no_abort = 0;
+        if (!ok && ahead) mbar_wait(res_bar, res_seen & 1, &no_abort, p.status, kTimeout);
+      }
+      __syncwarp();
     }
   }
   // Both CTAs' MMAs read each other's shared memory and signal each other's barriers.
