@@ -9,7 +9,7 @@ from . import _native
 from ._native import HYENA_DTYPE_BF16, HYENA_DTYPE_F32
 
 _TORCH = None
-_CODES = {}
+CODES = {}
 _FUNCTIONS = {}
 
 
@@ -17,7 +17,7 @@ def torch_():
     global _TORCH
     if _TORCH is None:
         import torch
-        _CODES.update({torch.bfloat16: HYENA_DTYPE_BF16, torch.float32: HYENA_DTYPE_F32})
+        CODES.update({torch.bfloat16: HYENA_DTYPE_BF16, torch.float32: HYENA_DTYPE_F32})
         _TORCH = torch
     return _TORCH
 
@@ -25,7 +25,7 @@ def torch_():
 def code(t, what):
     """The HYENA_DTYPE_* of a tensor."""
     torch_()
-    c = _CODES.get(t.dtype)
+    c = CODES.get(t.dtype)
     if c is None:
         raise TypeError("%s must be bfloat16 or float32, got %s" % (what, t.dtype))
     return c
@@ -51,6 +51,12 @@ def need(name, t, shape, dtype, device):
     if t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     raise ValueError("%s must be contiguous" % name)
+
+
+def like(t, shape, dtype, device):
+    """Whether ``t`` is what need() asks for."""
+    return (t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous())
 
 
 def ptr(t):

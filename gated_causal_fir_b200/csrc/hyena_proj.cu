@@ -17,6 +17,7 @@ using hyena::host::overlap;
 using hyena::host::round_up;
 
 constexpr int64_t kMaxDim = int64_t{1} << 30;
+constexpr int64_t kMaxReduced = int64_t{1} << 24;  // a tile's sum ends well inside a wait's 2 s
 constexpr int kSms = 148;
 constexpr int kMaxSplits = 16;
 
@@ -292,7 +293,7 @@ int operands(Operand *a, const void *pa, int64_t ra, Operand *b, const void *pb,
 
 int check_shape(int64_t M, int64_t N, int64_t K, int dtype) {
   if (dtype != HYENA_DTYPE_BF16 && dtype != HYENA_DTYPE_F32) return HYENA_ERR_INVALID_ARG;
-  if (M < 0 || N < 1 || K < 1 || M > kMaxDim || N > kMaxDim || K > kMaxDim)
+  if (M < 0 || N < 1 || K < 1 || M > kMaxDim || N > kMaxDim || K > kMaxReduced)
     return HYENA_ERR_INVALID_ARG;
   return HYENA_OK;
 }
@@ -485,7 +486,7 @@ int hyena_proj_bwd(const void *x, const void *w, const void *z, const void *dy,
     return HYENA_OK;
   }
   if (!dy || (dx && !w) || (dw && !x) || (act != HYENA_ACT_NONE && !z)) return HYENA_ERR_INVALID_ARG;
-  if (db_blocks(M) > 65535) return HYENA_ERR_UNSUPPORTED;
+  if (db_blocks(M) > 65535 || N > kMaxReduced) return HYENA_ERR_UNSUPPORTED;
   const int64_t need = hyena_proj_bwd_workspace_bytes(M, N, K, act, dtype);
   if (!workspace || static_cast<int64_t>(workspace_bytes) < need) return HYENA_ERR_INVALID_ARG;
   if (clash({{dx, nx}, {dw, nw}, {db, N * 4}, {workspace, need}},

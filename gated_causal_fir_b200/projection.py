@@ -6,8 +6,8 @@ x: CUDA [..., K], w: [N, K], all bf16 or all fp32; bias fp32 [N].  The functions
 CUDA tensors into pointers, sizes and a stream; outputs and workspaces that are not given come
 from torch.
 """
-from ._args import (code as code_of, cuda_tensor, keep, nbytes, need, ptr, run, stream_handle,
-                    torch_, workspace as workspace_of)
+from ._args import (CODES, code as code_of, cuda_tensor, keep, nbytes, need, ptr, run,
+                    stream_handle, torch_, workspace as workspace_of)
 from ._native import ACT_CODES, HYENA_DTYPE_BF16
 
 
@@ -20,6 +20,15 @@ def _act(act):
 
 def _rows(x, w):
     """(type code, M, N, K) of x [..., K] and w [N, K]."""
+    try:  # the calls that are right, quickly
+        shape, dtype, device = x.shape, x.dtype, x.device
+        code, (N, K) = CODES.get(dtype), w.shape
+        if (code is not None and x.is_cuda and len(shape) > 1 and shape[-1] == K and N > 0 and K > 0
+                and w.dtype is dtype and w.device == device and x.is_contiguous()
+                and w.is_contiguous()):
+            return code, x.numel() // K, N, K
+    except (AttributeError, TypeError, ValueError):
+        pass
     cuda_tensor("x", x, "[..., K] tensor")
     shape = x.shape
     if len(shape) < 2:
@@ -53,18 +62,17 @@ def hyena_proj_fwd(x, w, bias=None, act="none", residual=None, y=None, z=None, w
     hyena_proj_bwd.  y may be ``residual`` itself.  Runs asynchronously on ``stream`` (default:
     the current stream of x's device).
     """
-    torch = torch_()
     act = _act(act)
     code, M, N, K = _rows(x, w)
     shape = x.shape[:-1] + (N,)
     if bias is not None:
-        need("bias", bias, (N,), torch.float32, x.device)
+        need("bias", bias, (N,), torch_().float32, x.device)
     if residual is not None:
         need("residual", residual, shape, x.dtype, x.device)
     if z is not None:
         need("z", z, shape, x.dtype, x.device)
     if y is None:
-        y = x.new_empty(shape)
+        y = x.new_empty(shape) if residual is None else torch_().empty_like(residual)
         keep(stream, y)
     else:
         need("y", y, shape, x.dtype, x.device)

@@ -7,13 +7,24 @@ gates of the FIR operator around a state that the data lets decay.  The function
 CUDA tensors into pointers, sizes and a stream; outputs and workspaces that are not given come
 from torch.
 """
-from ._args import (code as code_of, cuda_tensor, keep, nbytes, need, ptr, run, stream_handle,
-                    torch_, workspace as workspace_of)
+from ._args import (CODES, code as code_of, cuda_tensor, keep, like, nbytes, need, ptr, run,
+                    stream_handle, torch_, workspace as workspace_of)
 from ._native import HYENA_DTYPE_BF16
 
 
 def _shapes(q, k, v, g, d_g, dims):
     """The type code of q [*dims, D], k, v like it and g [*dims, D // d_g]."""
+    try:  # the calls that are right, quickly
+        shape, dtype, device = q.shape, q.dtype, q.device
+        code = CODES.get(dtype)
+        if (code is not None and q.is_cuda and len(shape) == len(dims) // 3 + 1
+                and shape[-1] % d_g == 0 and q.is_contiguous()
+                and like(k, shape, dtype, device) and like(v, shape, dtype, device)
+                and like(g, shape if d_g == 1 else shape[:-1] + (shape[-1] // d_g,), dtype,
+                         device) and type(d_g) is int and d_g > 0 and shape[-1] > 0):
+            return code
+    except (AttributeError, TypeError, ZeroDivisionError):
+        pass
     cuda_tensor("q", q, "[%s] tensor" % dims)
     shape, dtype, device = q.shape, q.dtype, q.device
     if len(shape) != len(dims) // 3 + 1:
@@ -79,7 +90,8 @@ def hyena_scan_fwd(q, k, v, g, d_g, s0=None, y=None, s_out=None, ckpt=None, work
     else:
         need("y", y, q.shape, q.dtype, device)
     if s_out is None:
-        s_out = torch_().empty((B, D), dtype=torch_().float32, device=device)
+        s_out = (torch_().empty_like(s0) if s0 is not None else
+                 torch_().empty((B, D), dtype=torch_().float32, device=device))
         keep(stream, s_out)
     else:
         _state("s_out", s_out, q)

@@ -6,7 +6,8 @@
  * hyena_conv.h: DEVICE pointers, row-major contiguous tensors, buffers owned by the caller, no
  * device allocation, asynchronous on `stream`, argument errors found on the host before anything
  * is queued.  Outputs must not overlap inputs or each other unless an entry point says so.
- * A timeout inside a kernel raises HYENA_DEVICE_TIMEOUT in the status word of hyena_conv.h.
+ * Make the first call of each kind on a device before any stream capture (kernel attributes are
+ * set then).  A timeout inside a kernel raises HYENA_DEVICE_TIMEOUT in the status word of hyena_conv.h.
  */
 #ifndef HYENA_MIXER_H
 #define HYENA_MIXER_H
@@ -99,7 +100,7 @@ enum hyena_act {
  * x: [M, K], w: [N, K], residual, y, z: [M, N], all of `dtype`, 16-byte aligned.  bias: fp32 [N].
  * bias, residual and z may be NULL; z, where given, receives the value before the activation,
  * which hyena_proj_bwd wants (rounded to `dtype`).  y may be residual itself.
- * Any M >= 0, N, K >= 1.  The products run on tensor cores with fp32 accumulation: bf16 operands
+ * Any M >= 0, N, K >= 1 (M, N <= 2^30, K <= 2^24).  The products run on tensor cores with fp32 accumulation: bf16 operands
  * as they are (rows that are no multiple of 8 elements are copied into the workspace first); fp32
  * operands as three bf16 planes each and six products, which keeps fp32's precision (relative to
  * sum |x| |w|) for finite values; a product with an infinite operand may give NaN in its place.
@@ -124,7 +125,7 @@ int64_t hyena_proj_workspace_bytes(int64_t M, int64_t N, int64_t K, int dtype);
  * dx [M, K], dw [N, K] of `dtype` and db fp32 [N] are overwritten; each may be NULL (x is not
  * read without dw, nor w without dx, and may then be NULL).  dz is rounded to `dtype` as an
  * operand of the products (db is not).  All tensors 16-byte aligned (db 4).  M == 0 zeroes dw and
- * db.  Deterministic.
+ * db.  M up to 8388480 and N up to 2^24, else HYENA_ERR_UNSUPPORTED.  Deterministic.
  * workspace: at least hyena_proj_bwd_workspace_bytes(M, N, K, act, dtype) bytes, 256-byte aligned.
  */
 int hyena_proj_bwd(const void *x, const void *w, const void *z, const void *dy,
