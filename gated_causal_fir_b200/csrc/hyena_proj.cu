@@ -39,7 +39,13 @@ constexpr TileShape kShapes[] = {  // times measured on products of 16..8192 row
 struct Plan {
   int shape, splits, kb, pairs, per;  // per: blocks per cut
   int64_t tiles_m, tiles_n, whole;
+  bool join;  // the cuts of a tile are a cluster
 };
+
+// Clusters of so many CTAs, one per SM, that run at once (GPCs of 16 to 18 SMs; 16 clusters of 8
+// took two waves).
+constexpr int kMaxJoin = 8;
+constexpr int kClusters[kMaxJoin + 1] = {0, 148, 66, 40, 32, 20, 16, 8, 8};
 
 // The tile shape and the cuts along k with the least estimated time.  Persistent workers take the
 // tiles in waves; those of an unfinished last wave (or, in a small problem, all) are cut so that
@@ -61,11 +67,15 @@ Plan find_plan(int64_t M, int64_t N, int64_t K, int dtype) {
       // a tile's k-blocks run beside the epilogue of the one before it
       double ns = static_cast<double>(whole / t.workers) * std::max(static_cast<double>(total) * t.block, t.epi) +
                   (rest ? std::max(static_cast<double>(per) * t.block, whole ? t.epi : 0.0) : 0) + t.tail;
-      if (splits > 1)  // the second kernel, and the partial sums' way to it and back
+      const bool join = splits > 1 && whole == 0 && s != kPair256 && splits <= kMaxJoin &&
+                        rest <= kClusters[splits];
+      if (join)
+        ns += 1500;
+      else if (splits > 1)  // the second kernel, and the partial sums' way to it and back
         ns += 3000 + static_cast<double>(rest * splits) * std::min<int64_t>(M, t.m) * t.n * 4 / 4500;
       if (best_ns == 0 || ns < best_ns) {
         best_ns = ns;
-        best = Plan{s, splits, kb, pairs, static_cast<int>(per), tm, tn, splits > 1 ? whole : tm * tn};
+        best = Plan{s, splits, kb, pairs, static_cast<int>(per), tm, tn, splits > 1 ? whole : tm * tn, join};
       }
     }
   }
@@ -90,7 +100,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int dtype) {
 
 int64_t partial_bytes(int64_t M, int64_t N, int64_t K, int dtype) {
   const Plan p = plan_of(M, N, K, dtype);
-  const int64_t cut = (p.tiles_m * p.tiles_n - p.whole) * p.splits;
+  const int64_t cut = p.join ? 0 : (p.tiles_m * p.tiles_n - p.whole) * p.splits;
   return cut * kShapes[p.shape].m * kShapes[p.shape].n * 4;  // a multiple of 256
 }
 
@@ -141,10 +151,10 @@ struct Device {
   int pairs;  // resident pairs of CTAs
 };
 
-template <typename T, int kCG, int kBN, bool kAMn, bool kBMn>
+template <typename T, int kCG, int kBN, bool kAMn, bool kBMn, bool kJoin>
 cudaError_t allow(int *resident) {
   using L = pj::Tile<kCG, kBN>;
-  auto *fn = pj::proj_kernel<T, kCG, kBN, kAMn, kBMn>;
+  auto *fn = pj::proj_kernel<T, kCG, kBN, kAMn, kBMn, kJoin>;
   cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(fn),
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   if (e == cudaSuccess && kCG == 2 && resident) {
@@ -164,9 +174,11 @@ cudaError_t allow(int *resident) {
 template <typename T, bool kAMn, bool kBMn>
 cudaError_t allow_all(int *resident) {
   cudaError_t e = cudaSuccess;
-  if constexpr (sizeof(T) == 2) e = allow<T, 2, 256, kAMn, kBMn>(resident);
-  if (e == cudaSuccess) e = allow<T, 1, 128, kAMn, kBMn>(nullptr);
-  if (e == cudaSuccess) e = allow<T, 1, 64, kAMn, kBMn>(nullptr);
+  if constexpr (sizeof(T) == 2) e = allow<T, 2, 256, kAMn, kBMn, false>(resident);
+  if (e == cudaSuccess) e = allow<T, 1, 128, kAMn, kBMn, false>(nullptr);
+  if (e == cudaSuccess) e = allow<T, 1, 64, kAMn, kBMn, false>(nullptr);
+  if (e == cudaSuccess) e = allow<T, 1, 128, kAMn, kBMn, true>(nullptr);
+  if (e == cudaSuccess) e = allow<T, 1, 64, kAMn, kBMn, true>(nullptr);
   return e;
 }
 
@@ -193,26 +205,27 @@ int prepare_device(Device *d) {
   return err[dev] == cudaSuccess ? HYENA_OK : HYENA_ERR_CUDA;
 }
 
-template <typename T, int kCG, int kBN, bool kAMn, bool kBMn>
+template <typename T, int kCG, int kBN, bool kAMn, bool kBMn, bool kJoin = false>
 cudaError_t launch_shape(const CUtensorMap (&m)[5], const pj::Params &p, const Device &d,
                          cudaStream_t stream) {
   using L = pj::Tile<kCG, kBN>;
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
   const int64_t works = p.whole + (tiles - p.whole) * p.splits;
-  const int64_t workers = std::min<int64_t>(works, kCG == 2 ? d.pairs : d.info.sm_count);
+  const int64_t workers =
+      kJoin ? works : std::min<int64_t>(works, kCG == 2 ? d.pairs : d.info.sm_count);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim = {2, 1, 1};
+  attr[1].val.clusterDim = {static_cast<unsigned>(kJoin ? p.splits : 2), 1, 1};
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(workers * kCG));
   cfg.blockDim = dim3(pj::kThreads);
   cfg.dynamicSmemBytes = L::kSmem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = kCG == 2 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, pj::proj_kernel<T, kCG, kBN, kAMn, kBMn>, m[0], m[1], m[2], m[3],
+  cfg.numAttrs = kCG == 2 || kJoin ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, pj::proj_kernel<T, kCG, kBN, kAMn, kBMn, kJoin>, m[0], m[1], m[2], m[3],
                             m[4], p);
 }
 
@@ -254,11 +267,16 @@ int product(const Operand &a, const Operand &b, int64_t K, pj::Params p, int dty
       } else {
         return HYENA_ERR_UNSUPPORTED;  // not planned for fp32
       }
-    case kOne128: e = launch_shape<T, 1, 128, kAMn, kBMn>(m, p, d, stream); break;
-    default: e = launch_shape<T, 1, 64, kAMn, kBMn>(m, p, d, stream);
+    case kOne128:
+      e = pl.join ? launch_shape<T, 1, 128, kAMn, kBMn, true>(m, p, d, stream)
+                  : launch_shape<T, 1, 128, kAMn, kBMn>(m, p, d, stream);
+      break;
+    default:
+      e = pl.join ? launch_shape<T, 1, 64, kAMn, kBMn, true>(m, p, d, stream)
+                  : launch_shape<T, 1, 64, kAMn, kBMn>(m, p, d, stream);
   }
   if (e != cudaSuccess) return HYENA_ERR_CUDA;
-  if (p.splits == 1) return HYENA_OK;
+  if (p.splits == 1 || pl.join) return HYENA_OK;
   const TileShape &t = kShapes[pl.shape];
   const int64_t n = (pl.tiles_m * pl.tiles_n - pl.whole) * std::min<int64_t>(t.m, p.M) * (t.n / 4);
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>((n + 255) / 256, 8 * d.info.sm_count));

@@ -50,7 +50,8 @@ def test_workspace_sizes(lib):
     assert g.hyena_proj_workspace_bytes(8192, 4096, 4096) == 0          # operands as they are
     assert g.hyena_proj_workspace_bytes(8192, 4096, 4095) > 0           # rows to be padded
     assert g.hyena_proj_workspace_bytes(100, 64, 64, g.HYENA_DTYPE_F32) >= 3 * 2 * 164 * 64
-    assert g.hyena_proj_workspace_bytes(8, 256, 4096) > 0               # cut along k
+    assert g.hyena_proj_workspace_bytes(8, 256, 4096) == 0              # cut in a cluster
+    assert g.hyena_proj_workspace_bytes(4096, 4096, 8192) > 0           # the last wave is cut
     assert g.hyena_proj_workspace_bytes(0, 8, 8) == 0
     assert g.hyena_proj_bwd_workspace_bytes(8192, 4096, 4096, "silu") >= 8192 * 4096 * 2
     with pytest.raises(g.HyenaError):
