@@ -815,20 +815,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           });
         } else {
+          // rows that are no multiple of 16 bytes, and partial products: lane -> column, row by row,
+          // eight rows' residuals at a time
+          const int at = k.n * L::kN + col0 + c0 + lane;
+          const bool inside = at < p.N;
+          const float b = p.bias && k.part < 0 && inside ? p.bias[at] : 0.0f;
+          const T *res = static_cast<const T *>(p.residual);
 #pragma unroll 1
-          for (int i = 0; i < 4; ++i) {
-            float c[8];
-            staged(i, c);
-            const int64_t row = row0 + 8 * i + sub;
-            if (row >= p.M || col >= p.N) continue;
-            if (k.part < 0) {
-              finish<T, 8>(p, c, row, col);
-            } else {  // whole tiles of fp32: no care at the ragged edge
-              const int in_row = static_cast<int>(rank) * kRows + quad * 32 + 8 * i + sub;
-              float4 *to = reinterpret_cast<float4 *>(
-                  p.partial + (static_cast<int64_t>(k.part) * L::kM + in_row) * kBN + in_tile);
-              to[0] = make_float4(c[0], c[1], c[2], c[3]);
-              to[1] = make_float4(c[4], c[5], c[6], c[7]);
+          for (int r0 = 0; r0 < 32; r0 += 8) {
+            float add[8], v[8];
+            const int64_t first_at = static_cast<int64_t>(row0 + r0) * p.N + at;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              add[i] = k.part < 0 && res && inside && row0 + r0 + i < p.M
+                           ? to_f(res[first_at + static_cast<int64_t>(i) * p.N])
+                           : 0.0f;
+              v[i] = b + out[(r0 + i) * kChunk + (((lane >> 2) ^ i) * 4) + (lane & 3)];
+            }
+            if (k.part >= 0) {  // whole tiles of fp32: no care at the ragged edge
+              float *to = p.partial +
+                          (static_cast<int64_t>(k.part) * L::kM + static_cast<int>(rank) * kRows +
+                           quad * 32 + r0) * kBN + col0 + c0 + lane;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) to[i * kBN] = v[i];
+              continue;
+            }
+            float y[8];
+            with_act(p.act, [&](auto act) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) y[i] = act_of<T, decltype(act)::value>(v[i]) + add[i];
+            });
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (!inside || row0 + r0 + i >= p.M) continue;
+              const int64_t to = first_at + static_cast<int64_t>(i) * p.N;
+              if (p.z) from_f(v[i], static_cast<T *>(p.z) + to);
+              from_f(y[i], static_cast<T *>(p.y) + to);
             }
           }
         }
@@ -859,24 +881,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r0 = rows * cut / p.splits, r1 = rows * (cut + 1) / p.splits;
       constexpr int kQuads = kBN / 4;
       const uint32_t base = smem_u32(stages);
-      for (int i = threadIdx.x - 64; i < (r1 - r0) * kQuads; i += 32 * kEpiWarps) {
-        const int r = r0 + i / kQuads, q = i % kQuads, col = k.n * kBN + q * 4;
-        if (col >= p.N) continue;
-        // pieces are swizzled within groups of 8
-        const uint32_t at = base + (r * kBN + ((q & ~7) | ((q ^ r) & 7)) * 4) * 4;
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
+      constexpr int kBatch = 4;  // pieces in flight per thread
+      const int n = (r1 - r0) * kQuads, step_i = 32 * kEpiWarps;
+      for (int i0 = threadIdx.x - 64; i0 < n; i0 += kBatch * step_i) {
+        float c[kBatch][4] = {};
         for (int s = 0; s < p.splits; ++s) {
-          float4 v;
-          asm volatile("{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %4, %5;\n\t"
-                       "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
-                       : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                       : "r"(at), "r"(s)
-                       : "memory");
-          c[0] += v.x, c[1] += v.y, c[2] += v.z, c[3] += v.w;
+          uint32_t peer;
+          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(peer) : "r"(base), "r"(s));
+          float4 v[kBatch];
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            const int i = min(i0 + b * step_i, n - 1), r = r0 + i / kQuads, q = i % kQuads;
+            // pieces are swizzled within groups of 8
+            const uint32_t at = peer + (r * kBN + ((q & ~7) | ((q ^ r) & 7)) * 4) * 4;
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(v[b].x), "=f"(v[b].y), "=f"(v[b].z), "=f"(v[b].w)
+                         : "r"(at));
+          }
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b)
+            c[b][0] += v[b].x, c[b][1] += v[b].y, c[b][2] += v[b].z, c[b][3] += v[b].w;
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) c[e] += p.bias && col + e < p.N ? p.bias[col + e] : 0.0f;
-        finish<T, 4>(p, c, m0 + r, col);
+        for (int b = 0; b < kBatch; ++b) {
+          const int i = i0 + b * step_i, r = r0 + i / kQuads, col = k.n * kBN + i % kQuads * 4;
+          if (i >= n || col >= p.N) continue;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) c[b][e] += p.bias && col + e < p.N ? p.bias[col + e] : 0.0f;
+          finish<T, 4>(p, c[b], m0 + r, col);
+        }
       }
     }
     cluster_sync();  // no CTA leaves while others read its product
