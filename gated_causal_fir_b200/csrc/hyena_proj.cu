@@ -29,15 +29,16 @@ enum Shape { kPair256 = 0, kOne128 = 1, kOne64 = 2 };
 
 struct TileShape {
   int m, n, workers;
-  double block, tail, epi;  // ns per k-block of 64; outside the k-blocks; per tile's epilogue
+  double block, block_f32, tail, epi;  // ns per k-block of 64 (of bf16, fp32 operands), outside the
+                                       // k-blocks, and of a tile's epilogue
 };
 constexpr TileShape kShapes[] = {  // times measured on products of 16..8192 rows and columns
-    {256, 256, kSms / 2, 340, 5000, 3000},
-    {128, 128, kSms, 230, 3200, 1500},
-    {128, 64, kSms, 185, 2600, 900}};
+    {256, 256, kSms / 2, 340, 0, 5000, 3000},
+    {128, 128, kSms, 230, 1150, 3200, 1500},
+    {128, 64, kSms, 185, 950, 2600, 900}};
 
 struct Plan {
-  int shape, splits, kb, pairs, per;  // per: blocks per cut
+  int shape, splits, kb, per;  // per: blocks per cut
   int64_t tiles_m, tiles_n, whole;
   bool join;  // the cuts of a tile are a cluster
 };
@@ -54,19 +55,21 @@ constexpr int kClusters[kMaxJoin + 1] = {0, 148, 66, 40, 32, 20, 16, 8, 8};
 Plan find_plan(int64_t M, int64_t N, int64_t K, int dtype) {
   Plan best{};
   double best_ns = 0;
-  const int kb = static_cast<int>((K + pj::kBK - 1) / pj::kBK), pairs = dtype == HYENA_DTYPE_F32 ? 6 : 1;
-  const int64_t total = static_cast<int64_t>(kb) * pairs;
-  for (int s = dtype == HYENA_DTYPE_F32 ? kOne128 : kPair256; s <= kOne64; ++s) {
+  const bool f32 = dtype == HYENA_DTYPE_F32;
+  const int64_t total = (K + pj::kBK - 1) / pj::kBK;
+  const int least = f32 ? 2 : 4;  // k-blocks worth a cut
+  for (int s = f32 ? kOne128 : kPair256; s <= kOne64; ++s) {
     const TileShape &t = kShapes[s];
+    const double block = f32 ? t.block_f32 : t.block;
     const int64_t tm = (M + t.m - 1) / t.m, tn = (N + t.n - 1) / t.n;
     const int64_t whole = tm * tn / t.workers * t.workers, rest = tm * tn - whole;
     for (int want = 1; want <= (rest ? kMaxSplits : 1); ++want) {
       const int64_t per = (total + want - 1) / want;
       const int splits = static_cast<int>((total + per - 1) / per);
-      if (splits != want || (want > 1 && (per < 4 || rest * want > t.workers))) continue;
+      if (splits != want || (want > 1 && (per < least || rest * want > t.workers))) continue;
       // a tile's k-blocks run beside the epilogue of the one before it
-      double ns = static_cast<double>(whole / t.workers) * std::max(static_cast<double>(total) * t.block, t.epi) +
-                  (rest ? std::max(static_cast<double>(per) * t.block, whole ? t.epi : 0.0) : 0) + t.tail;
+      double ns = static_cast<double>(whole / t.workers) * std::max(static_cast<double>(total) * block, t.epi) +
+                  (rest ? std::max(static_cast<double>(per) * block, whole ? t.epi : 0.0) : 0) + t.tail;
       const bool join = splits > 1 && whole == 0 && s != kPair256 && splits <= kMaxJoin &&
                         rest <= kClusters[splits];
       if (join)
@@ -75,7 +78,7 @@ Plan find_plan(int64_t M, int64_t N, int64_t K, int dtype) {
         ns += 3000 + static_cast<double>(rest * splits) * std::min<int64_t>(M, t.m) * t.n * 4 / 4500;
       if (best_ns == 0 || ns < best_ns) {
         best_ns = ns;
-        best = Plan{s, splits, kb, pairs, static_cast<int>(per), tm, tn, splits > 1 ? whole : tm * tn, join};
+        best = Plan{s, splits, static_cast<int>(total), static_cast<int>(per), tm, tn, splits > 1 ? whole : tm * tn, join};
       }
     }
   }
@@ -238,7 +241,6 @@ int product(const Operand &a, const Operand &b, int64_t K, pj::Params p, int dty
   if (pl.tiles_m * pl.tiles_n * pl.splits > std::numeric_limits<int32_t>::max())
     return HYENA_ERR_UNSUPPORTED;
   p.kb = pl.kb;
-  p.pairs = pl.pairs;
   p.tiles_m = static_cast<int>(pl.tiles_m);
   p.tiles_n = static_cast<int>(pl.tiles_n);
   p.whole = static_cast<int>(pl.whole);

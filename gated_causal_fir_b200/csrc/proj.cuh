@@ -8,10 +8,12 @@
 //
 // fp32 operands are split into three bf16 planes a = a0 + a1 + a2 (8 bits of the mantissa each),
 // and C is the sum of the six products of planes i + j <= 2, smallest first; the three left out
-// are below 2^-26 of a b.  The tensor cores' accumulator truncates at every addition, which over
-// thousands of k is a bias above fp32's own rounding: every 256 k the epilogue warps take the
-// accumulator into registers, where the sum goes on with rounding to nearest (error of a
-// 4096-term product against 64 bits: ...).
+// are below 2^-26 of a b.  The planes of a k-block are three stages of the ring, from which the six
+// products take theirs.  The tensor cores' accumulator truncates at every addition, which over
+// thousands of k is a bias above fp32's own rounding: after each k-block the epilogue warps take
+// the accumulator into registers, where the sum goes on with rounding to nearest (normwise error
+// of a product over 4096 k: 1.2e-7, over 16384 k: 1.7e-7; fp32 FMAs: 1.1e-6 and 2.3e-6).  2048^3:
+// 97 us (fp32 FMA units: 306).
 //
 // Tiles.  kCG = 2: a pair of CTAs works on 256 x 256 outputs with tcgen05.mma.cta_group::2, each
 // holding 128 rows of A, 128 rows of B and 128 rows of the accumulator.  Each byte staged then
@@ -52,8 +54,9 @@ constexpr unsigned int kTimeout = 1u;          // HYENA_DEVICE_TIMEOUT
 enum Act { kNone = 0, kGelu = 1, kSilu = 2, kSigmoid = 3, kLogSigmoid = 4 };
 
 // The six products of bf16 planes, smallest first, as (plane of A, plane of B).
-__device__ constexpr uint8_t kPlaneA[6] = {0, 2, 1, 0, 1, 0};
-__device__ constexpr uint8_t kPlaneB[6] = {2, 0, 1, 1, 0, 0};
+constexpr int kProducts = 6;
+__host__ __device__ constexpr int plane_a(int i) { return i == 1 ? 2 : i == 2 || i == 4 ? 1 : 0; }
+__host__ __device__ constexpr int plane_b(int i) { return i == 0 ? 2 : i == 2 || i == 3 ? 1 : 0; }
 
 template <int kCG, int kBN>
 struct Tile {
@@ -69,15 +72,11 @@ struct Tile {
   static constexpr int kTmemCols = 2 * kBN < 32 ? 32 : 2 * kBN;  // two accumulators
 };
 
-// k-blocks per accumulator when sums go on in registers (fp32 operands).
-constexpr int kFlush = 4;
-
 struct Params {
-  int M, N, kb;                 // outputs; k-blocks of one product
-  int pairs;                    // 1 (bf16) or 6 (planes of fp32)
+  int M, N, kb;                 // outputs; k-blocks
   int tiles_m, tiles_n;
   int whole;                    // the first tiles, each one work
-  int splits, kb_per_split;     // cuts of the pairs * kb blocks of the other tiles
+  int splits, kb_per_split;     // cuts of the other tiles' k-blocks
   int group_m;                  // tiles of m that run together (their w tiles stay in L2)
   const float *bias;            // [N] or null
   const void *residual;         // [M, N] or null
@@ -337,7 +336,7 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_
 
 // ------------------------------------------------------------------------------- work
 struct Work {
-  int m, n, kb0, kb1;  // tile coordinates; blocks [kb0, kb1) of the pairs * kb
+  int m, n, kb0, kb1;  // tile coordinates; k-blocks [kb0, kb1)
   int part;            // index of its partial product, or -1
 };
 __device__ __forceinline__ void tile_at(const Params &p, int t, int *m, int *n) {
@@ -351,16 +350,16 @@ __device__ __forceinline__ int work_count(const Params &p) {
 }
 __device__ __forceinline__ Work work_at(const Params &p, int w) {
   Work k;
-  const int total = p.pairs * p.kb, rest = p.tiles_m * p.tiles_n - p.whole;
+  const int rest = p.tiles_m * p.tiles_n - p.whole;
   int tile = w;
   k.kb0 = 0;
-  k.kb1 = total;
+  k.kb1 = p.kb;
   k.part = -1;
   if (w >= p.whole && p.splits > 1) {  // a cut of all the other tiles, then the next cut
     const int r = w - p.whole, split = r / rest;
     tile = p.whole + r % rest;
     k.kb0 = split * p.kb_per_split;
-    k.kb1 = min(k.kb0 + p.kb_per_split, total);
+    k.kb1 = min(k.kb0 + p.kb_per_split, p.kb);
     k.part = (r % rest) * p.splits + split;
   }
   tile_at(p, tile, &k.m, &k.n);
@@ -376,6 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const __grid_constant__ CUtensorMap mr, const Params p) {
   using L = Tile<kCG, kBN>;
   constexpr bool kPromote = sizeof(T) == 4;
+  constexpr int kPlanes = kPromote ? 3 : 1;                // stages of a k-block
+  constexpr int kRing = L::kStages / kPlanes * kPlanes;  // stages in use
   static_assert(!kPromote || kCG == 1, "the sums of a pair's tile do not fit the registers");
   static_assert(!kJoin || kCG == 1, "a cluster is a pair or a tile's cuts");
   extern __shared__ uint8_t dynamic[];
@@ -432,13 +433,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Work k = work_at(p, w);
       const int m0 = k.m * L::kM + static_cast<int>(rank) * kRows;
       const int n0 = k.n * L::kN + static_cast<int>(rank) * L::kBRows;
-      int pair = k.kb0 / p.kb, k0 = (k.kb0 - pair * p.kb) * kBK;
-      int pa = p.pairs > 1 ? kPlaneA[pair] : 0, pb = p.pairs > 1 ? kPlaneB[pair] : 0;
-      for (int kb = k.kb0; kb < k.kb1; ++kb, ++it) {
-        if (it >= L::kStages && !wait(&empty[st], freed)) {
+      for (int i = k.kb0 * kPlanes; i < k.kb1 * kPlanes; ++i, ++it) {
+        if (it >= kRing && !wait(&empty[st], freed)) {
           ok = false;
           break;
         }
+        const int plane = i % kPlanes, k0 = i / kPlanes * kBK;
         uint8_t *a = stages + st * L::kStage, *b = a + L::kABytes;
         const uint32_t bar = full0 + 8 * st;
         if (lead) {
@@ -446,35 +446,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (kAMn) {
 #pragma unroll
             for (int h = 0; h < kRows / 64; ++h)
-              load_tile<kCG>(a + h * 8192, &ma, bar, m0 + h * 64, k0, pa);
+              load_tile<kCG>(a + h * 8192, &ma, bar, m0 + h * 64, k0, plane);
           } else {
-            load_tile<kCG>(a, &ma, bar, k0, m0, pa);
+            load_tile<kCG>(a, &ma, bar, k0, m0, plane);
           }
           if (kBMn) {
 #pragma unroll
             for (int h = 0; h < L::kBRows / 64; ++h)
-              load_tile<kCG>(b + h * 8192, &mb, bar, n0 + h * 64, k0, pb);
+              load_tile<kCG>(b + h * 8192, &mb, bar, n0 + h * 64, k0, plane);
           } else {
-            load_tile<kCG>(b, &mb, bar, k0, n0, pb);
+            load_tile<kCG>(b, &mb, bar, k0, n0, plane);
           }
         }
-        if (++st == L::kStages) {
+        if (++st == kRing) {
           st = 0;
           freed ^= 1;
-        }
-        k0 += kBK;
-        if (k0 >= p.kb * kBK && kb + 1 < k.kb1) {  // the next pair of planes
-          k0 = 0;
-          ++pair;
-          pa = kPlaneA[pair];
-          pb = kPlaneB[pair];
         }
       }
     }
     // Before the CTA ends every copy has landed and every release of a stage has arrived.  In
     // the leader `full` covers both CTAs' copies.
-    for (int j = it > L::kStages ? it - L::kStages : 0; j < it; ++j) {
-      const int s = j % L::kStages, parity = (j / L::kStages) & 1;
+    for (int j = it > kRing ? it - kRing : 0; j < it; ++j) {
+      const int s = j % kRing, parity = (j / kRing) & 1;
       int no_abort = 0;
       if (!wait(&empty[s], parity) && rank == 0)
         mbar_wait(&full[s], parity, &no_abort, p.status, kTimeout);
@@ -490,35 +483,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t db0 = umma_smem_desc(s0 + L::kABytes, kBMn ? 8192 : 16, 1024, 2);
       const uint32_t a_hi = static_cast<uint32_t>(da0 >> 32), b_hi = static_cast<uint32_t>(db0 >> 32);
       uint32_t a_lo = static_cast<uint32_t>(da0), b_lo = static_cast<uint32_t>(db0);
-      int it = 0, n = 0, st = 0;  // k-blocks; accumulators filled; stage
+      int it = 0, n = 0, st = 0;  // stages taken; accumulators filled; stage
       uint32_t filled = 0;        // parity of the stage's next fill
       bool ok = true;
       for (int w = first; w < works && ok; w += step) {
         const Work k = work_at(p, w);
         for (int kb = k.kb0; kb < k.kb1 && ok; ++n) {
-          const int acc = n & 1, end = kPromote ? min(kb + kFlush, k.kb1) : k.kb1;
+          const int acc = n & 1, end = kPromote ? kb + 1 : k.kb1;
           if (n >= 2 && !wait(&acc_empty[acc], (n / 2 - 1) & 1)) {
             ok = false;
             break;
           }
           tc_fence_after_sync();
           const uint32_t d = tmem + acc * kBN;
-          for (uint32_t more = 0; kb < end; ++kb, ++it) {
-            if (!wait(&full[st], filled)) {
-              ok = false;
-              break;
-            }
+          for (uint32_t more = 0; kb < end; ++kb, it += kPlanes) {
+#pragma unroll
+            for (int q = 0; q < kPlanes; ++q) ok = ok && wait(&full[st + q], filled);
+            if (!ok) break;
             tc_fence_after_sync();
             if (lead) {
 #pragma unroll
-              for (int s = 0; s < kBK / 16; ++s)
-                mma<kCG>(d, a_lo + s * kStepA, a_hi, b_lo + s * kStepB, b_hi, id, s > 0 ? 1u : more);
-              commit<kCG>(&empty[st]);
+              for (int q = 0; q < (kPromote ? kProducts : 1); ++q) {
+                constexpr uint32_t kUnits = L::kStage >> 4;
+                const uint32_t a = a_lo + (kPromote ? plane_a(q) * kUnits : 0);
+                const uint32_t b = b_lo + (kPromote ? plane_b(q) * kUnits : 0);
+#pragma unroll
+                for (int s = 0; s < kBK / 16; ++s)
+                  mma<kCG>(d, a + s * kStepA, a_hi, b + s * kStepB, b_hi, id,
+                           q > 0 || s > 0 ? 1u : more);
+              }
+#pragma unroll
+              for (int q = 0; q < kPlanes; ++q) commit<kCG>(&empty[st + q]);
             }
             more = 1;
-            a_lo += L::kStage >> 4;
-            b_lo += L::kStage >> 4;
-            if (++st == L::kStages) {
+            a_lo += kPlanes * (L::kStage >> 4);
+            b_lo += kPlanes * (L::kStage >> 4);
+            st += kPlanes;
+            if (st == kRing) {
               st = 0;
               filled ^= 1;
               a_lo = static_cast<uint32_t>(da0);
@@ -532,8 +533,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // MMAs still reading shared memory when a wait gave up: let them finish
       if (!ok || abort) {
         int no_abort = 0;
-        for (int j = it > L::kStages ? it - L::kStages : 0; j < it; ++j)
-          mbar_wait(&empty[j % L::kStages], (j / L::kStages) & 1, &no_abort, p.status, kTimeout);
+        for (int j = it > kRing ? it - kRing : 0; j < it; ++j)
+          mbar_wait(&empty[j % kRing], (j / kRing) & 1, &no_abort, p.status, kTimeout);
       }
     }
   } else {
@@ -619,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (kPromote) {
 #pragma unroll
         for (int c = 0; c < kBN / 2; ++c) sum[c] = 0.0f;
-        for (int kb = k.kb0; kb < k.kb1 && ok; kb += kFlush, ++n) {
+        for (int kb = k.kb0; kb < k.kb1 && ok; ++kb, ++n) {
           const int acc = n & 1;
           ok = wait(&acc_full[acc], (n / 2) & 1);
           if (!ok) break;
