@@ -280,12 +280,22 @@ int product(const Operand &a, const Operand &b, int64_t K, pj::Params p, int dty
   if (e != cudaSuccess) return HYENA_ERR_CUDA;
   if (p.splits == 1 || pl.join) return HYENA_OK;
   const TileShape &t = kShapes[pl.shape];
-  const int64_t n = (pl.tiles_m * pl.tiles_n - pl.whole) * std::min<int64_t>(t.m, p.M) * (t.n / 4);
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((n + 255) / 256, 8 * d.info.sm_count));
-  return hyena::host::launch(pj::proj_join_kernel<T>, dim3(grid), dim3(256), 0, stream, p, t.m,
-                             t.n) == cudaSuccess
-             ? HYENA_OK
-             : HYENA_ERR_CUDA;
+  const int64_t rest = pl.tiles_m * pl.tiles_n - pl.whole;
+  const int64_t quads = std::min<int64_t>(t.m, p.M) * (t.n / 4);
+  const int64_t want = std::max<int64_t>(1, 8 * d.info.sm_count / rest);
+  const dim3 grid(static_cast<unsigned>(std::min((quads + 255) / 256, want)),
+                  static_cast<unsigned>(rest));
+  const auto join = [&](auto *kernel) {
+    return hyena::host::launch(kernel, grid, dim3(256), 0, stream, p);
+  };
+  switch (pl.shape) {
+    case kPair256:
+      if constexpr (sizeof(T) == 2) e = join(pj::proj_join_kernel<T, 256, 256>);
+      break;
+    case kOne128: e = join(pj::proj_join_kernel<T, 128, 128>); break;
+    default: e = join(pj::proj_join_kernel<T, 128, 64>);
+  }
+  return e == cudaSuccess ? HYENA_OK : HYENA_ERR_CUDA;
 }
 
 // Up to two inputs of one row length as operands: themselves, or (`at` advances) bf16 planes in

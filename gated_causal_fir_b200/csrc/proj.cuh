@@ -127,12 +127,20 @@ __device__ __forceinline__ float gelu_slope(float z) {
   return fmaf(z * 0.39894228f, e, z > 0.0f ? 1.0f - tail : tail);
 }
 
+// log(1 + e) for 0 <= e <= 1; for bf16 results the fast logarithm, and near 0, where 1 + e rounds
+// most of e away, three terms of the series (within 2^-20 of the value at e = 2^-6).
+template <typename T>
+__device__ __forceinline__ float log1p_of(float e) {
+  if constexpr (sizeof(T) == 4) return log1pf(e);
+  return e < 0.015625f ? e * fmaf(e, fmaf(e, 0.33333333f, -0.5f), 1.0f) : __logf(1.0f + e);
+}
+
 template <typename T, int kAct>
 __device__ __forceinline__ float act_of(float z) {
   if constexpr (kAct == kGelu) return gelu_of<T>(z);
   if constexpr (kAct == kSilu) return ratio<T>(z, 1.0f + exp_of<T>(-z));
   if constexpr (kAct == kSigmoid) return sigmoid_of<T>(z);
-  if constexpr (kAct == kLogSigmoid) return fminf(z, 0.0f) - log1pf(exp_of<T>(-fabsf(z)));
+  if constexpr (kAct == kLogSigmoid) return fminf(z, 0.0f) - log1p_of<T>(exp_of<T>(-fabsf(z)));
   return z;
 }
 
@@ -922,52 +930,56 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The sums of the cut tiles' partial products, in order, and their epilogue: four columns of a row
-// per thread, rows of tile_m x tile_n tiles.
-template <typename T>
-__global__ void __launch_bounds__(256) proj_join_kernel(const Params p, int tile_m, int tile_n) {
+// The sums of the cut tiles' partial products, in order, and their epilogue: a tile per blockIdx.y,
+// four columns of a row per thread.
+template <typename T, int kM, int kN>
+__global__ void __launch_bounds__(256) proj_join_kernel(const Params p) {
   griddep_launch_dependents();
   griddep_wait();
+  int tm, tn;
+  tile_at(p, p.whole + blockIdx.y, &tm, &tn);
   // rows of a tile that can be in range at all: a product of few rows fills little of its tiles
-  const int rows = min(tile_m, p.M), per_tile = rows * (tile_n / 4);
-  const int64_t n = static_cast<int64_t>(p.tiles_m * p.tiles_n - p.whole) * per_tile;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += step) {
-    const int tile = static_cast<int>(i / per_tile), r = static_cast<int>(i % per_tile);
-    int tm, tn;
-    tile_at(p, p.whole + tile, &tm, &tn);
-    const int in_row = r / (tile_n / 4), in_col = r % (tile_n / 4) * 4;
-    const int64_t row = static_cast<int64_t>(tm) * tile_m + in_row;
-    const int col = tn * tile_n + in_col;
-    if (row >= p.M || col >= p.N) continue;
-    const int64_t size = static_cast<int64_t>(tile_m) * tile_n;
-    const float *from = p.partial + (static_cast<int64_t>(tile) * p.splits) * size + in_row * tile_n + in_col;
+  const int rows = min(kM, p.M - tm * kM);
+  const float *part = p.partial + static_cast<int64_t>(blockIdx.y) * p.splits * (kM * kN);
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < rows * (kN / 4); i += gridDim.x * blockDim.x) {
+    const int r = i / (kN / 4), c4 = i % (kN / 4) * 4, col = tn * kN + c4;
+    if (col >= p.N) continue;
     float c[4] = {0.f, 0.f, 0.f, 0.f};
+    const float *from = part + r * kN + c4;
 #pragma unroll 4
     for (int s = 0; s < p.splits; ++s) {
-      const float4 v = *reinterpret_cast<const float4 *>(from + s * size);
-      c[0] += v.x;
-      c[1] += v.y;
-      c[2] += v.z;
-      c[3] += v.w;
+      const float4 v = *reinterpret_cast<const float4 *>(from + static_cast<int64_t>(s) * (kM * kN));
+      c[0] += v.x, c[1] += v.y, c[2] += v.z, c[3] += v.w;
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) c[e] += p.bias && col + e < p.N ? p.bias[col + e] : 0.0f;
-    finish<T, 4>(p, c, row, col);
+    finish<T, 4>(p, c, static_cast<int64_t>(tm) * kM + r, col);
   }
 }
 
 // ------------------------------------------------------------------------------- operands
-// x as a sum of bf16 planes, each the nearest to what the ones before leave (the first towards
-// zero where the nearest would overflow); values that are not finite stay in the first.
+// Eight values as bf16 planes, each the nearest to what the planes before leave; one plane is the
+// value rounded.  Of three, the first goes towards zero where the nearest would overflow, and values
+// that are not finite stay in it.
 template <int kPlanes>
-__device__ __forceinline__ void planes_of(float x, __nv_bfloat16 (&o)[kPlanes]) {
+__device__ __forceinline__ void planes_of(const float (&v)[8], VecOf<__nv_bfloat16, 8> (&o)[kPlanes]) {
+  if constexpr (kPlanes == 1) {
 #pragma unroll
-  for (int i = 0; i < kPlanes; ++i) {
-    o[i] = __float2bfloat16_rn(x);
-    if (i == 0 && isinf(__bfloat162float(o[0])) && !isinf(x)) o[0] = __float2bfloat16_rz(x);
-    const float rest = x - __bfloat162float(o[i]);
-    x = isfinite(x) ? rest : 0.0f;
+    for (int e = 0; e < 8; e += 2)
+      *reinterpret_cast<__nv_bfloat162 *>(&o[0].e[e]) = __floats2bfloat162_rn(v[e], v[e + 1]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float x = v[e];
+      const bool finite = isfinite(x);
+#pragma unroll
+      for (int q = 0; q < kPlanes; ++q) {
+        __nv_bfloat16 b = __float2bfloat16_rn(x);
+        if (q == 0 && finite && isinf(__bfloat162float(b))) b = __float2bfloat16_rz(x);
+        o[q].e[e] = b;
+        x = finite ? x - __bfloat162float(b) : 0.0f;
+      }
+    }
   }
 }
 
@@ -998,13 +1010,7 @@ __global__ void __launch_bounds__(256)
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = col + e < cols ? to_f(o.src[row * cols + col + e]) : 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      __nv_bfloat16 pl[kPlanes];
-      planes_of<kPlanes>(v[e], pl);
-#pragma unroll
-      for (int q = 0; q < kPlanes; ++q) out[q].e[e] = pl[q];
-    }
+    planes_of<kPlanes>(v, out);
 #pragma unroll
     for (int q = 0; q < kPlanes; ++q)
       *reinterpret_cast<VecOf<__nv_bfloat16, 8> *>(o.dst + (q * o.rows + row) * ld + col) = out[q];
@@ -1053,13 +1059,7 @@ __global__ void __launch_bounds__(256)
     }
     if (dz) {
       VecOf<__nv_bfloat16, 8> o[kPlanes];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        __nv_bfloat16 pl[kPlanes];
-        planes_of<kPlanes>(d[e], pl);
-#pragma unroll
-        for (int q = 0; q < kPlanes; ++q) o[q].e[e] = pl[q];
-      }
+      planes_of<kPlanes>(d, o);
 #pragma unroll
       for (int q = 0; q < kPlanes; ++q)
         *reinterpret_cast<VecOf<__nv_bfloat16, 8> *>(dz + (q * M + row) * ld + col) = o[q];
