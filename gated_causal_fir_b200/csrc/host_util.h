@@ -37,11 +37,11 @@ inline bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
 inline int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
 // Launch with programmatic stream serialisation: the kernel waits (griddepcontrol.wait) before
-// its first access to global memory.
+// its first access to global memory.  In clusters of `cluster` CTAs where that is not 1.
 template <typename... Exp, typename... Act>
-cudaError_t launch(void (*kernel)(Exp...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
-                   Act &&...args) {
-  cudaLaunchAttribute attr[1];
+cudaError_t launch_in_clusters(unsigned cluster, void (*kernel)(Exp...), dim3 grid, dim3 block,
+                               size_t smem, cudaStream_t s, Act &&...args) {
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
@@ -49,9 +49,16 @@ cudaError_t launch(void (*kernel)(Exp...), dim3 grid, dim3 block, size_t smem, c
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {cluster, 1, 1};
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Act>(args)...);
+}
+template <typename... Exp, typename... Act>
+cudaError_t launch(void (*kernel)(Exp...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                   Act &&...args) {
+  return launch_in_clusters(1, kernel, grid, block, smem, s, std::forward<Act>(args)...);
 }
 
 }  // namespace host

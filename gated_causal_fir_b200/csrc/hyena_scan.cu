@@ -48,29 +48,39 @@ int check_shape(const Shape &s) {
   return HYENA_OK;
 }
 
-// Cuts of the time axis.  A CTA streams ~50 GB/s at best (a tile in ~0.8 us), so fewer than ~100
-// columns of 32 channels leave HBM idle; but every cut except one costs a second read of k, v and
-// g, and all of them a launch.  Cut where that saves at least 6 us.
-int64_t split_count(const Shape &s) {
-  constexpr int64_t kCtas = 148;
-  constexpr double kTileUs = 0.8, kAggregateUs = 0.5, kLaunchUs = 6.0;
-  const int64_t blocks = s.B * s.n_cb(), tiles = s.n_tiles();
-  if (blocks * 2 > kCtas) return 1;
-  const int64_t n = std::min(kCtas / blocks, tiles / 2);
-  if (n < 2) return 1;
-  const double whole = static_cast<double>(tiles) * kTileUs;
-  const double cut = static_cast<double>(tiles) / static_cast<double>(n) * (kTileUs + kAggregateUs);
-  return cut + kLaunchUs < whole ? n : 1;
-}
-
-// What `blocks` CTAs' worth of cuts leaves after rounding to whole tiles per cut.
+// How the time axis of a column of 32 channels is shared, where there are too few columns for the
+// device (a CTA streams ~50 GB/s at best, a tile in ~0.8 us): by a cluster whose CTAs take
+// neighbouring tiles and tell each other their (A, S), round by round, or by cuts, whose (A, S) a
+// first pass over k, v and g finds; that reaches more CTAs, but costs a launch and reads three of
+// the five streams again.  Times in us.
 struct Cuts {
-  int splits, tiles_per_split;
+  int splits, tiles_per_split, cluster;
 };
 Cuts cuts_of(const Shape &s) {
-  const int64_t want = split_count(s), nt = s.n_tiles();
-  const int64_t per = (nt + want - 1) / want;
-  return Cuts{static_cast<int>((nt + per - 1) / per), static_cast<int>(per)};
+  constexpr int64_t kCtas = 148;
+  constexpr double kTile = 0.8, kExchange = 0.5, kAggregate = 0.5, kLaunch = 6.0;
+  // clusters of so many CTAs that run at once (GPCs of 16 to 18 SMs)
+  constexpr int kClusters[sc::kMaxCluster + 1] = {0, 148, 66, 40, 32, 20, 16, 8, 8};
+  const int64_t blocks = s.B * s.n_cb(), tiles = s.n_tiles();
+  Cuts best{1, static_cast<int>(tiles), 1};
+  if (blocks * 2 > kCtas) return best;
+  double best_us = static_cast<double>(tiles) * kTile;
+  for (int n = 2; n <= sc::kMaxCluster && n <= tiles; ++n) {
+    const int64_t waves = (blocks + kClusters[n] - 1) / kClusters[n];
+    const double us = static_cast<double>(waves) *
+                      (static_cast<double>((tiles + n - 1) / n) * (kTile + kExchange) + 1.0);
+    if (us < best_us) {
+      best_us = us;
+      best = Cuts{1, static_cast<int>(tiles), n};
+    }
+  }
+  const int64_t want = std::min(kCtas / blocks, tiles / 2);
+  if (want > 1) {
+    const int64_t per = (tiles + want - 1) / want;
+    if (static_cast<double>(per) * (kTile + kAggregate) + kLaunch < best_us)
+      best = Cuts{static_cast<int>((tiles + per - 1) / per), static_cast<int>(per), 1};
+  }
+  return best;
 }
 
 int64_t agg_bytes(const Shape &s) {
@@ -134,11 +144,14 @@ void allow(F *kernel, cudaError_t *e) {
 }
 template <typename C, int kFeed, bool kBackward>
 void allow_smem(cudaError_t *e) {
-  allow(sc::scan_fwd_kernel<C, kFeed, true>, e);
-  allow(sc::scan_fwd_kernel<C, kFeed, false>, e);
+  allow(sc::scan_fwd_kernel<C, kFeed, true, false>, e);
+  allow(sc::scan_fwd_kernel<C, kFeed, true, true>, e);
+  allow(sc::scan_fwd_kernel<C, kFeed, false, false>, e);
   if constexpr (kBackward && kFeed != sc::kTmaRaw) {
-    allow(sc::scan_bwd_kernel<C, kFeed, true>, e);
-    allow(sc::scan_bwd_kernel<C, kFeed, false>, e);
+    allow(sc::scan_fwd_kernel<C, kFeed, false, true>, e);
+    allow(sc::scan_bwd_kernel<C, kFeed, true, false>, e);
+    allow(sc::scan_bwd_kernel<C, kFeed, true, true>, e);
+    allow(sc::scan_bwd_kernel<C, kFeed, false, false>, e);
   }
 }
 
@@ -185,6 +198,7 @@ sc::Params base_params(const Shape &s, const void *g, const hyena::host::DeviceI
   p.n_tiles = static_cast<int>(s.n_tiles());
   p.splits = c.splits;
   p.tiles_per_split = c.tiles_per_split;
+  p.cluster = c.cluster;
   p.pieces = s.d_g % sc::kCh == 0   ? 1
              : sc::kCh % s.d_g == 0 ? sc::kCh / s.d_g
                                     : (sc::kCh + s.d_g - 2) / s.d_g + 1;
@@ -219,12 +233,12 @@ Launch plan(sc::Params &p, int feed, int streams, int first, int count, int sm_c
   p.unit_splits = count;
   p.n_units = p.B * count * p.n_cb;
   Launch l;
-  l.grid = static_cast<unsigned>(std::min(p.n_units, sm_count));
+  l.grid = static_cast<unsigned>(p.cluster > 1 ? p.n_units * p.cluster : std::min(p.n_units, sm_count));
   l.smem = static_cast<size_t>(p.stages) * p.stage_bytes + sc::kStageAlign;
   return l;
 }
 
-template <typename C, int kFeed, bool kOut>
+template <typename C, int kFeed, bool kOut, bool kCl>
 int run_fwd(const Shape &s, sc::Params p, int first, int count, int sms, cudaStream_t stream) {
   const Launch l = plan<C>(p, kFeed, kOut ? 3 : 2, first, count, sms);
   CUtensorMap mk{}, mv{}, mq{}, mg{};
@@ -234,14 +248,15 @@ int run_fwd(const Shape &s, sc::Params p, int first, int count, int sms, cudaStr
         (s.d_g > 1 && p.g_feed == sc::kGroupsTma && encode(&mg, s, p.g, s.G(), p.g_box)))
       return HYENA_ERR_CUDA;
   }
-  return hyena::host::launch(sc::scan_fwd_kernel<C, kFeed, kOut>, dim3(l.grid),
+  return hyena::host::launch_in_clusters(
+             kCl ? p.cluster : 1, sc::scan_fwd_kernel<C, kFeed, kOut, kCl>, dim3(l.grid),
                              dim3(sc::kThreads), l.smem, stream, mk, mv, mq, mg,
                              p) == cudaSuccess
              ? HYENA_OK
              : HYENA_ERR_CUDA;
 }
 
-template <typename C, int kFeed, bool kOut>
+template <typename C, int kFeed, bool kOut, bool kCl>
 int run_bwd(const Shape &s, sc::Params p, int first, int count, int sms, cudaStream_t stream) {
   const Launch l = plan<C>(p, kFeed, kOut ? 4 : 2, first, count, sms);
   CUtensorMap mq{}, mdy{}, mk{}, mv{}, mg{};
@@ -251,7 +266,8 @@ int run_bwd(const Shape &s, sc::Params p, int first, int count, int sms, cudaStr
         (s.d_g > 1 && p.g_feed == sc::kGroupsTma && encode(&mg, s, p.g, s.G(), p.g_box)))
       return HYENA_ERR_CUDA;
   }
-  return hyena::host::launch(sc::scan_bwd_kernel<C, kFeed, kOut>, dim3(l.grid),
+  return hyena::host::launch_in_clusters(
+             kCl ? p.cluster : 1, sc::scan_bwd_kernel<C, kFeed, kOut, kCl>, dim3(l.grid),
                              dim3(sc::kThreads), l.smem, stream, mq, mdy, mk, mv, mg,
                              p) == cudaSuccess
              ? HYENA_OK
@@ -266,11 +282,12 @@ int states(const Shape &s, sc::Params p, float2 *agg, int sms, cudaStream_t stre
     a.agg = agg;
     a.ckpt = nullptr;
     a.s_out = nullptr;
-    const int rc = run_fwd<C, kFeed, false>(s, a, 0, p.splits - 1, sms, stream);
+    const int rc = run_fwd<C, kFeed, false, false>(s, a, 0, p.splits - 1, sms, stream);
     if (rc != HYENA_OK) return rc;
     p.agg = agg;
   }
-  return run_fwd<C, kFeed, kOut>(s, p, 0, p.splits, sms, stream);
+  if (p.cluster > 1) return run_fwd<C, kFeed, kOut, true>(s, p, 0, 1, sms, stream);
+  return run_fwd<C, kFeed, kOut, false>(s, p, 0, p.splits, sms, stream);
 }
 
 template <typename C, int kFeed>
@@ -293,10 +310,11 @@ int backward(const Shape &s, sc::Params p, void *ws, int sms, cudaStream_t strea
   }
   if (p.splits > 1) {
     p.agg = agg;
-    rc = run_bwd<C, kFeed, false>(s, p, 1, p.splits - 1, sms, stream);
+    rc = run_bwd<C, kFeed, false, false>(s, p, 1, p.splits - 1, sms, stream);
     if (rc != HYENA_OK) return rc;
   }
-  rc = run_bwd<C, kFeed, true>(s, p, 0, p.splits, sms, stream);
+  rc = p.cluster > 1 ? run_bwd<C, kFeed, true, true>(s, p, 0, 1, sms, stream)
+                     : run_bwd<C, kFeed, true, false>(s, p, 0, p.splits, sms, stream);
   if (rc != HYENA_OK || p.dg_mode == 0) return rc;
   const int64_t n = s.B * s.L * s.G();
   const int width = p.dg_mode == 1 ? s.d_g / sc::kCh : s.d_g;

@@ -104,6 +104,7 @@ struct Params {
   int n_cb, n_tiles, splits, tiles_per_split;
   int unit_split0, unit_splits;     // the cuts this launch works on
   int n_units;                      // B x unit_splits x n_cb
+  int cluster;                      // CTAs that share a unit's tiles (kCl)
   int pieces, piece_bits;           // groups a block of 32 channels touches at most; and the
                                     // least power of two that holds them
   int g_feed;                       // how the groups' rows of g arrive (GroupFeed)
@@ -194,6 +195,61 @@ struct Unit {
     tile1 = min(tile0 + p.tiles_per_split, p.n_tiles);
   }
 };
+
+// The tiles of a unit that this CTA takes: `first`, then every step-th up to (kReverse: down to)
+// the unit's bound.  kCl: every cluster-th one, in rounds; the last (kReverse: first) round may lie
+// past the unit's tiles for it.
+template <bool kCl, bool kReverse>
+struct Walk {
+  int first, step, end;
+  __device__ Walk(const Params &p, const Unit &u, int rank) {
+    const int size = kCl ? p.cluster : 1;
+    const int rounds = (u.tile1 - u.tile0 + size - 1) / size;
+    first = u.tile0 + (kReverse ? (rounds - 1) * size : 0) + (kCl ? rank : 0);
+    step = kReverse ? -size : size;
+    end = kReverse ? u.tile0 : u.tile0 + rounds * size;
+  }
+  __device__ bool more(int tile) const { return kReverse ? tile >= end : tile < end; }
+};
+
+// The CTA's rank in its cluster.
+__device__ __forceinline__ int cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return static_cast<int>(r);
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                   : "memory");
+}
+
+// What the CTAs of a cluster tell each other in a round: the (A, S) of the tile that each took.
+struct Exchange {
+  ulonglong2 of[2][8][kCh / 2];
+  uint64_t all[2];  // the round's bytes from every CTA
+};
+constexpr int kMaxCluster = 8;
+
+// Sends this tile's (A, S) (one warp; lane l and 16 + l hold the same) to every CTA of the cluster:
+// stores that count their bytes on the receiver's barrier, one way.
+__device__ __forceinline__ void send(Exchange &x, int round, int rank, int size, F2 A, F2 S) {
+  const int lane = threadIdx.x % 32;
+  if (lane == 0) mbar_arrive_expect_tx(&x.all[round & 1], size * (kCh / 2) * 16);
+  const uint32_t slot = smem_u32(&x.of[round & 1][rank][lane % 16]);
+  const uint32_t bar = smem_u32(&x.all[round & 1]);
+  for (int to = lane / 16; to < size; to += 2)
+    asm volatile(
+        "{\n\t.reg .u32 a, b;\n\tmapa.shared::cluster.u32 a, %0, %2;\n\t"
+        "mapa.shared::cluster.u32 b, %1, %2;\n\t"
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [a], {%3, %4}, [b];\n\t}" ::"r"(
+            slot),
+        "r"(bar), "r"(to), "l"(A), "l"(S)
+        : "memory");
+}
+// Waits until every CTA's word of this round is here.
+__device__ __forceinline__ bool received(Exchange &x, int round, Ring &ring, const Params &p) {
+  return mbar_wait(&x.all[round & 1], (round >> 1) & 1, &ring.abort, p.status, kTimeout);
+}
 
 // One decay per row and group of the block by the warps [0, warps): lanes take groups first, in a
 // power of two of columns (p.piece_bits), so that no index is divided; g_at(row, group) is the log
@@ -358,7 +414,7 @@ __device__ __forceinline__ bool store_arrivals(const Params &p) {
 
 // The helper warps: NS streams of every tile of the CTA's units into the ring, in the order the
 // compute warps take them (kReverse: last tile first).
-template <typename C, int kFeed, bool kReverse, int NS>
+template <typename C, int kFeed, bool kReverse, int NS, bool kCl>
 __device__ __forceinline__ void feed(const Params &p, Ring &ring, uint8_t *stages,
                                      const CUtensorMap *const (&maps)[5],
                                      const void *const (&ptrs)[5]) {
@@ -377,11 +433,14 @@ __device__ __forceinline__ void feed(const Params &p, Ring &ring, uint8_t *stage
   if (kFeed == kTmaChannel && warp != 0) return;
   if (kFeed == kTmaRaw && warp != 0 && !copies) return;
   int it = 0, last = 0;
-  for (int u = blockIdx.x; u < p.n_units; u += gridDim.x) {
+  const int size = kCl ? p.cluster : 1, rank = kCl ? cluster_rank() : 0;
+  for (int u = blockIdx.x / size; u < p.n_units; u += gridDim.x / size) {
     const Unit un(p, u);
+    const Walk<kCl, kReverse> walk(p, un, rank);
     const int c0 = un.cb * kCh;
-    for (int i = un.tile0; i < un.tile1; ++i, ++it) {
-      const int tile = kReverse ? un.tile1 - 1 - (i - un.tile0) : i, t0 = tile * tile_rows<C>();
+    for (int tile = walk.first; walk.more(tile); tile += walk.step) {
+      if (kCl && tile >= un.tile1) continue;
+      const int t0 = tile * tile_rows<C>();
       const int st = it % p.stages, round = it / p.stages;
       uint8_t *buf = stages + st * p.stage_bytes;
       float *as = reinterpret_cast<float *>(buf + NS * kBytes);  // decays (kTmaGroup)
@@ -435,6 +494,7 @@ __device__ __forceinline__ void feed(const Params &p, Ring &ring, uint8_t *stage
         if (copy_arrivals<kFeed>(p)) arrive_after_copies(&ring.full[st]);
         if (store_arrivals<kFeed>(p)) mbar_arrive(&ring.full[st]);
       }
+      ++it;
     }
   }
 out:
@@ -592,10 +652,25 @@ constexpr int kWarps = kComputeThreads / 32;
 
 __device__ __forceinline__ F2 from_other_half(F2 x) { return __shfl_xor_sync(0xffffffffu, x, 16); }
 
+// The cluster's barriers exist before a peer arrives on them, and a CTA stays until the last has.
+__device__ __forceinline__ void exchange_init(Exchange &x) {
+  if (threadIdx.x == 0) {
+    mbar_init(&x.all[0], 1);
+    mbar_init(&x.all[1], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  cluster_sync();
+}
+__device__ __forceinline__ void exchange_end() {
+  __syncwarp();
+  cluster_sync();
+}
+
 // ---------------------------------------------------------------------------- forward
 // kOut: y and the last state (streams k, v, q); otherwise only states: checkpoints, or the (A, S)
 // of the unit's time cut from a zero state (streams k, v).
-template <typename C, int kFeed, bool kOut>
+template <typename C, int kFeed, bool kOut, bool kCl>
 __global__ void __launch_bounds__(kThreads, 1)
     scan_fwd_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                     const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg,
@@ -608,21 +683,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int R = C::R, NS = kOut ? 3 : 2, kBytes = stream_bytes<C>();
   using Raw = typename Pair<T>::Raw;
   using Dec = Decays<C, kFeed>;
+  __shared__ Exchange xch;
   ring_init<kFeed>(p, ring);
+  if (kCl) exchange_init(xch);
   griddep_launch_dependents();
   griddep_wait();
   if (threadIdx.x >= kComputeThreads) {
     const CUtensorMap *const maps[5] = {&mk, &mv, kOut ? &mq : &mg, &mg, &mg};
     const void *const ptrs[5] = {p.k, p.v, kOut ? p.q : p.g, p.g, nullptr};
-    feed<C, kFeed, false, NS>(p, ring, stages, maps, ptrs);
+    feed<C, kFeed, false, NS, kCl>(p, ring, stages, maps, ptrs);
+    if (kCl) exchange_end();
     return;
   }
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, l = lane % 16;
   const int seg = threadIdx.x / 16;
   const bool second = lane >= 16;
+  const int size = kCl ? p.cluster : 1, rank = kCl ? cluster_rank() : 0;
   bool dead = false;
-  int it = 0;
-  for (int u = blockIdx.x; u < p.n_units; u += gridDim.x) {
+  int round = 0, empty = 0;  // tiles, and rounds without one
+  for (int u = blockIdx.x / size; u < p.n_units; u += gridDim.x / size) {
     const Unit un(p, u);
     const int c0 = un.cb * kCh, c = c0 + 2 * l;
     const bool from_zero = !kOut && !p.ckpt;  // (A, S) of a cut
@@ -633,8 +712,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < un.split; ++j)
         carry = through_cut(agg + static_cast<int64_t>(j) * p.D, c, p.D, carry);
     }
-    for (int tile = un.tile0; tile < un.tile1; ++tile, ++it) {
-      const int st = it % p.stages;
+    const Walk<kCl, false> walk(p, un, rank);
+    for (int tile = walk.first; walk.more(tile); tile += walk.step, ++round) {
+      const int buffer = round & 1;
+      if (kCl && tile >= un.tile1) {  // an empty round: the state passes unchanged
+        compute_barrier();  // nobody here still reads what peers may overwrite after this send
+        if (warp == 0) send(xch, round, rank, size, kOnes, 0);
+        if (!received(xch, round, ring, p)) dead = true;
+        for (int j = 0; j < size; ++j) {
+          const ulonglong2 m = xch.of[buffer][j][l];
+          carry = fma2(m.x, carry, m.y);
+        }
+        ++empty;
+        continue;
+      }
+      const int it = kCl ? round - empty : round, st = it % p.stages;
       const uint8_t *buf = stages + st * p.stage_bytes;
       if (!mbar_wait(&ring.full[st], (it / p.stages) & 1, &ring.abort, p.status, kTimeout))
         dead = true;
@@ -659,19 +751,43 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // the halves of the warp, joined by the first; the second keeps the first's
       const F2 Ao = from_other_half(A), So = from_other_half(S);
-      if (!second) joint[it & 1][warp][l] = make_ulonglong2(mul2(Ao, A), fma2(Ao, S, So));
+      if (!second) joint[buffer][warp][l] = make_ulonglong2(mul2(Ao, A), fma2(Ao, S, So));
       __syncwarp();
       if (lane == 0) mbar_arrive(&ring.empty[st]);  // the segment is in registers
       compute_barrier();
-      if (p.ckpt && seg == 0 && !dead)
-        put_state(p.ckpt, static_cast<int64_t>(un.b) * p.n_tiles + tile, c, p.D, carry);
       F2 s = carry;
+      if constexpr (kCl) {
+        // the tile as a whole and up to this warp; then the tiles of the round, in order
+        F2 Ap = kOnes, Sp = 0, At = kOnes, St = 0;
 #pragma unroll
-      for (int j = 0; j < kWarps; ++j) {
-        const ulonglong2 m = joint[it & 1][j][l];
-        if (j == warp) s = carry;
-        carry = fma2(m.x, carry, m.y);
-        if (!kOut) whole = mul2(whole, m.x);
+        for (int j = 0; j < kWarps; ++j) {
+          const ulonglong2 m = joint[buffer][j][l];
+          if (j == warp) Ap = At, Sp = St;
+          St = fma2(m.x, St, m.y);
+          At = mul2(At, m.x);
+        }
+        if (warp == 0) send(xch, round, rank, size, At, St);
+        if (!received(xch, round, ring, p)) dead = true;
+#pragma unroll
+        for (int j = 0; j < kMaxCluster; ++j) {
+          if (j >= size) break;
+          const ulonglong2 m = xch.of[buffer][j][l];
+          if (j == rank) s = carry;
+          carry = fma2(m.x, carry, m.y);
+        }
+        if (p.ckpt && seg == 0 && !dead)
+          put_state(p.ckpt, static_cast<int64_t>(un.b) * p.n_tiles + tile, c, p.D, s);
+        s = fma2(Ap, s, Sp);
+      } else {
+        if (p.ckpt && seg == 0 && !dead)
+          put_state(p.ckpt, static_cast<int64_t>(un.b) * p.n_tiles + tile, c, p.D, carry);
+#pragma unroll
+        for (int j = 0; j < kWarps; ++j) {
+          const ulonglong2 m = joint[buffer][j][l];
+          if (j == warp) s = carry;
+          carry = fma2(m.x, carry, m.y);
+          if (!kOut) whole = mul2(whole, m.x);
+        }
       }
       if (kOut) {
         if (second) s = fma2(Ao, s, So);
@@ -684,10 +800,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (seg == 0 && !dead) {
-      if (p.s_out && un.tile1 == p.n_tiles) put_state(p.s_out, un.b, c, p.D, carry);
+      if (p.s_out && un.tile1 == p.n_tiles && rank == 0) put_state(p.s_out, un.b, c, p.D, carry);
       if (from_zero) put_cut(agg + static_cast<int64_t>(un.split) * p.D, c, p.D, whole, carry);
     }
   }
+  if (kCl) exchange_end();
 }
 
 // ---------------------------------------------------------------------------- backward
@@ -716,7 +833,7 @@ __device__ __forceinline__ void sum_groups(const float (&v)[R], int l, F &&put) 
 
 // kOut: the gradients (streams q, dy, k, v and the checkpoints); otherwise the (A, W) of the
 // unit's time cut from w = 0 (streams q, dy).
-template <typename C, int kFeed, bool kOut>
+template <typename C, int kFeed, bool kOut, bool kCl>
 __global__ void __launch_bounds__(kThreads, 1)
     scan_bwd_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mdy,
                     const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
@@ -730,21 +847,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int R = C::R, NS = kOut ? 4 : 2, kBytes = stream_bytes<C>();
   using Raw = typename Pair<T>::Raw;
   using Dec = Decays<C, kFeed>;
+  __shared__ Exchange xch;
   ring_init<kFeed>(p, ring);
+  if (kCl) exchange_init(xch);
   griddep_launch_dependents();
   griddep_wait();
   if (threadIdx.x >= kComputeThreads) {
     const CUtensorMap *const maps[5] = {&mq, &mdy, kOut ? &mk : &mg, &mv, &mg};
     const void *const ptrs[5] = {p.q, p.dy, kOut ? p.k : p.g, p.v, p.g};
-    feed<C, kFeed, true, NS>(p, ring, stages, maps, ptrs);
+    feed<C, kFeed, true, NS, kCl>(p, ring, stages, maps, ptrs);
+    if (kCl) exchange_end();
     return;
   }
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, l = lane % 16;
   const int seg = threadIdx.x / 16;
   const bool second = lane >= 16;
+  const int size = kCl ? p.cluster : 1, rank = kCl ? cluster_rank() : 0;
   bool dead = false;
-  int it = 0;
-  for (int u = blockIdx.x; u < p.n_units; u += gridDim.x) {
+  int round = 0, empty = 0;  // tiles, and rounds without one
+  for (int u = blockIdx.x / size; u < p.n_units; u += gridDim.x / size) {
     const Unit un(p, u);
     const int c0 = un.cb * kCh, c = c0 + 2 * l;
     float2 *agg = p.agg + static_cast<int64_t>(un.b) * p.splits * p.D;
@@ -755,13 +876,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         w_in = through_cut(agg + static_cast<int64_t>(j) * p.D, c, p.D, w_in);
     }
     const int64_t ckpt0 = static_cast<int64_t>(un.b) * p.n_tiles;
+    const Walk<kCl, true> walk(p, un, rank);
     F2 start = 0;  // the state before the tile, requested a tile ahead
-    if (kOut) start = get_state(p.ckpt, ckpt0 + un.tile1 - 1, c, p.D);
-    for (int tile = un.tile1 - 1; tile >= un.tile0; --tile, ++it) {
-      const int st = it % p.stages;
-      const uint8_t *buf = stages + st * p.stage_bytes;
+    if (kOut && walk.first < un.tile1) start = get_state(p.ckpt, ckpt0 + walk.first, c, p.D);
+    for (int tile = walk.first; walk.more(tile); tile += walk.step, ++round) {
+      const int buffer = round & 1;
       F2 s = start;
-      if (kOut && tile > un.tile0) start = get_state(p.ckpt, ckpt0 + tile - 1, c, p.D);
+      if (kOut && walk.more(tile + walk.step))
+        start = get_state(p.ckpt, ckpt0 + tile + walk.step, c, p.D);
+      if (kCl && tile >= un.tile1) {  // an empty round: w passes unchanged
+        compute_barrier();  // nobody here still reads what peers may overwrite after this send
+        if (warp == 0) send(xch, round, rank, size, kOnes, 0);
+        if (!received(xch, round, ring, p)) dead = true;
+        for (int j = size - 1; j >= 0; --j) {
+          const ulonglong2 m = xch.of[buffer][j][l];
+          w_in = fma2(m.x, w_in, m.y);
+        }
+        ++empty;
+        continue;
+      }
+      const int it = kCl ? round - empty : round, st = it % p.stages;
+      const uint8_t *buf = stages + st * p.stage_bytes;
       if (!mbar_wait(&ring.full[st], (it / p.stages) & 1, &ring.abort, p.status, kTimeout))
         dead = true;
       Raw qr[R], dyr[R], kr[R], vr[R];
@@ -790,8 +925,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const F2 Ao = from_other_half(A), So = from_other_half(S), Wo = from_other_half(W);
       if (!second) {  // S through the second half, W through the first
-        joint[it & 1][warp][l] = make_ulonglong2(mul2(Ao, A), fma2(Ao, S, So));
-        joint_w[it & 1][warp][l] = fma2(A, Wo, W);
+        joint[buffer][warp][l] = make_ulonglong2(mul2(Ao, A), fma2(Ao, S, So));
+        joint_w[buffer][warp][l] = fma2(A, Wo, W);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ring.empty[st]);
@@ -800,16 +935,38 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int j = 0; j < kWarps; ++j) {  // states before each warp's rows, in order
         if (!kOut) break;
-        const ulonglong2 m = joint[it & 1][j][l];
+        const ulonglong2 m = joint[buffer][j][l];
         if (j == warp) s = state;
         state = fma2(m.x, state, m.y);
       }
+      if constexpr (kCl) {
+        // what reaches the tile's first row and this warp's last, from 0; then the round's tiles
+        F2 Ap = kOnes, Wp = 0, At = kOnes, Wt = 0;
 #pragma unroll
-      for (int j = kWarps - 1; j >= 0; --j) {  // what reaches the end of each, backwards
-        const F2 m = joint[it & 1][j][l].x;
-        if (j == warp) w = w_in;
-        w_in = fma2(m, w_in, joint_w[it & 1][j][l]);
-        if (!kOut) whole = mul2(whole, m);
+        for (int j = kWarps - 1; j >= 0; --j) {
+          const F2 m = joint[buffer][j][l].x;
+          if (j == warp) Ap = At, Wp = Wt;
+          Wt = fma2(m, Wt, joint_w[buffer][j][l]);
+          At = mul2(At, m);
+        }
+        if (warp == 0) send(xch, round, rank, size, At, Wt);
+        if (!received(xch, round, ring, p)) dead = true;
+#pragma unroll
+        for (int j = kMaxCluster - 1; j >= 0; --j) {
+          if (j >= size) continue;
+          const ulonglong2 m = xch.of[buffer][j][l];
+          if (j == rank) w = w_in;
+          w_in = fma2(m.x, w_in, m.y);
+        }
+        w = fma2(Ap, w, Wp);
+      } else {
+#pragma unroll
+        for (int j = kWarps - 1; j >= 0; --j) {  // what reaches the end of each, backwards
+          const F2 m = joint[buffer][j][l].x;
+          if (j == warp) w = w_in;
+          w_in = fma2(m, w_in, joint_w[buffer][j][l]);
+          if (!kOut) whole = mul2(whole, m);
+        }
       }
       if (kOut) {
         if (second)
@@ -868,10 +1025,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (seg == 0 && !dead) {
-      if (kOut && p.ds0 && un.tile0 == 0) put_state(p.ds0, un.b, c, p.D, w_in);
+      if (kOut && p.ds0 && un.tile0 == 0 && rank == 0) put_state(p.ds0, un.b, c, p.D, w_in);
       if (!kOut) put_cut(agg + static_cast<int64_t>(un.split) * p.D, c, p.D, whole, w_in);
     }
   }
+  if (kCl) exchange_end();
 }
 
 // dg of group j in a row: the sum of `width` neighbouring partial sums, in order.

@@ -44,7 +44,10 @@ SHAPES = [
     (1, 300, 1, 1), (1, 143, 64, 4), (2, 144, 64, 2), (1, 145, 128, 32), (1, 289, 264, 4),
     (2, 300, 66, 2), (1, 700, 100, 2),
     (2, 200, 1732, 2), (1, 310, 440, 8), (1, 300, 488, 8), (1, 200, 272, 16), (2, 180, 192, 96),
-    (1, 200, 208, 4), (1, 150, 24, 2), (1, 330, 50, 10), (1, 5000, 32, 1), (1, 4000, 72, 24), (5, 190, 1024, 1), (160, 3, 64, 32),
+    (1, 200, 208, 4), (1, 150, 24, 2), (1, 330, 50, 10),
+    # clusters of 2 to 8 CTAs, with and without an empty last round; the time axis cut
+    (1, 530, 96, 1), (2, 900, 64, 32), (1, 1250, 320, 64), (3, 1410, 100, 2), (1, 2500, 36, 1),
+    (1, 1600, 512, 16), (1, 9000, 48, 48), (2, 20000, 8, 1), (1, 5000, 32, 1), (1, 4000, 72, 24), (5, 190, 1024, 1), (160, 3, 64, 32),
 ]
 
 
