@@ -49,18 +49,26 @@ int check_shape(const Shape &s) {
 }
 
 // How the time axis of a column of 32 channels is shared, where there are too few columns for the
-// device (a CTA streams ~50 GB/s at best, a tile in ~0.8 us): by a cluster whose CTAs take
-// neighbouring tiles and tell each other their (A, S), round by round, or by cuts, whose (A, S) a
-// first pass over k, v and g finds; that reaches more CTAs, but costs a launch and reads three of
-// the five streams again.  Times in us.
+// device (a CTA streams ~50 GB/s at best): by a cluster whose CTAs take neighbouring tiles and tell
+// each other their (A, S), round by round, or by cuts, whose (A, S) a first pass over k, v and g
+// finds; that reaches more CTAs, but costs a launch and reads three of the five streams again.  The
+// constants are us a tile, from both sides' measurements of bf16 forwards:
+//                              alone   cluster    cuts
+//   [1, 8192, 2048], d_g 64     46.2      35.5    47.1
+//   [2, 5000, 512],  d_g 64     29.2      14.1    19.7
+//   [1, 65536, 496], d_g 1     386.7     104.6   105.1   (backward 825.7, 168.3, 151.1)
+//   [1, 65536, 500], d_g 1     519.0     135.0   116.8   (backward 1454, 271.0, 224.1)
+//   [1, 65536, 498], d_g 2      1855     318.2   404.8   (rows by single elements)
 struct Cuts {
   int splits, tiles_per_split, cluster;
 };
 Cuts cuts_of(const Shape &s) {
   constexpr int64_t kCtas = 148;
-  constexpr double kTile = 0.8, kExchange = 0.5, kAggregate = 0.5, kLaunch = 6.0;
-  // clusters of so many CTAs that run at once (GPCs of 16 to 18 SMs)
-  constexpr int kClusters[sc::kMaxCluster + 1] = {0, 148, 66, 40, 32, 20, 16, 8, 8};
+  constexpr double kTile = 1.0, kExchange = 0.7, kLaunch = 6.0;
+  const double two_passes = s.D * s.es() % 8 == 0 ? 2.4 : 3.2;
+  // clusters of so many CTAs that run at once, a little below what the occupancy query answers (74,
+  // 45, 33, 26, 22, 15, 15), since it varies with the SMs that a GPC has
+  constexpr int kClusters[sc::kMaxCluster + 1] = {0, 148, 72, 44, 32, 24, 20, 14, 14};
   const int64_t blocks = s.B * s.n_cb(), tiles = s.n_tiles();
   Cuts best{1, static_cast<int>(tiles), 1};
   if (blocks * 2 > kCtas) return best;
@@ -77,7 +85,7 @@ Cuts cuts_of(const Shape &s) {
   const int64_t want = std::min(kCtas / blocks, tiles / 2);
   if (want > 1) {
     const int64_t per = (tiles + want - 1) / want;
-    if (static_cast<double>(per) * (kTile + kAggregate) + kLaunch < best_us)
+    if (static_cast<double>(per) * two_passes + kLaunch < best_us)
       best = Cuts{static_cast<int>((tiles + per - 1) / per), static_cast<int>(per), 1};
   }
   return best;

@@ -10,12 +10,13 @@
 //     u_t = q_t dy_t + w_{t+1},   w_t = a_t u_t      (u = dLoss/ds_t, w what reaches s_{t-1})
 //     dq = dy s,   dk = u v,   dv = u k,   dg = sum over the group of w_t s_{t-1}.
 //
-// Split: a CTA owns 32 channels of one sequence and walks its rows in tiles of 16 R; nothing is
-// exchanged between CTAs, so the sums have one order and the result is the same in every run.
-// (A row of 32 channels is 64 bytes in bf16.  At D = 4096 that gives 128 CTAs; a wider piece
-// would leave most of the 148 SMs without work.)  Where a problem has too few such columns for
-// the device, its time axis is cut as well: a first pass over k, v and g finds each cut's
-// (A, S), and every CTA of the second pass joins those before it.
+// Split: a CTA owns 32 channels of one sequence and walks its rows in tiles of 16 R.  (A row of
+// 32 channels is 64 bytes in bf16.  At D = 4096 that gives 128 CTAs; a wider piece would leave most
+// of the 148 SMs without work.)  Where a problem has too few such columns for the device, its time
+// axis is shared as well: by a cluster of CTAs that take neighbouring tiles and send each other
+// their (A, S) through distributed shared memory, or by cuts, whose (A, S) a first pass over k, v
+// and g finds and every CTA of the second pass joins.  Either way the sums have one order and the
+// result is the same in every run.
 //
 // Within a CTA: one warp streams the tiles in with TMA through a ring of shared-memory stages;
 // eight warps compute.  Half a warp (16 lanes of 2 channels) owns a segment of R consecutive
