@@ -24,14 +24,11 @@ constexpr int64_t kI32 = std::numeric_limits<int32_t>::max();
 struct Shape {
   int64_t B, L, D;
   int d_g, dtype;
-  bool train = false;  // the backward's tiles (checkpoints)
   int64_t es() const { return dtype == HYENA_DTYPE_F32 ? 4 : 2; }
   int64_t G() const { return D / d_g; }
   int64_t n_cb() const { return (D + sc::kCh - 1) / sc::kCh; }
   int64_t rows() const {
-    return dtype == HYENA_DTYPE_F32 ? sc::tile_rows<sc::F32>()
-           : train                  ? sc::tile_rows<sc::Bf16Train>()
-                                    : sc::tile_rows<sc::Bf16>();
+    return dtype == HYENA_DTYPE_F32 ? sc::tile_rows<sc::F32>() : sc::tile_rows<sc::Bf16>();
   }
   int64_t n_tiles() const { return (L + rows() - 1) / rows(); }
   int64_t numel() const { return B * L * D; }
@@ -150,15 +147,25 @@ void allow(F *kernel, cudaError_t *e) {
     *e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax - kStaticSmem);
 }
-template <typename C, int kFeed, bool kBackward>
+// A kernel that moves registers between its warps waits for ever if it starts with fewer than it
+// counts on, so what it was compiled to is looked up.
+template <typename F>
+void allow_registers(F *kernel, cudaError_t *e) {
+  cudaFuncAttributes a{};
+  if (*e == cudaSuccess) *e = cudaFuncGetAttributes(&a, reinterpret_cast<const void *>(kernel));
+  if (*e == cudaSuccess && a.numRegs < sc::kStartRegs) *e = cudaErrorInvalidConfiguration;
+}
+template <typename C, int kFeed>
 void allow_smem(cudaError_t *e) {
   allow(sc::scan_fwd_kernel<C, kFeed, true, false>, e);
   allow(sc::scan_fwd_kernel<C, kFeed, true, true>, e);
   allow(sc::scan_fwd_kernel<C, kFeed, false, false>, e);
-  if constexpr (kBackward && kFeed != sc::kTmaRaw) {
+  if constexpr (kFeed != sc::kTmaRaw) {
     allow(sc::scan_fwd_kernel<C, kFeed, false, true>, e);
     allow(sc::scan_bwd_kernel<C, kFeed, true, false>, e);
     allow(sc::scan_bwd_kernel<C, kFeed, true, true>, e);
+    allow_registers(sc::scan_bwd_kernel<C, kFeed, true, false>, e);
+    allow_registers(sc::scan_bwd_kernel<C, kFeed, true, true>, e);
     allow(sc::scan_bwd_kernel<C, kFeed, false, false>, e);
   }
 }
@@ -184,9 +191,8 @@ int prepare_device(hyena::host::DeviceInfo *info) {
   std::call_once(once[dev], [dev]() {
     cudaError_t e = cudaSuccess;
     with_feed([&](auto feed) {
-      allow_smem<sc::F32, decltype(feed)::value, true>(&e);
-      allow_smem<sc::Bf16Train, decltype(feed)::value, true>(&e);
-      allow_smem<sc::Bf16, decltype(feed)::value, false>(&e);
+      allow_smem<sc::F32, decltype(feed)::value>(&e);
+      allow_smem<sc::Bf16, decltype(feed)::value>(&e);
     });
     err[dev] = e;
   });
@@ -399,20 +405,20 @@ bool misaligned(uintptr_t a, std::initializer_list<const void *> ptrs) {
 extern "C" {
 
 int64_t hyena_scan_ckpt_tiles(int64_t L, int dtype) {
-  const Shape s{1, L, 1, 1, dtype, true};
+  const Shape s{1, L, 1, 1, dtype};
   if (check_shape(s) != HYENA_OK) return -HYENA_ERR_INVALID_ARG;
   return s.n_tiles();
 }
 
 int64_t hyena_scan_workspace_bytes(int64_t B, int64_t L, int64_t D, int d_g, int dtype) {
-  const Shape s{B, L, D, d_g, dtype}, t{B, L, D, d_g, dtype, true};
+  const Shape s{B, L, D, d_g, dtype};
   if (check_shape(s) != HYENA_OK) return -HYENA_ERR_INVALID_ARG;
-  return B == 0 || L == 0 ? 0 : std::max(agg_bytes(s), agg_bytes(t));
+  return B == 0 || L == 0 ? 0 : agg_bytes(s);
 }
 
 int64_t hyena_scan_bwd_workspace_bytes(int64_t B, int64_t L, int64_t D, int d_g, int dtype,
                                        int have_ckpt) {
-  const Shape s{B, L, D, d_g, dtype, true};
+  const Shape s{B, L, D, d_g, dtype};
   if (check_shape(s) != HYENA_OK) return -HYENA_ERR_INVALID_ARG;
   if (B == 0 || L == 0) return 0;
   return agg_bytes(s) + dg_bytes(s) + (have_ckpt ? 0 : ckpt_bytes(s));
@@ -421,7 +427,7 @@ int64_t hyena_scan_bwd_workspace_bytes(int64_t B, int64_t L, int64_t D, int d_g,
 int hyena_scan_fwd(const void *q, const void *k, const void *v, const void *g, const float *s0,
                    void *y, float *s_out, float *ckpt, int64_t B, int64_t L, int64_t D, int d_g,
                    int dtype, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
-  const Shape s{B, L, D, d_g, dtype, ckpt != nullptr};
+  const Shape s{B, L, D, d_g, dtype};
   int rc = check_shape(s);
   if (rc != HYENA_OK) return rc;
   if (misaligned(4, {s0, s_out, ckpt})) return HYENA_ERR_MISALIGNED;
@@ -457,8 +463,7 @@ int hyena_scan_fwd(const void *q, const void *k, const void *v, const void *g, c
     constexpr int kFeed = decltype(f)::value;
     if (dtype == HYENA_DTYPE_F32)
       return forward<sc::F32, kFeed>(s, p, workspace, info.sm_count, stream);
-    return s.train ? forward<sc::Bf16Train, kFeed>(s, p, workspace, info.sm_count, stream)
-                   : forward<sc::Bf16, kFeed>(s, p, workspace, info.sm_count, stream);
+    return forward<sc::Bf16, kFeed>(s, p, workspace, info.sm_count, stream);
   });
 }
 
@@ -466,7 +471,7 @@ int hyena_scan_bwd(const void *q, const void *k, const void *v, const void *g, c
                    const void *dy, const float *ds_out, const float *ckpt, void *dq, void *dk,
                    void *dv, void *dg, float *ds0, int64_t B, int64_t L, int64_t D, int d_g,
                    int dtype, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
-  const Shape s{B, L, D, d_g, dtype, true};
+  const Shape s{B, L, D, d_g, dtype};
   int rc = check_shape(s);
   if (rc != HYENA_OK) return rc;
   if (misaligned(4, {s0, ds_out, ckpt, ds0})) return HYENA_ERR_MISALIGNED;
@@ -512,7 +517,7 @@ int hyena_scan_bwd(const void *q, const void *k, const void *v, const void *g, c
     else
       return dtype == HYENA_DTYPE_F32
                  ? backward<sc::F32, kFeed>(s, p, workspace, info.sm_count, stream)
-                 : backward<sc::Bf16Train, kFeed>(s, p, workspace, info.sm_count, stream);
+                 : backward<sc::Bf16, kFeed>(s, p, workspace, info.sm_count, stream);
   });
 }
 

@@ -31,6 +31,7 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cstdint>
+#include <type_traits>
 
 #include "ptx.cuh"
 
@@ -41,7 +42,7 @@ constexpr int kCh = 32;               // channels of a CTA
 constexpr int kSegs = 16;             // segments of a tile: 8 warps x 2 halves
 constexpr int kComputeThreads = 256;
 constexpr int kHelperWarps = 4;       // warp 0 of them issues TMA, 1..3 form decays (12 warps in
-                                      // all: 3 per scheduler leave a thread 168 registers)
+                                      // all: 3 per scheduler start with 168 registers a thread)
 constexpr int kThreads = kComputeThreads + 32 * kHelperWarps;
 constexpr int kMaxStages = 8;
 constexpr unsigned int kTimeout = 1u; // HYENA_DEVICE_TIMEOUT
@@ -63,17 +64,17 @@ __host__ __device__ constexpr bool per_channel(int feed) {
 enum GroupFeed { kGroupsElement = 0, kGroupsTma = 1, kGroupsCopy = 2 };
 
 // An element type with R, the rows of a segment (a tile has 16 R).  The joining of segments costs
-// the same per tile whatever R is, so the forward takes as many as its registers allow (B=1 L=8192
-// D=4096 d_g=64 bf16: 48 us with 11, 55 with 9); the backward, which holds five values a row where
-// the forward holds three, runs out of them earlier (162 us with 11 and spills, 121 with 9, 133
-// with 7).  Checkpoints tie a training forward to the backward's tiles.
+// the same per tile whatever R is, so it takes as many as registers and the ring allow.  B=1 L=8192
+// D=4096 bf16, forward and backward in us, d_g = 64 | d_g = 1, and L=65536 D=500 d_g=1:
+//     R =  9   55, 109 | 60, 103 | 120, 224
+//     R = 11   49, 107 | 57,  98 | 115, 214
+//     R = 13   49, 101 | 64,  97 | 128, 279   (rings of two or three stages where g is a stream)
 template <typename E, int kRows>
 struct Cfg {
   using T = E;
   static constexpr int R = kRows;
 };
 using Bf16 = Cfg<__nv_bfloat16, 11>;
-using Bf16Train = Cfg<__nv_bfloat16, 9>;
 using F32 = Cfg<float, 7>;
 
 template <typename C>
@@ -610,8 +611,10 @@ struct Out {
     hi = c + 1 < p.D;
     pairs = by_tma(kFeed) || p.pair_out;
   }
+  // kWhole: all rows up to r are inside (live > r)
+  template <bool kWhole = false>
   __device__ void put(int r, F2 x) const {
-    if (r >= live) return;
+    if (!kWhole && r >= live) return;
     T *to = reinterpret_cast<T *>(reinterpret_cast<uint8_t *>(at) +
                                   static_cast<uint64_t>(stride) * static_cast<uint32_t>(r));
     if (pairs) {  // D is even: a pair is inside or outside
@@ -809,27 +812,62 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------- backward
-// Sums over `kSpan` neighbouring lanes of one value per row, kSpan rows at a time: each exchange
-// halves the rows a lane holds, so that lane i of the group ends with row i (kSpan - 1 exchanges
-// for kSpan rows).  put(row, group of lanes, sum) gets each row's.
-template <int kSpan, int R, typename F>
-__device__ __forceinline__ void sum_groups(const float (&v)[R], int l, F &&put) {
+// Sums over 2 kHalf neighbouring lanes of one value per row.  Each exchange halves the rows that a
+// lane holds: of n rows the upper lane keeps those from h = ceil(n / 2) on and gives the others; an
+// odd row out is summed in both.  row(p) is the row that position p holds after the exchanges
+// (rows 9 over 16 lanes: 11 exchanges where sums of each row would take 36).
+template <int kHalf, int n>
+struct GroupSum {
+  static constexpr int h = (n + 1) / 2;
+  using Next = GroupSum<kHalf / 2, h>;
+  static constexpr int kLeft = Next::kLeft;
+  __device__ static __forceinline__ void sum(float *w, int l) {
+    const bool up = l & kHalf;
 #pragma unroll
-  for (int r0 = 0; r0 < R; r0 += kSpan) {
-    float w[kSpan];
-#pragma unroll
-    for (int i = 0; i < kSpan; ++i) w[i] = r0 + i < R ? v[r0 + i] : 0.f;
-#pragma unroll
-    for (int o = kSpan / 2; o >= 1; o /= 2) {
-      const bool up = l & o;
-#pragma unroll
-      for (int i = 0; i < o; ++i) {
-        const float give = up ? w[i] : w[i + o], keep = up ? w[i + o] : w[i];
-        w[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-      }
+    for (int i = 0; i < h; ++i) {
+      const bool pair = i + h < n;
+      const float give = pair && !up ? w[pair ? i + h : i] : w[i];
+      const float keep = pair && up ? w[pair ? i + h : i] : w[i];
+      w[i] = keep + __shfl_xor_sync(0xffffffffu, give, kHalf);
     }
-    put(r0 + l % kSpan, l / kSpan, w[0]);
+    Next::sum(w, l);
   }
+  __device__ static __forceinline__ int row(int p, int l) {
+    const int i = Next::row(p, l);
+    return (l & kHalf) && i + h < n ? i + h : i;
+  }
+};
+template <int n>
+struct GroupSum<0, n> {
+  static constexpr int kLeft = n;
+  __device__ static __forceinline__ void sum(float *, int) {}
+  __device__ static __forceinline__ int row(int p, int) { return p; }
+};
+// put(row, group of lanes, sum) gets each row's.
+template <int kSpan, int R, typename F>
+__device__ __forceinline__ void sum_groups(float (&v)[R], int l, F &&put) {
+  using S = GroupSum<kSpan / 2, R>;
+  S::sum(v, l);
+#pragma unroll
+  for (int i = 0; i < S::kLeft; ++i) put(S::row(i, l), l / kSpan, v[i]);
+}
+
+// The backward holds five values a row where the forward holds three, so its compute warps take
+// registers from the helpers: a block starts with 65536 / 384, rounded down to a multiple of 8, a
+// thread, and the shares sum to what it starts with.  (Without, R = 9 fitted with a few spills,
+// and what is spilled leaves the small L1 beside the ring: 119 us at d_g = 64 instead of 107.)
+constexpr int kStartRegs = 168, kHelperRegs = 88, kComputeRegs = 208;
+static_assert(kComputeThreads % 128 == 0 && kHelperWarps % 4 == 0, "whole warpgroups");
+static_assert(kComputeThreads * kComputeRegs + 32 * kHelperWarps * kHelperRegs <=
+                  kThreads * kStartRegs,
+              "the block's registers");
+template <int n>
+__device__ __forceinline__ void registers_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(n));
+}
+template <int n>
+__device__ __forceinline__ void registers_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(n));
 }
 
 // kOut: the gradients (streams q, dy, k, v and the checkpoints); otherwise the (A, W) of the
@@ -854,12 +892,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch_dependents();
   griddep_wait();
   if (threadIdx.x >= kComputeThreads) {
+    if (kOut) registers_down<kHelperRegs>();
     const CUtensorMap *const maps[5] = {&mq, &mdy, kOut ? &mk : &mg, &mv, &mg};
     const void *const ptrs[5] = {p.q, p.dy, kOut ? p.k : p.g, p.v, p.g};
     feed<C, kFeed, true, NS, kCl>(p, ring, stages, maps, ptrs);
     if (kCl) exchange_end();
     return;
   }
+  if (kOut) registers_up<kComputeRegs>();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, l = lane % 16;
   const int seg = threadIdx.x / 16;
   const bool second = lane >= 16;
@@ -975,34 +1015,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           w = fma2(Ao, w, Wo);
         const int t0 = tile * tile_rows<C>() + seg * R;
-        F2 before[R];  // s_{t-1}
         const Out<T, kFeed> dq(p.dq, p, un.b, t0, c, dead);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          before[r] = s;
-          s = fma2(Dec::pair(a[r]), s, mul2(Pair<T>::f(kr[r]), Pair<T>::f(vr[r])));
-          dq.put(r, mul2(Pair<T>::f(dyr[r]), s));
-        }
         const Out<T, kFeed> dk(p.dk, p, un.b, t0, c, dead), dv(p.dv, p, un.b, t0, c, dead);
         const Out<T, kFeed> dg(p.dg, p, un.b, t0, c, dead);  // where d_g = 1
         float sum[R];
+        // apart for whole tiles, whose stores need no conditions, and for dg by single channels
+        const auto gradients = [&](auto whole, auto single) {
+          constexpr bool kWhole = decltype(whole)::value, kSingle = decltype(single)::value;
+          F2 before[R];  // s_{t-1}
 #pragma unroll
-        for (int r = R - 1; r >= 0; --r) {
-          const F2 ut = fma2(Pair<T>::f(qr[r]), Pair<T>::f(dyr[r]), w);
-          w = mul2(Dec::pair(a[r]), ut);
-          const F2 d = mul2(w, before[r]);
-          dk.put(r, mul2(ut, Pair<T>::f(vr[r])));
-          dv.put(r, mul2(ut, Pair<T>::f(kr[r])));
-          if (per_channel(kFeed)) {
-            dg.put(r, d);
-          } else if (p.dg_mode == 2) {
-            if (r < dg.live)
-              put_state(p.dg_part, static_cast<int64_t>(un.b) * p.L + t0 + r, c, p.D, d);
-          } else {
-            const float2 two = unpack(d);
-            sum[r] = two.x + two.y;
+          for (int r = 0; r < R; ++r) {
+            before[r] = s;
+            s = fma2(Dec::pair(a[r]), s, mul2(Pair<T>::f(kr[r]), Pair<T>::f(vr[r])));
+            dq.template put<kWhole>(r, mul2(Pair<T>::f(dyr[r]), s));
           }
-        }
+#pragma unroll
+          for (int r = R - 1; r >= 0; --r) {
+            const F2 ut = fma2(Pair<T>::f(qr[r]), Pair<T>::f(dyr[r]), w);
+            w = mul2(Dec::pair(a[r]), ut);
+            const F2 d = mul2(w, before[r]);
+            dk.template put<kWhole>(r, mul2(ut, Pair<T>::f(vr[r])));
+            dv.template put<kWhole>(r, mul2(ut, Pair<T>::f(kr[r])));
+            if (per_channel(kFeed)) {
+              dg.template put<kWhole>(r, d);
+            } else if (kSingle) {
+              if (r < dg.live)
+                put_state(p.dg_part, static_cast<int64_t>(un.b) * p.L + t0 + r, c, p.D, d);
+            } else {
+              const float2 two = unpack(d);
+              sum[r] = two.x + two.y;
+            }
+          }
+        };
+        using Yes = std::true_type;
+        using No = std::false_type;
+        if (!per_channel(kFeed) && p.dg_mode == 2)
+          gradients(No(), Yes());
+        else if (by_tma(kFeed) && dq.live >= R)
+          gradients(Yes(), No());
+        else
+          gradients(No(), No());
         if (!per_channel(kFeed) && p.dg_mode != 2) {
           // groups of 2, 4, ..., 16 channels or whole blocks: sums over neighbouring lanes
           const int64_t row0 = static_cast<int64_t>(un.b) * p.L + t0;
