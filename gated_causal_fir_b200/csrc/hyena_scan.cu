@@ -160,7 +160,7 @@ void allow_smem(cudaError_t *e) {
   allow(sc::scan_fwd_kernel<C, kFeed, true, false>, e);
   allow(sc::scan_fwd_kernel<C, kFeed, true, true>, e);
   allow(sc::scan_fwd_kernel<C, kFeed, false, false>, e);
-  if constexpr (kFeed != sc::kTmaRaw) {
+  if constexpr (kFeed != sc::kTmaRaw || sizeof(typename C::T) == 2) {
     allow(sc::scan_fwd_kernel<C, kFeed, false, true>, e);
     allow(sc::scan_bwd_kernel<C, kFeed, true, false>, e);
     allow(sc::scan_bwd_kernel<C, kFeed, true, true>, e);
@@ -341,11 +341,12 @@ int backward(const Shape &s, sc::Params p, void *ws, int sms, cudaStream_t strea
 }
 
 // Which feed takes the tensors, from their rows and addresses; sets the copies' and stores' width.
-// TMA needs rows and bases of 16 bytes, and a group's decay for both channels of a pair.  raw:
-// whether groups of 2 and 4 take their exps in the compute warps (the backward's have no time for
-// them: 175 us against 147 at L = 8192, D = 4096, d_g = 2).
+// TMA needs rows and bases of 16 bytes, and a group's decay for both channels of a pair.  The
+// compute warps take the exps of groups up to `raw` channels, the helpers those of wider ones.  L =
+// 8192, D = 4096, by compute warps | by helpers, in us: forward, bf16, d_g = 2 54 | 99; backward,
+// bf16, d_g = 2 132 | 163, 4 122 | 118; backward, fp32, d_g = 2 203 | 174, 4 158 | 159.
 int choose_feed(const Shape &s, std::initializer_list<const void *> streams,
-                std::initializer_list<const void *> outs, const void *g, bool raw, sc::Params *p) {
+                std::initializer_list<const void *> outs, const void *g, int raw, sc::Params *p) {
   uintptr_t bits = static_cast<uintptr_t>(s.D * s.es()), out_bits = bits;
   for (const void *t : streams) bits |= reinterpret_cast<uintptr_t>(t);
   if (s.d_g == 1) bits |= reinterpret_cast<uintptr_t>(g);
@@ -355,9 +356,9 @@ int choose_feed(const Shape &s, std::initializer_list<const void *> streams,
   p->copy = bits % 8 == 0 ? 8 : bits % 4 == 0 ? 4 : 0;
   const bool tma = bits % 16 == 0 && p->pair_out && s.D * s.es() * s.L < (int64_t{1} << 40) &&
                    (s.d_g == 1 || s.d_g % 2 == 0);
-  return tma ? (s.d_g == 1                  ? sc::kTmaChannel
-                : raw && s.d_g <= 4 && p->g_feed != sc::kGroupsElement ? sc::kTmaRaw
-                                             : sc::kTmaGroup)
+  return tma ? (s.d_g == 1                                        ? sc::kTmaChannel
+                : s.d_g <= raw && p->g_feed != sc::kGroupsElement ? sc::kTmaRaw
+                                                                  : sc::kTmaGroup)
              : (s.d_g == 1 ? sc::kCopyChannel : sc::kCopyGroup);
 }
 
@@ -458,7 +459,7 @@ int hyena_scan_fwd(const void *q, const void *k, const void *v, const void *g, c
   p.s_out = s_out;
   p.ckpt = ckpt;
   p.y = y;
-  const int feed = choose_feed(s, {q, k, v}, {y}, g, true, &p);
+  const int feed = choose_feed(s, {q, k, v}, {y}, g, 4, &p);
   return with_one_feed(feed, [&](auto f) {
     constexpr int kFeed = decltype(f)::value;
     if (dtype == HYENA_DTYPE_F32)
@@ -508,16 +509,15 @@ int hyena_scan_bwd(const void *q, const void *k, const void *v, const void *g, c
   p.dv = dv;
   p.dg = dg;
   p.ds0 = ds0;
-  const int feed = s.d_g == 1 ? choose_feed(s, {q, k, v, dy}, {dq, dk, dv, dg}, g, false, &p)
-                              : choose_feed(s, {q, k, v, dy}, {dq, dk, dv}, g, false, &p);
+  const int raw = dtype == HYENA_DTYPE_F32 ? 0 : 2;
+  const int feed = s.d_g == 1 ? choose_feed(s, {q, k, v, dy}, {dq, dk, dv, dg}, g, raw, &p)
+                              : choose_feed(s, {q, k, v, dy}, {dq, dk, dv}, g, raw, &p);
   return with_one_feed(feed, [&](auto f) {
     constexpr int kFeed = decltype(f)::value;
-    if constexpr (kFeed == sc::kTmaRaw)
-      return static_cast<int>(HYENA_ERR_UNSUPPORTED);  // not chosen here
-    else
-      return dtype == HYENA_DTYPE_F32
-                 ? backward<sc::F32, kFeed>(s, p, workspace, info.sm_count, stream)
-                 : backward<sc::Bf16, kFeed>(s, p, workspace, info.sm_count, stream);
+    if constexpr (kFeed != sc::kTmaRaw)
+      if (dtype == HYENA_DTYPE_F32)
+        return backward<sc::F32, kFeed>(s, p, workspace, info.sm_count, stream);
+    return backward<sc::Bf16, kFeed>(s, p, workspace, info.sm_count, stream);
   });
 }
 

@@ -51,7 +51,7 @@ constexpr unsigned int kTimeout = 1u; // HYENA_DEVICE_TIMEOUT
 // of 16 bytes by asynchronous 8- or 4-byte copies (single elements where not even those are
 // aligned).  One decay per channel: g is a stream like k and v and the compute warps take its exp.
 // One per group: the helper warps do, except for groups of 2 and 4 channels (kTmaRaw), whose many
-// exps are quicker where they are used (L = 8192, D = 4096, d_g = 2: 99 us by the helpers).
+// exps are quicker where they are used (choose_feed on the host has the measurements).
 enum Feed { kTmaChannel = 0, kTmaGroup = 1, kCopyChannel = 2, kCopyGroup = 3, kTmaRaw = 4 };
 __host__ __device__ constexpr bool by_tma(int feed) {
   return feed == kTmaChannel || feed == kTmaGroup || feed == kTmaRaw;

@@ -35,7 +35,7 @@ def make(B, L, D, d_g, dtype, seed=0, resets=False):
     return q, k, v, lg.to(dtype).cuda(), s0, dy, ds
 
 
-# rows of a tile: 176 (bf16), 144 (bf16 with checkpoints and backward), 112 (fp32)
+# rows of a tile: 176 (bf16), 112 (fp32)
 SHAPES = [
     # B, L, D, d_g
     (1, 1, 8, 1), (2, 1, 64, 64), (1, 2, 32, 8), (3, 7, 40, 1), (1, 175, 64, 16), (1, 176, 64, 1),
