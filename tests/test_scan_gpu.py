@@ -47,6 +47,8 @@ SHAPES = [
     (1, 200, 208, 4), (1, 150, 24, 2), (1, 330, 50, 10),
     # clusters of 2 to 8 CTAs, with and without an empty last round; the time axis cut
     (1, 530, 96, 1), (2, 900, 64, 32), (1, 1250, 320, 64), (3, 1410, 100, 2), (1, 2500, 36, 1),
+    # groups of 2 and 4 (their exps where they are used) shared by clusters and by cuts
+    (1, 900, 64, 2), (2, 1500, 128, 4), (1, 20000, 64, 2), (1, 353, 2048, 2),
     (1, 1600, 512, 16), (1, 9000, 48, 48), (2, 20000, 8, 1), (1, 5000, 32, 1), (1, 4000, 72, 24), (5, 190, 1024, 1), (160, 3, 64, 32),
 ]
 
