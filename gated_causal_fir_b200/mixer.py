@@ -77,6 +77,8 @@ def hyena_mixer_bwd(x, p, saved, dout, ds_out=None):
     """(dx, ds0, grads) for dout (of out) and ds_out (of the last state): grads maps "q", "k", "v",
     "out" and "gate" to (dw, db) and "filters" to its gradient."""
     import gated_causal_fir_b200 as fir
+    if ds_out is not None and p.gate is None:
+        raise ValueError("the FIR keeps no state")
     q, k, v, g, z, ckpt, y, s0 = saved
     grads = {}
     dy, *grads["out"] = hyena_proj_bwd(y, p.out.w, dout)

@@ -172,6 +172,31 @@ def test_captured_training_step():
             assert torch.equal(a, b)
 
 
+def test_two_training_steps_at_once():
+    """Two layers (time axis by clusters and by cuts) on two streams give what they give in turn."""
+    jobs = []
+    for L, E, D, d_g in ((2500, 128, 256, 64), (9000, 64, 64, 32)):
+        p = make("scan", E, D, d_g, BF16)
+        x, dout = (torch.randn(1, L, E, device="cuda").to(BF16) for _ in range(2))
+
+        def step(p=p, x=x, dout=dout):
+            out, state, saved = g.hyena_mixer_fwd(x, p, save=True)
+            dx, ds0, grads = g.hyena_mixer_bwd(x, p, saved, dout)
+            return [out, state, dx, ds0] + [t for n in sorted(grads) for t in grads[n]]
+        jobs.append((step, step(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    results = [[], []]
+    for _ in range(4):
+        for i, (step, _, stream) in enumerate(jobs):
+            with torch.cuda.stream(stream):
+                results[i].append(step())
+    torch.cuda.synchronize()
+    for (_, alone, _), runs in zip(jobs, results):
+        for run in runs:
+            for a, b in zip(alone, run):
+                assert torch.equal(a, b)
+
+
 def test_refusals():
     p = make("fir", 64, 64, 16, BF16)
     x = torch.randn(1, 10, 64, device="cuda").to(BF16)
@@ -179,5 +204,8 @@ def test_refusals():
         g.hyena_mixer_step(x[:, 0], p, torch.zeros(1, 64, device="cuda"))
     with pytest.raises(ValueError):
         g.hyena_mixer_fwd(x, p, s0=torch.zeros(1, 64, device="cuda"))
+    saved = g.hyena_mixer_fwd(x, p, save=True)[2]
+    with pytest.raises(ValueError):
+        g.hyena_mixer_bwd(x, p, saved, x, ds_out=torch.zeros(1, 64, device="cuda"))
     with pytest.raises(ValueError):
         g.MixerParams(p.q, p.k, p.v, p.out, 16)
