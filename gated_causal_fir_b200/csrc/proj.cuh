@@ -115,8 +115,9 @@ __device__ __forceinline__ float erfc_of(float z, float e) {
 template <typename T>
 __device__ __forceinline__ float gelu_of(float z) {
   if constexpr (sizeof(T) == 4) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
-  const float half = 0.5f * z * erfc_of(z, __expf(-0.5f * z * z));  // z (1 - Phi(|z|))
-  return z > 0.0f ? z - half : half;
+  // z times Phi, which is 1 at +inf (z less a part of z would be inf - inf times 0 there)
+  const float tail = 0.5f * erfc_of(z, __expf(-0.5f * z * z));  // 1 - Phi(|z|)
+  return z * (z > 0.0f ? 1.0f - tail : tail);
 }
 template <typename T>
 __device__ __forceinline__ float gelu_slope(float z) {

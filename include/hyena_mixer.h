@@ -86,7 +86,8 @@ int hyena_scan_step(const void *q, const void *k, const void *v, const void *g, 
 
 enum hyena_act {
     HYENA_ACT_NONE = 0,
-    HYENA_ACT_GELU = 1,          /* z Phi(z), the exact form (erf) */
+    HYENA_ACT_GELU = 1,          /* z Phi(z), the exact form (erf); inf at inf; NaN, as silu, at -inf
+                                    (inf times 0) */
     HYENA_ACT_SILU = 2,          /* z sigmoid(z) */
     HYENA_ACT_SIGMOID = 3,
     HYENA_ACT_LOGSIGMOID = 4     /* log sigmoid(z): a log decay for hyena_scan_* */
