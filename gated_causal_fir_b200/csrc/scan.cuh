@@ -404,14 +404,16 @@ __device__ __forceinline__ void arrive_after_copies(uint64_t *bar) {
                : "memory");
 }
 
-// Which arrivals a helper thread of a copying feed makes on a tile's barrier.
+// Which arrivals a helper thread of a copying feed makes on a tile's barrier: one when its copies
+// have landed, one (a release) for what it stored itself.  Groups' rows that TMA could take are
+// stored by elements here too, as groups_tile does with all that it does not copy.
 template <int kFeed>
 __device__ __forceinline__ bool copy_arrivals(const Params &p) {
   return p.copy || (!per_channel(kFeed) && p.g_feed == kGroupsCopy);
 }
 template <int kFeed>
 __device__ __forceinline__ bool store_arrivals(const Params &p) {
-  return !p.copy || (!per_channel(kFeed) && p.g_feed == kGroupsElement);
+  return !p.copy || (!per_channel(kFeed) && p.g_feed != kGroupsCopy);
 }
 
 // The helper warps: NS streams of every tile of the CTA's units into the ring, in the order the

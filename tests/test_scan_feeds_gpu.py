@@ -1,0 +1,55 @@
+"""The recurrence where its streams and its groups' rows reach shared memory in different ways, and
+where it is called again and again (needs a B200).  Bounds: _scan_ref."""
+import pytest
+import torch
+
+import gated_causal_fir_b200 as g
+from tests import _scan_ref as R
+from tests.test_scan_gpu import make
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+    from gated_causal_fir_b200 import build
+    build.build()
+    g.hyena_device_status(clear=True)
+    yield
+    assert g.hyena_device_status(clear=True) == 0, "a kernel raised its device status word"
+
+
+def moved(t, elements):
+    """The values of t in a contiguous view that starts `elements` into its storage."""
+    base = torch.empty(t.numel() + elements, dtype=t.dtype, device=t.device)
+    base[elements:] = t.flatten()
+    return base[elements:].view(t.shape)
+
+
+@pytest.mark.parametrize("dtype", (BF16, F32), ids=("bf16", "f32"))
+@pytest.mark.parametrize("B,L,D,d_g,shift", (
+    (1, 700, 24, 3, 0), (2, 900, 72, 9, 0), (1, 2500, 40, 5, 0), (1, 20000, 56, 7, 0),
+    (2, 400, 200, 25, 0),        # odd groups: TMA cannot give a pair of channels one decay
+    (1, 700, 128, 16, 4), (1, 900, 128, 16, 2), (2, 500, 2048, 64, 4)))  # streams off 16 bytes
+def test_copied_streams_with_groups_rows_that_tma_could_take(B, L, D, d_g, shift, dtype):
+    """q, k, v, dy arrive by asynchronous copies while the groups' rows (whole 16-byte vectors, in
+    aligned memory) are stored by the helper threads: both are in the tile when it is read."""
+    q, k, v, lg, s0, dy, ds = make(B, L, D, d_g, dtype, seed=3)
+    ref = R.Ref(q, k, v, lg, d_g, s0, dy, ds)
+    if shift:
+        q, k, v, dy = (moved(t, shift) for t in (q, k, v, dy))
+    first = None
+    for _ in range(8):
+        ckpt = g.hyena_scan_ckpt(q)
+        y, s_out = g.hyena_scan_fwd(q, k, v, lg, d_g, s0=s0, ckpt=ckpt)
+        got = [y, s_out] + list(g.hyena_scan_bwd(q, k, v, lg, dy, d_g, s0=s0, ds_out=ds, ckpt=ckpt))
+        if first is None:
+            first = got
+            for name, t in zip(("y", "s_out", "dq", "dk", "dv", "dg", "ds0"), got):
+                R.check(name, t, ref)
+        for a, b in zip(got, first):
+            assert torch.equal(a, b)
