@@ -653,6 +653,20 @@ __device__ __forceinline__ void put_cut(float2 *agg, int c, int D, F2 a, F2 v) {
   if (c + 1 < D) agg[c + 1] = make_float2(A.y, S.y);
 }
 
+// Reads every loaded word in an instruction that cannot be left out, so that the warp waits until
+// the loads have returned: what is only used after its stage has been handed back could otherwise
+// still be in flight when the next tile's copy lands there.  (B=1 L=8192 D=4096 bf16 d_g=64: 47.1 us
+// without, 47.7 with it.)
+template <typename Raw, int R>
+__device__ __forceinline__ void consume(const Raw (&v)[R]) {
+  Raw any = v[0];
+#pragma unroll
+  for (int r = 1; r < R; ++r) any |= v[r];
+  const uint32_t word = static_cast<uint32_t>(any) | static_cast<uint32_t>(static_cast<uint64_t>(any) >> 32);
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %0, 0xfffffffe;\n\t@p nanosleep.u32 0;\n\t}" ::"r"(
+      word));
+}
+
 constexpr F2 kOnes = 0x3f8000003f800000ull;
 constexpr int kWarps = kComputeThreads / 32;
 
@@ -758,6 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the halves of the warp, joined by the first; the second keeps the first's
       const F2 Ao = from_other_half(A), So = from_other_half(S);
       if (!second) joint[buffer][warp][l] = make_ulonglong2(mul2(Ao, A), fma2(Ao, S, So));
+      if (kOut) consume(qr);  // (k, v and the decays went into A and S)
       __syncwarp();
       if (lane == 0) mbar_arrive(&ring.empty[st]);  // the segment is in registers
       compute_barrier();
@@ -972,7 +987,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         joint_w[buffer][warp][l] = fma2(A, Wo, W);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ring.empty[st]);
+      if (lane == 0) mbar_arrive(&ring.empty[st]);  // every word went into A, S or W
       compute_barrier();
       F2 w = w_in, state = s;
 #pragma unroll

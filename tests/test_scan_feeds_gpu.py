@@ -53,3 +53,20 @@ def test_copied_streams_with_groups_rows_that_tma_could_take(B, L, D, d_g, shift
                 R.check(name, t, ref)
         for a, b in zip(got, first):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", (BF16, F32), ids=("bf16", "f32"))
+@pytest.mark.parametrize("L,D,d_g", ((4000, 4096, 64), (4000, 4096, 1), (3000, 1032, 3),
+                                     (20000, 256, 16)))
+def test_tiles_are_read_before_the_next_ones_land(L, D, d_g, dtype):
+    """Rings that turn over many times, called again and again over changing neighbours: the same
+    bits in every call."""
+    q, k, v, lg, s0, dy, ds = make(1, L, D, d_g, dtype, seed=11)
+    ckpt = g.hyena_scan_ckpt(q)
+    want = None
+    for _ in range(30):
+        y, s_out = g.hyena_scan_fwd(q, k, v, lg, d_g, s0=s0, ckpt=ckpt)
+        got = [y, s_out, *g.hyena_scan_bwd(q, k, v, lg, dy, d_g, s0=s0, ds_out=ds, ckpt=ckpt)]
+        if want is None:
+            want = got
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
