@@ -102,6 +102,8 @@ MIXER_SIGNATURES = {
 TESTING_SIGNATURES = {
     "hyena_testing_fwd_fault": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _i32,
                                        _i32, ctypes.c_uint64, _vp]),
+    "hyena_testing_proj_fault": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32,
+                                        ctypes.c_uint64, _vp]),
 }
 
 _LIB = None

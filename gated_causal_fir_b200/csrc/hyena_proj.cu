@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "host_util.h"
+#include "hyena_conv_testing.h"
 #include "hyena_mixer.h"
 #include "proj.cuh"
 
@@ -247,6 +248,7 @@ int product(const Operand &a, const Operand &b, int64_t K, pj::Params p, int dty
   p.splits = pl.splits;
   p.kb_per_split = pl.per;
   p.group_m = pl.shape == kPair256 ? 8 : 16;
+  if (p.wait_ns == 0) p.wait_ns = hyena::kWaitTimeoutNs;
   p.partial = partial;
   const int64_t per16 = 16 / elem(dtype);
   p.vec = p.N % per16 == 0 && aligned(p.y, 16) && aligned(p.z, 16) && aligned(p.residual, 16);
@@ -442,32 +444,10 @@ bool misaligned16(std::initializer_list<const void *> ptrs) {
   return false;
 }
 
-}  // namespace
-
-extern "C" {
-
-int64_t hyena_proj_workspace_bytes(int64_t M, int64_t N, int64_t K, int dtype) {
-  if (check_shape(M, N, K, dtype) != HYENA_OK) return -HYENA_ERR_INVALID_ARG;
-  if (M == 0) return 0;
-  int64_t n = partial_bytes(M, N, K, dtype);
-  if (needs_pack(K, dtype)) n += pack_bytes(M, K, dtype) + pack_bytes(N, K, dtype);
-  return n;
-}
-
-int64_t hyena_proj_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int act, int dtype) {
-  if (check_shape(M, N, K, dtype) != HYENA_OK || act < HYENA_ACT_NONE || act > HYENA_ACT_LOGSIGMOID)
-    return -HYENA_ERR_INVALID_ARG;
-  if (M == 0) return 0;
-  int64_t n = round_up(db_blocks(M) * N * 4, 256);
-  if (needs_dz(N, act, dtype)) n += pack_bytes(M, N, dtype);
-  if (needs_pack(K, dtype)) n += pack_bytes(M, K, dtype) + pack_bytes(N, K, dtype);
-  // the two products run one after the other and share the room for partial sums
-  return n + std::max(partial_bytes(M, K, N, dtype), partial_bytes(N, K, M, dtype));
-}
-
-int hyena_proj_fwd(const void *x, const void *w, const float *bias, const void *residual, void *y,
-                   void *z, int64_t M, int64_t N, int64_t K, int act, int dtype, void *workspace,
-                   size_t workspace_bytes, cudaStream_t stream) {
+// hyena_proj_fwd with the test settings of hyena_testing_proj_fault (0, 0 in the product path).
+int proj_fwd(const void *x, const void *w, const float *bias, const void *residual, void *y,
+             void *z, int64_t M, int64_t N, int64_t K, int act, int dtype, void *workspace,
+             size_t workspace_bytes, int fault, uint64_t wait_ns, cudaStream_t stream) {
   const int rc = check_shape(M, N, K, dtype);
   if (rc != HYENA_OK) return rc;
   if (act < HYENA_ACT_NONE || act > HYENA_ACT_LOGSIGMOID) return HYENA_ERR_INVALID_ARG;
@@ -494,9 +474,52 @@ int hyena_proj_fwd(const void *x, const void *w, const float *bias, const void *
   p.z = z;
   p.act = act;
   p.status = d.info.status;
+  p.fault = fault;
+  p.wait_ns = wait_ns;
   uint8_t *at = static_cast<uint8_t *>(workspace);
   return dtype == HYENA_DTYPE_F32 ? forward<float>(x, w, p, K, dtype, at, d, stream)
                                   : forward<__nv_bfloat16>(x, w, p, K, dtype, at, d, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t hyena_proj_workspace_bytes(int64_t M, int64_t N, int64_t K, int dtype) {
+  if (check_shape(M, N, K, dtype) != HYENA_OK) return -HYENA_ERR_INVALID_ARG;
+  if (M == 0) return 0;
+  int64_t n = partial_bytes(M, N, K, dtype);
+  if (needs_pack(K, dtype)) n += pack_bytes(M, K, dtype) + pack_bytes(N, K, dtype);
+  return n;
+}
+
+int64_t hyena_proj_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int act, int dtype) {
+  if (check_shape(M, N, K, dtype) != HYENA_OK || act < HYENA_ACT_NONE || act > HYENA_ACT_LOGSIGMOID)
+    return -HYENA_ERR_INVALID_ARG;
+  if (M == 0) return 0;
+  int64_t n = round_up(db_blocks(M) * N * 4, 256);
+  if (needs_dz(N, act, dtype)) n += pack_bytes(M, N, dtype);
+  if (needs_pack(K, dtype)) n += pack_bytes(M, K, dtype) + pack_bytes(N, K, dtype);
+  // the two products run one after the other and share the room for partial sums
+  return n + std::max(partial_bytes(M, K, N, dtype), partial_bytes(N, K, M, dtype));
+}
+
+int hyena_proj_fwd(const void *x, const void *w, const float *bias, const void *residual, void *y,
+                   void *z, int64_t M, int64_t N, int64_t K, int act, int dtype, void *workspace,
+                   size_t workspace_bytes, cudaStream_t stream) {
+  return proj_fwd(x, w, bias, residual, y, z, M, N, K, act, dtype, workspace, workspace_bytes,
+                  pj::kNoFault, 0, stream);
+}
+
+int hyena_testing_proj_fault(const void *x, const void *w, const void *residual, void *y,
+                             int64_t M, int64_t N, int64_t K, int fault, uint64_t wait_ns,
+                             cudaStream_t stream) {
+  if (fault < pj::kNoFault || fault > pj::kNoResidual || wait_ns < 1000000ull ||
+      wait_ns > hyena::kWaitTimeoutNs)
+    return HYENA_ERR_INVALID_ARG;
+  if (N % 8 != 0 || K % 8 != 0 || K > 4 * pj::kBK) return HYENA_ERR_UNSUPPORTED;
+  return proj_fwd(x, w, nullptr, residual, y, nullptr, M, N, K, HYENA_ACT_NONE, HYENA_DTYPE_BF16,
+                  nullptr, 0, fault, wait_ns, stream);
 }
 
 int hyena_proj_bwd(const void *x, const void *w, const void *z, const void *dy,

@@ -87,7 +87,10 @@ struct Params {
   int bias_vec;                 // bias is 16-byte aligned
   int vec;                      // rows of y, z, residual are whole, aligned 16-byte vectors
   unsigned int *status;
+  uint64_t wait_ns;             // limit of the waits between roles
+  int fault;                    // test hook (enum Fault)
 };
+enum Fault { kNoFault = 0, kNoResidual = 1 };  // 1: residuals are never requested
 
 // ------------------------------------------------------------------------------- activations
 // fp32 results take the accurate exp and division; a bf16 result rounds away what the fast ones
@@ -431,7 +434,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // A wait of the whole warp, with one answer for all of it.
   const auto wait = [&](uint64_t *bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, &abort, p.status, kTimeout)) != 0;
+    return __all_sync(0xffffffffu,
+                      mbar_wait(bar, parity, &abort, p.status, kTimeout, p.wait_ns)) != 0;
   };
   // The TMA and MMA warps run their loops as a whole and only the instruction itself in one lane:
   // descriptors and coordinates then stay in uniform registers.  With the loops inside one lane,
@@ -575,12 +579,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *bufs = reinterpret_cast<uint8_t *>(out);
     uint64_t *res_bar = &res_full[warp - 2];
     [[maybe_unused]] uint64_t once = 0;  // L2 policy of what is read or written once
-    [[maybe_unused]] uint32_t writes = 0, res_seen = 0;
+    [[maybe_unused]] uint32_t writes = 0, res_asked = 0, res_seen = 0;  // res_*: residual chunks
     if constexpr (!kPromote)
       asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
     // Requests the residual of the chunk at column c0 of work k into the buffer of write `at`; the
     // stores so far have read their buffers.
     const auto request = [&](const Work &k, int c0, uint32_t at) {
+      if (p.fault == kNoResidual) return;
+      ++res_asked;
       if (lane == 0) {
         mbar_arrive_expect_tx(res_bar, 2048);
         asm volatile(
@@ -684,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (!kPromote) {
         if (p.tma && k.part < 0) {
 #pragma unroll 1
-          for (int c0 = 0; c0 < kBN / 2 && ok; c0 += kChunk) {
+          for (int c0 = 0; c0 < kBN / 2; c0 += kChunk) {
             const bool last = c0 + kChunk >= kBN / 2;
             const int col = k.n * L::kN + col0 + c0;
             float v[32];
@@ -720,7 +726,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int e = 0; e < 32; ++e) v[e] = act_of<T, decltype(act)::value>(v[e]);
             });
             if (p.residual) {
-              ok = wait(res_bar, res_seen++ & 1);
+              ok = wait(res_bar, res_seen & 1);
+              if (!ok) break;  // no further request on this barrier: its phase is still open
+              ++res_seen;
               const uint8_t *buf = bufs + (writes & 1) * 2048;
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
@@ -745,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (lane == 0) bulk_wait_group_read<1>();
               __syncwarp();
             }
-            if (ok) store(&my, v, row0, col);
+            store(&my, v, row0, col);
           }
           ++n;
           continue;
@@ -878,7 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bulk_wait_group<0>();
         // a residual requested for a chunk that a failed wait kept from being read
         int no_abort = 0;
-        if (!ok && ahead) mbar_wait(res_bar, res_seen & 1, &no_abort, p.status, kTimeout);
+        if (res_asked != res_seen) mbar_wait(res_bar, res_seen & 1, &no_abort, p.status, kTimeout);
       }
       __syncwarp();
     }

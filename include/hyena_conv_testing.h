@@ -1,7 +1,7 @@
 /*
- * hyena_conv_testing.h -- test-only entry point of libhyena_conv.so.  Not part of the
- * operation's interface (hyena_conv.h); the pages have no counterpart.  It exists so that a
- * test can make the tensor-core forward's failure detection fire without faulting the GPU.
+ * hyena_conv_testing.h -- test-only entry points of libhyena_conv.so.  Not part of the
+ * operations' interface (hyena_conv.h, hyena_mixer.h); the pages have no counterpart.  They exist
+ * so that a test can make the kernels' failure detection fire without faulting the GPU.
  */
 #ifndef HYENA_CONV_TESTING_H
 #define HYENA_CONV_TESTING_H
@@ -30,6 +30,17 @@ extern "C" {
 int hyena_testing_fwd_fault(const void *q, const void *k, const void *v, const float *h, void *y,
                             int64_t B, int64_t L, int64_t D, int d_g, int l_h, int fault,
                             uint64_t wait_ns, cudaStream_t stream);
+
+/*
+ * hyena_proj_fwd (include/hyena_mixer.h) of bf16 with a residual and no bias or activation, under
+ * the same two settings.  fault == 1: no residual is ever requested, so the epilogue's wait for it
+ * runs out; every role leaves, copies and MMAs in flight are waited for, tensor memory is freed,
+ * HYENA_DEVICE_TIMEOUT is raised and y stays incomplete.  K up to 256, so that no workspace is
+ * needed; N and K multiples of 8.
+ */
+int hyena_testing_proj_fault(const void *x, const void *w, const void *residual, void *y,
+                             int64_t M, int64_t N, int64_t K, int fault, uint64_t wait_ns,
+                             cudaStream_t stream);
 
 #ifdef __cplusplus
 }
