@@ -90,7 +90,8 @@ struct Params {
   uint64_t wait_ns;             // limit of the waits between roles
   int fault;                    // test hook (enum Fault)
 };
-enum Fault { kNoFault = 0, kNoResidual = 1 };  // 1: residuals are never requested
+// 1: residuals are never requested; 2: the first accumulator is never announced
+enum Fault { kNoFault = 0, kNoResidual = 1, kNoAccumulator = 2 };
 
 // ------------------------------------------------------------------------------- activations
 // fp32 results take the accurate exp and division; a bf16 result rounds away what the fast ones
@@ -544,16 +545,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               b_lo = static_cast<uint32_t>(db0);
             }
           }
-          if (ok && lead) commit<kCG>(&acc_full[acc]);
+          if (ok && lead && !(p.fault == kNoAccumulator && n == 0)) commit<kCG>(&acc_full[acc]);
           __syncwarp();
         }
       }
-      // MMAs still reading shared memory when a wait gave up: let them finish
-      if (!ok || abort) {
-        int no_abort = 0;
-        for (int j = it > kRing ? it - kRing : 0; j < it; ++j)
-          mbar_wait(&empty[j % kRing], (j / kRing) & 1, &no_abort, p.status, kTimeout);
-      }
+      // The MMAs issued are done before the CTA ends, also where another warp gives up after this
+      // one has issued its last.
+      int no_abort = 0;
+      for (int j = it > kRing ? it - kRing : 0; j < it; ++j)
+        mbar_wait(&empty[j % kRing], (j / kRing) & 1, &no_abort, p.status, kTimeout);
     }
   } else {
     // --------------------------------------------------------------------------- epilogue

@@ -55,7 +55,7 @@ def test_short_limit_without_fault_runs_normally(shape):
     assert torch.equal(y, want) and g.hyena_device_status(clear=True) == 0
 
 
-FAULTS = {"residual never requested": 1}
+FAULTS = {"residual never requested": 1, "accumulator never announced": 2}
 
 
 @pytest.mark.parametrize("fault", FAULTS.values(), ids=FAULTS)
