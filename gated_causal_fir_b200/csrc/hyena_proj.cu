@@ -514,10 +514,11 @@ int hyena_proj_fwd(const void *x, const void *w, const float *bias, const void *
 int hyena_testing_proj_fault(const void *x, const void *w, const void *residual, void *y,
                              int64_t M, int64_t N, int64_t K, int fault, uint64_t wait_ns,
                              cudaStream_t stream) {
-  if (fault < pj::kNoFault || fault > pj::kNoAccumulator || wait_ns < 1000000ull ||
+  if (fault < pj::kNoFault || fault > pj::kStagesEnd || wait_ns < 1000000ull ||
       wait_ns > hyena::kWaitTimeoutNs)
     return HYENA_ERR_INVALID_ARG;
-  if (N % 8 != 0 || K % 8 != 0 || K > 4 * pj::kBK) return HYENA_ERR_UNSUPPORTED;
+  if (N % 8 != 0 || hyena_proj_workspace_bytes(M, N, K, HYENA_DTYPE_BF16) > 0)
+    return HYENA_ERR_UNSUPPORTED;
   return proj_fwd(x, w, nullptr, residual, y, nullptr, M, N, K, HYENA_ACT_NONE, HYENA_DTYPE_BF16,
                   nullptr, 0, fault, wait_ns, stream);
 }

@@ -87,11 +87,12 @@ struct Params {
   int bias_vec;                 // bias is 16-byte aligned
   int vec;                      // rows of y, z, residual are whole, aligned 16-byte vectors
   unsigned int *status;
-  uint64_t wait_ns;             // limit of the waits between roles
+  uint64_t wait_ns;             // limit of the waits between roles (bf16; 2 s but in tests)
   int fault;                    // test hook (enum Fault)
 };
-// 1: residuals are never requested; 2: the first accumulator is never announced
-enum Fault { kNoFault = 0, kNoResidual = 1, kNoAccumulator = 2 };
+// 1: residuals are never requested; 2: the first accumulator is never announced; 3: the TMA warp of
+// a pair's leader gives up after one stage
+enum Fault { kNoFault = 0, kNoResidual = 1, kNoAccumulator = 2, kStagesEnd = 3 };
 
 // ------------------------------------------------------------------------------- activations
 // fp32 results take the accurate exp and division; a bf16 result rounds away what the fast ones
@@ -270,6 +271,9 @@ __device__ __forceinline__ uint32_t in_cta(const void *p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
+__device__ __forceinline__ void put_in_cta(int *p, uint32_t rank, int v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(in_cta(p, rank)), "r"(v) : "memory");
+}
 __device__ __forceinline__ void arrive_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
@@ -402,6 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t res_full[kEpiWarps];
   __shared__ uint32_t tmem_at;
   __shared__ int abort;
+  __shared__ int issued, peer_abort, peer_issued;  // (pairs) stages that a CTA's copies were issued for
   uint8_t *stages = dynamic + (1024 - smem_u32(dynamic) % 1024) % 1024;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const uint32_t rank = kCG == 2 ? cluster_rank() : 0;
@@ -416,6 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kEpiWarps; ++i) mbar_init(&res_full[i], 1);
     abort = 0;
+    peer_abort = peer_issued = 0;
     fence_mbar_init();
   }
   if (warp == 1) tmem_get<kCG>(&tmem_at, L::kTmemCols);
@@ -436,7 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // A wait of the whole warp, with one answer for all of it.
   const auto wait = [&](uint64_t *bar, uint32_t parity) {
     return __all_sync(0xffffffffu,
-                      mbar_wait(bar, parity, &abort, p.status, kTimeout, p.wait_ns)) != 0;
+                      mbar_wait(bar, parity, &abort, p.status, kTimeout,
+                                kPromote ? kWaitTimeoutNs : p.wait_ns)) != 0;
   };
   // The TMA and MMA warps run their loops as a whole and only the instruction itself in one lane:
   // descriptors and coordinates then stay in uniform registers.  With the loops inside one lane,
@@ -454,6 +461,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n0 = k.n * L::kN + static_cast<int>(rank) * L::kBRows;
       for (int i = k.kb0 * kPlanes; i < k.kb1 * kPlanes; ++i, ++it) {
         if (it >= kRing && !wait(&empty[st], freed)) {
+          ok = false;
+          break;
+        }
+        if (kCG == 2 && p.fault == kStagesEnd && rank == 0 && it == 1) {
+          abort = 1;
+          if (lead) atomicOr(p.status, kTimeout);
           ok = false;
           break;
         }
@@ -491,6 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait(&empty[s], parity) && rank == 0)
         mbar_wait(&full[s], parity, &no_abort, p.status, kTimeout);
     }
+    if (lane == 0) issued = it;
   } else if (warp == 1) {
     if (rank == 0) {
       // ------------------------------------------------------------------------- MMA
@@ -545,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               b_lo = static_cast<uint32_t>(db0);
             }
           }
-          if (ok && lead && !(p.fault == kNoAccumulator && n == 0)) commit<kCG>(&acc_full[acc]);
+          if (ok && lead && (kPromote || p.fault != kNoAccumulator || n > 0)) commit<kCG>(&acc_full[acc]);
           __syncwarp();
         }
       }
@@ -894,7 +908,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Both CTAs' MMAs read each other's shared memory and signal each other's barriers.
   tc_fence_before_sync();
   __syncthreads();
-  if (kCG == 2) cluster_sync();
+  if constexpr (kCG == 2) {
+    if (threadIdx.x == 0 && abort) {
+      put_in_cta(&peer_issued, rank ^ 1, issued);
+      put_in_cta(&peer_abort, rank ^ 1, 1);
+    }
+    cluster_sync();
+    if (abort || peer_abort) {  // in both CTAs
+      // The other CTA's copies for stages that the leader gave up before: their bytes count on the
+      // leader's barriers, which it arms for them alone.
+      if (rank == 0 && warp == 0) {
+        int no_abort = 0;
+        for (int j = issued; j < peer_issued; ++j) {
+          if (lane == 0) mbar_arrive_expect_tx(&full[j % kRing], L::kStage);
+          __syncwarp();
+          mbar_wait(&full[j % kRing], (j / kRing) & 1, &no_abort, p.status, kTimeout);
+        }
+      }
+      __syncwarp();
+      cluster_sync();
+    }
+  }
   if constexpr (kJoin) {
     cluster_sync();  // every cut's partial product is there
     if (warp >= 2 && !abort) {

@@ -34,10 +34,11 @@ int hyena_testing_fwd_fault(const void *q, const void *k, const void *v, const f
 /*
  * hyena_proj_fwd (include/hyena_mixer.h) of bf16 with a residual and no bias or activation, under
  * the same two settings.  fault == 1: no residual is ever requested, so the epilogue's wait for it
- * runs out; fault == 2: the first accumulator of each CTA (or pair) is never announced.  Every
- * role leaves, copies and MMAs in flight are waited for, tensor memory is freed,
- * HYENA_DEVICE_TIMEOUT is raised and y stays incomplete.  K up to 256, so that no workspace is
- * needed; N and K multiples of 8.
+ * runs out; fault == 2: the first accumulator of each CTA (or pair) is never announced; fault ==
+ * 3: the TMA warp of a pair's leader gives up after one stage (pairs of CTAs only).  Every role
+ * leaves, copies and MMAs in flight are waited for, tensor memory is freed, HYENA_DEVICE_TIMEOUT
+ * is raised and y stays incomplete.  N a multiple of 8 and sizes that need no workspace, else
+ * HYENA_ERR_UNSUPPORTED.
  */
 int hyena_testing_proj_fault(const void *x, const void *w, const void *residual, void *y,
                              int64_t M, int64_t N, int64_t K, int fault, uint64_t wait_ns,

@@ -9,7 +9,7 @@ ARGS = dict(x=1 << 24, w=2 << 24, residual=3 << 24, y=4 << 24, M=64, N=128, K=72
 
 @pytest.mark.parametrize("kw,code", [
     (dict(fault=-1), 1), (dict(fault=9), 1), (dict(wait_ns=1000), 1), (dict(wait_ns=3 * 10**9), 1),
-    (dict(N=100), 2), (dict(K=60), 2), (dict(K=512), 2), (dict(x=None), 1), (dict(y=1 << 24), 1),
+    (dict(N=100), 2), (dict(K=60), 2), (dict(M=4096, N=4096, K=8192, y=1 << 40), 2), (dict(x=None), 1), (dict(y=1 << 24), 1),
     (dict(x=(1 << 24) + 2), 3), (dict(M=0), 0)])
 def test_refusals(kw, code):
     build.build()
