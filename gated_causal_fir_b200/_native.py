@@ -104,6 +104,8 @@ TESTING_SIGNATURES = {
                                        _i32, ctypes.c_uint64, _vp]),
     "hyena_testing_proj_fault": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32,
                                         ctypes.c_uint64, _vp]),
+    "hyena_testing_scan_fault": (_i32, [_vp] * 6 + [_i64] * 3 + [_i32] * 3 +
+                                 [ctypes.c_uint64, _vp]),
 }
 
 _LIB = None

@@ -6,6 +6,7 @@
 #include <mutex>
 
 #include "host_util.h"
+#include "hyena_conv_testing.h"
 #include "hyena_mixer.h"
 #include "scan.cuh"
 
@@ -203,6 +204,7 @@ sc::Params base_params(const Shape &s, const void *g, const hyena::host::DeviceI
   sc::Params p{};
   const Cuts c = cuts_of(s);
   p.status = info.status;
+  p.wait_ns = hyena::kWaitTimeoutNs;
   p.B = static_cast<int>(s.B);
   p.L = static_cast<int>(s.L);
   p.D = static_cast<int>(s.D);
@@ -401,33 +403,11 @@ bool misaligned(uintptr_t a, std::initializer_list<const void *> ptrs) {
   return false;
 }
 
-}  // namespace
-
-extern "C" {
-
-int64_t hyena_scan_ckpt_tiles(int64_t L, int dtype) {
-  const Shape s{1, L, 1, 1, dtype};
-  if (check_shape(s) != HYENA_OK) return -HYENA_ERR_INVALID_ARG;
-  return s.n_tiles();
-}
-
-int64_t hyena_scan_workspace_bytes(int64_t B, int64_t L, int64_t D, int d_g, int dtype) {
-  const Shape s{B, L, D, d_g, dtype};
-  if (check_shape(s) != HYENA_OK) return -HYENA_ERR_INVALID_ARG;
-  return B == 0 || L == 0 ? 0 : agg_bytes(s);
-}
-
-int64_t hyena_scan_bwd_workspace_bytes(int64_t B, int64_t L, int64_t D, int d_g, int dtype,
-                                       int have_ckpt) {
-  const Shape s{B, L, D, d_g, dtype};
-  if (check_shape(s) != HYENA_OK) return -HYENA_ERR_INVALID_ARG;
-  if (B == 0 || L == 0) return 0;
-  return agg_bytes(s) + dg_bytes(s) + (have_ckpt ? 0 : ckpt_bytes(s));
-}
-
-int hyena_scan_fwd(const void *q, const void *k, const void *v, const void *g, const float *s0,
-                   void *y, float *s_out, float *ckpt, int64_t B, int64_t L, int64_t D, int d_g,
-                   int dtype, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+// hyena_scan_fwd with the test settings of hyena_testing_scan_fault (0, 0 in the product path).
+int scan_fwd(const void *q, const void *k, const void *v, const void *g, const float *s0, void *y,
+             float *s_out, float *ckpt, int64_t B, int64_t L, int64_t D, int d_g, int dtype,
+             void *workspace, size_t workspace_bytes, int fault, uint64_t wait_ns,
+             cudaStream_t stream) {
   const Shape s{B, L, D, d_g, dtype};
   int rc = check_shape(s);
   if (rc != HYENA_OK) return rc;
@@ -459,6 +439,8 @@ int hyena_scan_fwd(const void *q, const void *k, const void *v, const void *g, c
   p.s_out = s_out;
   p.ckpt = ckpt;
   p.y = y;
+  p.fault = fault;
+  if (wait_ns > 0) p.wait_ns = wait_ns;
   const int feed = choose_feed(s, {q, k, v}, {y}, g, 4, &p);
   return with_one_feed(feed, [&](auto f) {
     constexpr int kFeed = decltype(f)::value;
@@ -466,6 +448,50 @@ int hyena_scan_fwd(const void *q, const void *k, const void *v, const void *g, c
       return forward<sc::F32, kFeed>(s, p, workspace, info.sm_count, stream);
     return forward<sc::Bf16, kFeed>(s, p, workspace, info.sm_count, stream);
   });
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t hyena_scan_ckpt_tiles(int64_t L, int dtype) {
+  const Shape s{1, L, 1, 1, dtype};
+  if (check_shape(s) != HYENA_OK) return -HYENA_ERR_INVALID_ARG;
+  return s.n_tiles();
+}
+
+int64_t hyena_scan_workspace_bytes(int64_t B, int64_t L, int64_t D, int d_g, int dtype) {
+  const Shape s{B, L, D, d_g, dtype};
+  if (check_shape(s) != HYENA_OK) return -HYENA_ERR_INVALID_ARG;
+  return B == 0 || L == 0 ? 0 : agg_bytes(s);
+}
+
+int64_t hyena_scan_bwd_workspace_bytes(int64_t B, int64_t L, int64_t D, int d_g, int dtype,
+                                       int have_ckpt) {
+  const Shape s{B, L, D, d_g, dtype};
+  if (check_shape(s) != HYENA_OK) return -HYENA_ERR_INVALID_ARG;
+  if (B == 0 || L == 0) return 0;
+  return agg_bytes(s) + dg_bytes(s) + (have_ckpt ? 0 : ckpt_bytes(s));
+}
+
+int hyena_scan_fwd(const void *q, const void *k, const void *v, const void *g, const float *s0,
+                   void *y, float *s_out, float *ckpt, int64_t B, int64_t L, int64_t D, int d_g,
+                   int dtype, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return scan_fwd(q, k, v, g, s0, y, s_out, ckpt, B, L, D, d_g, dtype, workspace, workspace_bytes,
+                  0, 0, stream);
+}
+
+int hyena_testing_scan_fault(const void *q, const void *k, const void *v, const void *g, void *y,
+                             float *s_out, int64_t B, int64_t L, int64_t D, int d_g, int dtype,
+                             int fault, uint64_t wait_ns, cudaStream_t stream) {
+  if (fault < 0 || fault > 1 || wait_ns < 1000000ull || wait_ns > hyena::kWaitTimeoutNs)
+    return HYENA_ERR_INVALID_ARG;
+  const Shape s{B, L, D, d_g, dtype};
+  const int rc = check_shape(s);
+  if (rc != HYENA_OK) return rc;
+  if (B > 0 && L > 0 && cuts_of(s).cluster < 2) return HYENA_ERR_UNSUPPORTED;
+  return scan_fwd(q, k, v, g, nullptr, y, s_out, nullptr, B, L, D, d_g, dtype, nullptr, 0, fault,
+                  wait_ns, stream);
 }
 
 int hyena_scan_bwd(const void *q, const void *k, const void *v, const void *g, const float *s0,

@@ -116,6 +116,8 @@ struct Params {
   int pair_out;                     // rows and bases allow stores of two channels
   int stages, stage_bytes;
   int dg_mode;                      // 0: dg itself, 1: one partial per block, 2: per channel
+  uint64_t wait_ns;                 // limit of a cluster's waits (2 s but in tests)
+  int fault;                        // test hook: 1: rank 0 of a cluster withholds its first (A, S)
 };
 
 // ---------------------------------------------------------------------------- two channels
@@ -233,12 +235,15 @@ struct Exchange {
 constexpr int kMaxCluster = 8;
 
 // Sends this tile's (A, S) (one warp; lane l and 16 + l hold the same) to every CTA of the cluster:
-// stores that count their bytes on the receiver's barrier, one way.
-__device__ __forceinline__ void send(Exchange &x, int round, int rank, int size, F2 A, F2 S) {
+// stores that count their bytes on the receiver's barrier, one way.  A CTA that has given up sends
+// no more: the phase that it gave up on is open, and may not be armed a second time.
+__device__ __forceinline__ void send(Exchange &x, int round, int rank, int size, F2 A, F2 S,
+                                     int fault) {
   const int lane = threadIdx.x % 32;
   if (lane == 0) mbar_arrive_expect_tx(&x.all[round & 1], size * (kCh / 2) * 16);
   const uint32_t slot = smem_u32(&x.of[round & 1][rank][lane % 16]);
   const uint32_t bar = smem_u32(&x.all[round & 1]);
+  if (fault == 1 && round == 0 && rank == 0) return;
   for (int to = lane / 16; to < size; to += 2)
     asm volatile(
         "{\n\t.reg .u32 a, b;\n\tmapa.shared::cluster.u32 a, %0, %2;\n\t"
@@ -250,7 +255,7 @@ __device__ __forceinline__ void send(Exchange &x, int round, int rank, int size,
 }
 // Waits until every CTA's word of this round is here.
 __device__ __forceinline__ bool received(Exchange &x, int round, Ring &ring, const Params &p) {
-  return mbar_wait(&x.all[round & 1], (round >> 1) & 1, &ring.abort, p.status, kTimeout);
+  return mbar_wait(&x.all[round & 1], (round >> 1) & 1, &ring.abort, p.status, kTimeout, p.wait_ns);
 }
 
 // One decay per row and group of the block by the warps [0, warps): lanes take groups first, in a
@@ -682,9 +687,15 @@ __device__ __forceinline__ void exchange_init(Exchange &x) {
   __syncthreads();
   cluster_sync();
 }
-__device__ __forceinline__ void exchange_end() {
+__device__ __forceinline__ void exchange_end(bool gave_up) {
   __syncwarp();
   cluster_sync();
+  // What peers sent in rounds that this CTA gave up on lands within a few microseconds; nobody
+  // waits for those bytes, so the CTA stays while they arrive.
+  if (gave_up) {
+    const uint64_t t0 = global_timer_ns();
+    for (int i = 0; i < 10000 && global_timer_ns() - t0 < 200000; ++i) __nanosleep(1000);
+  }
 }
 
 // ---------------------------------------------------------------------------- forward
@@ -712,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const CUtensorMap *const maps[5] = {&mk, &mv, kOut ? &mq : &mg, &mg, &mg};
     const void *const ptrs[5] = {p.k, p.v, kOut ? p.q : p.g, p.g, nullptr};
     feed<C, kFeed, false, NS, kCl>(p, ring, stages, maps, ptrs);
-    if (kCl) exchange_end();
+    if (kCl) exchange_end(false);
     return;
   }
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, l = lane % 16;
@@ -737,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int buffer = round & 1;
       if (kCl && tile >= un.tile1) {  // an empty round: the state passes unchanged
         compute_barrier();  // nobody here still reads what peers may overwrite after this send
-        if (warp == 0) send(xch, round, rank, size, kOnes, 0);
+        if (warp == 0 && !dead) send(xch, round, rank, size, kOnes, 0, p.fault);
         if (!received(xch, round, ring, p)) dead = true;
         for (int j = 0; j < size; ++j) {
           const ulonglong2 m = xch.of[buffer][j][l];
@@ -787,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           St = fma2(m.x, St, m.y);
           At = mul2(At, m.x);
         }
-        if (warp == 0) send(xch, round, rank, size, At, St);
+        if (warp == 0 && !dead) send(xch, round, rank, size, At, St, p.fault);
         if (!received(xch, round, ring, p)) dead = true;
 #pragma unroll
         for (int j = 0; j < kMaxCluster; ++j) {
@@ -825,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (from_zero) put_cut(agg + static_cast<int64_t>(un.split) * p.D, c, p.D, whole, carry);
     }
   }
-  if (kCl) exchange_end();
+  if (kCl) exchange_end(dead);
 }
 
 // ---------------------------------------------------------------------------- backward
@@ -913,7 +924,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const CUtensorMap *const maps[5] = {&mq, &mdy, kOut ? &mk : &mg, &mv, &mg};
     const void *const ptrs[5] = {p.q, p.dy, kOut ? p.k : p.g, p.v, p.g};
     feed<C, kFeed, true, NS, kCl>(p, ring, stages, maps, ptrs);
-    if (kCl) exchange_end();
+    if (kCl) exchange_end(false);
     return;
   }
   if (kOut) registers_up<kComputeRegs>();
@@ -944,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         start = get_state(p.ckpt, ckpt0 + tile + walk.step, c, p.D);
       if (kCl && tile >= un.tile1) {  // an empty round: w passes unchanged
         compute_barrier();  // nobody here still reads what peers may overwrite after this send
-        if (warp == 0) send(xch, round, rank, size, kOnes, 0);
+        if (warp == 0 && !dead) send(xch, round, rank, size, kOnes, 0, p.fault);
         if (!received(xch, round, ring, p)) dead = true;
         for (int j = size - 1; j >= 0; --j) {
           const ulonglong2 m = xch.of[buffer][j][l];
@@ -1007,7 +1018,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           Wt = fma2(m, Wt, joint_w[buffer][j][l]);
           At = mul2(At, m);
         }
-        if (warp == 0) send(xch, round, rank, size, At, Wt);
+        if (warp == 0 && !dead) send(xch, round, rank, size, At, Wt, p.fault);
         if (!received(xch, round, ring, p)) dead = true;
 #pragma unroll
         for (int j = kMaxCluster - 1; j >= 0; --j) {
@@ -1099,7 +1110,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!kOut) put_cut(agg + static_cast<int64_t>(un.split) * p.D, c, p.D, whole, w_in);
     }
   }
-  if (kCl) exchange_end();
+  if (kCl) exchange_end(dead);
 }
 
 // dg of group j in a row: the sum of `width` neighbouring partial sums, in order.

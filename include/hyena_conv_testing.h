@@ -44,6 +44,16 @@ int hyena_testing_proj_fault(const void *x, const void *w, const void *residual,
                              int64_t M, int64_t N, int64_t K, int fault, uint64_t wait_ns,
                              cudaStream_t stream);
 
+/*
+ * hyena_scan_fwd (include/hyena_mixer.h) without an initial state, for shapes whose time axis a
+ * cluster of CTAs shares (HYENA_ERR_UNSUPPORTED for others).  `wait_ns` limits the waits of the
+ * cluster's CTAs for each other; fault == 1 makes its first CTA withhold what it tells the others
+ * of its first tile: their waits run out, every CTA leaves and HYENA_DEVICE_TIMEOUT is raised.
+ */
+int hyena_testing_scan_fault(const void *q, const void *k, const void *v, const void *g, void *y,
+                             float *s_out, int64_t B, int64_t L, int64_t D, int d_g, int dtype,
+                             int fault, uint64_t wait_ns, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,4 +1,4 @@
-"""Host-side refusals of the projections' test entry point (no GPU)."""
+"""Host-side refusals of the mixer operators' test entry points (no GPU)."""
 import pytest
 
 from gated_causal_fir_b200 import _native, build
@@ -15,3 +15,16 @@ def test_refusals(kw, code):
     build.build()
     a = dict(ARGS, **kw)
     assert _native.lib().hyena_testing_proj_fault(*[a[n] for n in ARGS], None) == code
+
+
+SCAN = dict(q=1 << 24, k=2 << 24, v=3 << 24, g=4 << 24, y=5 << 24, s_out=6 << 24, B=1, L=1250, D=320,
+            d_g=64, dtype=0, fault=0, wait_ns=20_000_000)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(fault=2), 1), (dict(fault=-1), 1), (dict(wait_ns=10), 1), (dict(wait_ns=1 << 40), 1),
+    (dict(L=100), 2), (dict(D=4096), 2), (dict(q=None), 1), (dict(d_g=7), 1), (dict(y=1 << 24), 1)])
+def test_scan_refusals(kw, code):
+    build.build()
+    a = dict(SCAN, **kw)
+    assert _native.lib().hyena_testing_scan_fault(*[a[n] for n in SCAN], None) == code
