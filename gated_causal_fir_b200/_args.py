@@ -69,11 +69,23 @@ def stream_handle(device, stream):
             else stream.cuda_stream)
 
 
-def keep(stream, *tensors):
-    """Marks buffers made for a call as in use on the stream that the caller gave."""
-    if stream is not None:
-        for t in tensors:
-            t.record_stream(stream)
+def made(stream, device, make):
+    """make(), a buffer for a call on the stream that the caller gave (None: the current one).
+
+    The buffer comes from that stream's memory: one from the current stream's could have been in use
+    a moment ago by work that is still queued there, which the given stream does not wait for.  The
+    current stream is told of it too, since results are read and dropped there."""
+    if stream is None:
+        return make()
+    torch = torch_()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+    current = torch.cuda.current_stream(device)
+    with torch.cuda.stream(stream):
+        t = make()
+    if stream != current:
+        t.record_stream(current)
+    return t
 
 
 def run(name, device, *args):
@@ -96,8 +108,8 @@ def workspace(given, size, device, stream):
     if given is None:
         if size == 0:
             return None, 0, None
-        ws = torch_().empty(size, dtype=torch_().uint8, device=device)
-        keep(stream, ws)
+        ws = made(stream, device,
+                  lambda: torch_().empty(size, dtype=torch_().uint8, device=device))
         return ws.data_ptr(), size, ws
     if not isinstance(given, torch_().Tensor) or given.device != device \
             or not given.is_contiguous():

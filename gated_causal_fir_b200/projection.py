@@ -6,7 +6,7 @@ x: CUDA [..., K], w: [N, K], all bf16 or all fp32; bias fp32 [N].  The functions
 CUDA tensors into pointers, sizes and a stream; outputs and workspaces that are not given come
 from torch.
 """
-from ._args import (CODES, code as code_of, cuda_tensor, keep, nbytes, need, ptr, run,
+from ._args import (CODES, code as code_of, cuda_tensor, made, nbytes, need, ptr, run,
                     stream_handle, torch_, workspace as workspace_of)
 from ._native import ACT_CODES, HYENA_DTYPE_BF16
 
@@ -59,8 +59,9 @@ def hyena_proj_fwd(x, w, bias=None, act="none", residual=None, y=None, z=None, w
     """y = act(x w^T + bias) + residual, [..., N]; returns y.
 
     z: optional [..., N] tensor of x's type that receives the value before the activation, for
-    hyena_proj_bwd.  y may be ``residual`` itself.  Runs asynchronously on ``stream`` (default:
-    the current stream of x's device).
+    hyena_proj_bwd.  y may be ``residual`` itself.  Tensors start on 16-byte boundaries (views into
+    others may not), biases on 4-byte ones.  Runs asynchronously on ``stream`` (default: the
+    current stream of x's device), which waits for nothing queued on others.
     """
     act = _act(act)
     code, M, N, K = _rows(x, w)
@@ -72,8 +73,8 @@ def hyena_proj_fwd(x, w, bias=None, act="none", residual=None, y=None, z=None, w
     if z is not None:
         need("z", z, shape, x.dtype, x.device)
     if y is None:
-        y = x.new_empty(shape) if residual is None else torch_().empty_like(residual)
-        keep(stream, y)
+        y = made(stream, x.device, lambda: x.new_empty(shape) if residual is None else
+                 torch_().empty_like(residual))
     else:
         need("y", y, shape, x.dtype, x.device)
     size = nbytes("hyena_proj_workspace_bytes", M, N, K, code)
@@ -102,16 +103,16 @@ def hyena_proj_bwd(x, w, dy, z=None, act="none", dx_add=None, grads=None, worksp
         raise ValueError("z, the value before the activation, is needed for act %r" % (act,))
     if dx_add is not None:
         need("dx_add", dx_add, x.shape, x.dtype, x.device)
-    made = ()
     if grads is None:
-        grads = made = (torch.empty_like(x), torch.empty_like(w),
-                        torch.empty((N,), dtype=torch.float32, device=x.device))
+        grads = (made(stream, x.device, lambda: torch.empty_like(x)),
+                 made(stream, x.device, lambda: torch.empty_like(w)),
+                 made(stream, x.device,
+                      lambda: torch.empty((N,), dtype=torch.float32, device=x.device)))
     dx, dw, db = grads
     for name, t, like, dt in (("dx", dx, x.shape, x.dtype), ("dw", dw, w.shape, x.dtype),
                               ("db", db, (N,), torch.float32)):
         if t is not None:
             need(name, t, like, dt, x.device)
-    keep(stream, *made)
     act = _act(act)
     size = nbytes("hyena_proj_bwd_workspace_bytes", M, N, K, act, code)
     ws, nws, _buf = workspace_of(workspace, size, x.device, stream)

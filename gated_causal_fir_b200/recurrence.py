@@ -7,7 +7,7 @@ gates of the FIR operator around a state that the data lets decay.  The function
 CUDA tensors into pointers, sizes and a stream; outputs and workspaces that are not given come
 from torch.
 """
-from ._args import (CODES, code as code_of, cuda_tensor, keep, like, nbytes, need, ptr, run,
+from ._args import (CODES, code as code_of, cuda_tensor, like, made, nbytes, need, ptr, run,
                     stream_handle, torch_, workspace as workspace_of)
 from ._native import HYENA_DTYPE_BF16
 
@@ -77,7 +77,7 @@ def hyena_scan_fwd(q, k, v, g, d_g, s0=None, y=None, s_out=None, ckpt=None, work
     decays <= 0; -inf drops the state before its token.  s0: fp32 [B, D], the state before the
     first token (zeros when None).  s_out: fp32 [B, D], the state after the last.  ckpt: a
     tensor of hyena_scan_ckpt(q), filled for hyena_scan_bwd.  Runs asynchronously on ``stream``
-    (default: the current stream of q's device).
+    (default: the current stream of q's device), which waits for nothing queued on others.
     """
     code = _shapes(q, k, v, g, d_g, "B, L, D")
     B, L, D = q.shape
@@ -85,14 +85,12 @@ def hyena_scan_fwd(q, k, v, g, d_g, s0=None, y=None, s_out=None, ckpt=None, work
     _state("s0", s0, q)
     _ckpt(ckpt, q, code)
     if y is None:
-        y = torch_().empty_like(q)
-        keep(stream, y)
+        y = made(stream, q.device, lambda: torch_().empty_like(q))
     else:
         need("y", y, q.shape, q.dtype, device)
     if s_out is None:
-        s_out = (torch_().empty_like(s0) if s0 is not None else
-                 torch_().empty((B, D), dtype=torch_().float32, device=device))
-        keep(stream, s_out)
+        s_out = made(stream, device, lambda: torch_().empty_like(s0) if s0 is not None else
+                     torch_().empty((B, D), dtype=torch_().float32, device=device))
     else:
         _state("s_out", s_out, q)
     size = nbytes("hyena_scan_workspace_bytes", B, L, D, d_g, code)
@@ -118,13 +116,13 @@ def hyena_scan_bwd(q, k, v, g, dy, d_g, s0=None, ds_out=None, ckpt=None, grads=N
     _state("s0", s0, q)
     _state("ds_out", ds_out, q)
     _ckpt(ckpt, q, code)
-    made = []
-    if grads is None:
-        grads = made = (torch.empty_like(q), torch.empty_like(q), torch.empty_like(q),
-                        torch.empty_like(g),
-                        torch.empty((B, D), dtype=torch.float32, device=q.device))
+    given = grads is not None
+    if not given:
+        grads = [made(stream, q.device, lambda t=t: torch.empty_like(t)) for t in (q, q, q, g)]
+        grads.append(made(stream, q.device,
+                          lambda: torch.empty((B, D), dtype=torch.float32, device=q.device)))
     dq, dk, dv, dg, ds0 = grads
-    if not made:
+    if given:
         for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
             need(name, t, q.shape, q.dtype, q.device)
         need("dg", dg, g.shape, g.dtype, q.device)
@@ -133,7 +131,6 @@ def hyena_scan_bwd(q, k, v, g, dy, d_g, s0=None, ds_out=None, ckpt=None, grads=N
         _state("ds0", ds0, q)
     size = nbytes("hyena_scan_bwd_workspace_bytes", B, L, D, d_g, code, int(ckpt is not None))
     ws, nws, _buf = workspace_of(workspace, size, q.device, stream)
-    keep(stream, *made)
     run("hyena_scan_bwd", q.device, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
         ptr(s0), dy.data_ptr(), ptr(ds_out), ptr(ckpt), dq.data_ptr(), dk.data_ptr(),
         dv.data_ptr(), dg.data_ptr(), ds0.data_ptr(), B, L, D, d_g, code, ws, nws,
@@ -156,8 +153,7 @@ def hyena_scan_step(q, k, v, g, state, d_g, y=None, state_out=None, stream=None)
     else:
         _state("state_out", state_out, q)
     if y is None:
-        y = torch_().empty_like(q)
-        keep(stream, y)
+        y = made(stream, q.device, lambda: torch_().empty_like(q))
     else:
         need("y", y, q.shape, q.dtype, q.device)
     run("hyena_scan_step", q.device, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(),
