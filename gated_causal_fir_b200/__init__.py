@@ -17,6 +17,7 @@ projections around a mixer (``hyena_proj_*``), and whole mixer layers over them
 import ctypes
 
 from . import _native
+from ._args import made as _made
 from ._native import (HYENA_ALGO_AUTO, HYENA_ALGO_DIRECT, HYENA_ALGO_FFT, HYENA_ALGO_TENSOR,
                       HYENA_ALGO_WINDOW, HYENA_DEVICE_F16_RANGE, HYENA_DEVICE_TIMEOUT,
                       HYENA_DTYPE_BF16, HYENA_DTYPE_F32, ALGO_NAMES, HyenaError)
@@ -69,7 +70,7 @@ def _dtype_code(t):
     raise TypeError("q, k, v must be bfloat16 or float32, got %s" % t.dtype)
 
 
-def _check(q, k, v, h, d_g, y):
+def _check(q, k, v, h, d_g, y, stream=None):
     torch = _torch()
     for name, t in (("q", q), ("k", k), ("v", v), ("h", h)):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -86,7 +87,7 @@ def _check(q, k, v, h, d_g, y):
     if d_g < 1 or D % d_g != 0 or h.shape[0] * d_g != D:
         raise ValueError("h has %d rows; D=%d with d_g=%d needs D // d_g" % (h.shape[0], D, d_g))
     if y is None:
-        y = torch.empty_like(q)
+        y = _made(stream, q.device, lambda: torch.empty_like(q))
     elif (not isinstance(y, torch.Tensor) or y.shape != q.shape or y.dtype != q.dtype
           or not y.is_cuda or not y.is_contiguous()):
         raise ValueError("y must be a contiguous CUDA tensor like q")
@@ -101,7 +102,7 @@ def hyena_conv_fwd_ex(q, k, v, h, d_g, l_b, algo=HYENA_ALGO_AUTO, y=None, stream
     on l_b).  y: optional preallocated output.  Runs asynchronously on ``stream`` (default: the
     current torch stream).
     """
-    y = _check(q, k, v, h, d_g, y)
+    y = _check(q, k, v, h, d_g, y, stream)
     B, L, D = q.shape
     rc = _native.lib().hyena_conv_fwd_ex(q.data_ptr(), k.data_ptr(), v.data_ptr(), h.data_ptr(),
                                          y.data_ptr(), B, L, D, d_g, h.shape[1], l_b,
@@ -116,7 +117,7 @@ def hyena_conv_fwd_hist(q, k, v, h, d_g, l_b, k_hist, v_hist, algo=HYENA_ALGO_AU
     precede row 0 of every sequence (their last l_h - 1 rows are read); returns y [B, L, D].
     L_hist = 0 (or k_hist None) is zero history."""
     torch = _torch()
-    y = _check(q, k, v, h, d_g, y)
+    y = _check(q, k, v, h, d_g, y, stream)
     B, L, D = q.shape
     if k_hist is None or k_hist.shape[1] == 0:
         kp = vp = None
@@ -152,11 +153,12 @@ def hyena_conv_fwd_fft(q, k, v, h, d_g, l_b, workspace=None, y=None, stream=None
     hyena_conv_fwd_ex; ``workspace`` is a CUDA uint8 tensor of at least
     hyena_conv_fwd_fft_workspace_bytes() bytes (allocated here when None)."""
     torch = _torch()
-    y = _check(q, k, v, h, d_g, y)
+    y = _check(q, k, v, h, d_g, y, stream)
     B, L, D = q.shape
     need = hyena_conv_fwd_fft_workspace_bytes(B, L, D, d_g, h.shape[1])
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        workspace = _made(stream, q.device,
+                          lambda: torch.empty(max(need, 1), dtype=torch.uint8, device=q.device))
     rc = _native.lib().hyena_conv_fwd_fft(q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                           h.data_ptr(), y.data_ptr(), B, L, D, d_g, h.shape[1],
                                           l_b, _dtype_code(q), workspace.data_ptr(),
@@ -168,7 +170,7 @@ def hyena_conv_fwd_fft(q, k, v, h, d_g, l_b, workspace=None, y=None, stream=None
 
 def hyena_conv_fwd(q, k, v, h, d_g, l_b, y=None, stream=None):
     """bf16 forward, fastest supported algorithm (C: hyena_conv_fwd); returns y."""
-    y = _check(q, k, v, h, d_g, y)
+    y = _check(q, k, v, h, d_g, y, stream)
     if _dtype_code(q) != HYENA_DTYPE_BF16:
         raise TypeError("hyena_conv_fwd takes bf16 q, k, v; use hyena_conv_fwd_f32 for fp32")
     B, L, D = q.shape
@@ -181,7 +183,7 @@ def hyena_conv_fwd(q, k, v, h, d_g, l_b, y=None, stream=None):
 
 def hyena_conv_fwd_f32(q, k, v, h, d_g, l_b, y=None, stream=None):
     """fp32 forward (C: hyena_conv_fwd_f32); returns y."""
-    y = _check(q, k, v, h, d_g, y)
+    y = _check(q, k, v, h, d_g, y, stream)
     if _dtype_code(q) != HYENA_DTYPE_F32:
         raise TypeError("hyena_conv_fwd_f32 takes fp32 q, k, v")
     B, L, D = q.shape
@@ -244,15 +246,14 @@ def hyena_conv_bwd_ex(q, k, v, h, dy, d_g, l_b, algo=HYENA_ALGO_AUTO, workspace=
     ``grads``: optional preallocated (dq, dk, dv, dh).
     """
     torch = _torch()
-    _check(q, k, v, h, d_g, None)
+    _check(q, k, v, h, d_g, q)
     if (not isinstance(dy, torch.Tensor) or not dy.is_cuda or dy.shape != q.shape
             or dy.dtype != q.dtype or not dy.is_contiguous()):
         raise ValueError("dy must be a contiguous CUDA tensor like q")
     B, L, D = q.shape
     l_h = h.shape[1]
     if grads is None:
-        grads = (torch.empty_like(q), torch.empty_like(q), torch.empty_like(q),
-                 torch.empty_like(h))
+        grads = [_made(stream, q.device, lambda t=t: torch.empty_like(t)) for t in (q, q, q, h)]
     dq, dk, dv, dh = grads
     for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
         if (t.shape != q.shape or t.dtype != q.dtype or not t.is_cuda
@@ -263,7 +264,8 @@ def hyena_conv_bwd_ex(q, k, v, h, dy, d_g, l_b, algo=HYENA_ALGO_AUTO, workspace=
         raise ValueError("dh must be a contiguous CUDA float32 tensor like h")
     need = hyena_conv_bwd_workspace_bytes(B, L, D, d_g, l_h)
     if workspace is None:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        workspace = _made(stream, q.device, lambda: torch.empty(max(need, 256), dtype=torch.uint8,
+                                                                device=q.device))
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
     ws_bytes = workspace.numel() * workspace.element_size()
@@ -283,7 +285,8 @@ def hyena_build_toeplitz(h, l_b, stream=None):
             or h.dim() != 2 or not h.is_contiguous():
         raise TypeError("h must be a contiguous CUDA float32 [G, l_h] tensor")
     G, l_h = h.shape
-    H = torch.empty((3, G, l_b, l_b), dtype=torch.float32, device=h.device)
+    H = _made(stream, h.device,
+              lambda: torch.empty((3, G, l_b, l_b), dtype=torch.float32, device=h.device))
     rc = _native.lib().hyena_build_toeplitz(h.data_ptr(), H[0].data_ptr(), H[1].data_ptr(),
                                             H[2].data_ptr(), G, l_h, l_b, _stream(stream))
     _native.check("hyena_build_toeplitz", rc)
@@ -308,7 +311,8 @@ def hyena_build_toeplitz_blocks(h, l_b, S=None, stream=None):
     G, l_h = h.shape
     if S is None:
         S = hyena_toeplitz_stages(l_h, l_b)
-    H = torch.empty((S, G, l_b, l_b), dtype=torch.float32, device=h.device)
+    H = _made(stream, h.device,
+              lambda: torch.empty((S, G, l_b, l_b), dtype=torch.float32, device=h.device))
     rc = _native.lib().hyena_build_toeplitz_blocks(h.data_ptr(), H.data_ptr(), S, G, l_h, l_b,
                                                    _stream(stream))
     _native.check("hyena_build_toeplitz_blocks", rc)
