@@ -17,7 +17,7 @@ projections around a mixer (``hyena_proj_*``), and whole mixer layers over them
 import ctypes
 
 from . import _native
-from ._args import made as _made
+from ._args import made as _made, run as _run, stream_handle as _stream
 from ._native import (HYENA_ALGO_AUTO, HYENA_ALGO_DIRECT, HYENA_ALGO_FFT, HYENA_ALGO_TENSOR,
                       HYENA_ALGO_WINDOW, HYENA_DEVICE_F16_RANGE, HYENA_DEVICE_TIMEOUT,
                       HYENA_DTYPE_BF16, HYENA_DTYPE_F32, ALGO_NAMES, HyenaError)
@@ -55,12 +55,6 @@ def _torch():
     return torch
 
 
-def _stream(stream):
-    torch = _torch()
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
-
-
 def _dtype_code(t):
     torch = _torch()
     if t.dtype == torch.bfloat16:
@@ -70,6 +64,11 @@ def _dtype_code(t):
     raise TypeError("q, k, v must be bfloat16 or float32, got %s" % t.dtype)
 
 
+def _same_device(name, t, q):
+    if t.device != q.device:
+        raise ValueError("%s is on %s, q on %s" % (name, t.device, q.device))
+
+
 def _check(q, k, v, h, d_g, y, stream=None):
     torch = _torch()
     for name, t in (("q", q), ("k", k), ("v", v), ("h", h)):
@@ -77,6 +76,7 @@ def _check(q, k, v, h, d_g, y, stream=None):
             raise TypeError("%s must be a CUDA tensor" % name)
         if not t.is_contiguous():
             raise ValueError("%s must be contiguous" % name)
+        _same_device(name, t, q)
     if q.dim() != 3 or k.shape != q.shape or v.shape != q.shape:
         raise ValueError("q, k, v must share one [B, L, D] shape")
     if k.dtype != q.dtype or v.dtype != q.dtype:
@@ -91,6 +91,8 @@ def _check(q, k, v, h, d_g, y, stream=None):
     elif (not isinstance(y, torch.Tensor) or y.shape != q.shape or y.dtype != q.dtype
           or not y.is_cuda or not y.is_contiguous()):
         raise ValueError("y must be a contiguous CUDA tensor like q")
+    else:
+        _same_device("y", y, q)
     return y
 
 
@@ -100,14 +102,13 @@ def hyena_conv_fwd_ex(q, k, v, h, d_g, l_b, algo=HYENA_ALGO_AUTO, y=None, stream
     q, k, v: CUDA [B, L, D], all bf16 or all fp32.  h: CUDA fp32 [D // d_g, l_h].
     l_b: block size of the decomposition (any l_h >= 1 is accepted; the result does not depend
     on l_b).  y: optional preallocated output.  Runs asynchronously on ``stream`` (default: the
-    current torch stream).
+    current torch stream of q's device).
     """
     y = _check(q, k, v, h, d_g, y, stream)
     B, L, D = q.shape
-    rc = _native.lib().hyena_conv_fwd_ex(q.data_ptr(), k.data_ptr(), v.data_ptr(), h.data_ptr(),
-                                         y.data_ptr(), B, L, D, d_g, h.shape[1], l_b,
-                                         _dtype_code(q), algo, _stream(stream))
-    _native.check("hyena_conv_fwd_ex", rc)
+    _run("hyena_conv_fwd_ex", q.device, q.data_ptr(), k.data_ptr(), v.data_ptr(), h.data_ptr(),
+         y.data_ptr(), B, L, D, d_g, h.shape[1], l_b, _dtype_code(q), algo,
+         _stream(q.device, stream))
     return y
 
 
@@ -132,11 +133,9 @@ def hyena_conv_fwd_hist(q, k, v, h, d_g, l_b, k_hist, v_hist, algo=HYENA_ALGO_AU
             raise ValueError("k_hist, v_hist must both be [B, L_hist, D] with q's B and D")
         kp, vp = k_hist.data_ptr(), v_hist.data_ptr()
         L_hist = k_hist.shape[1]
-    rc = _native.lib().hyena_conv_fwd_hist(q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                           h.data_ptr(), y.data_ptr(), kp, vp, L_hist, B, L, D,
-                                           d_g, h.shape[1], l_b, _dtype_code(q), algo,
-                                           _stream(stream))
-    _native.check("hyena_conv_fwd_hist", rc)
+    _run("hyena_conv_fwd_hist", q.device, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+         h.data_ptr(), y.data_ptr(), kp, vp, L_hist, B, L, D, d_g, h.shape[1], l_b,
+         _dtype_code(q), algo, _stream(q.device, stream))
     return y
 
 
@@ -159,12 +158,11 @@ def hyena_conv_fwd_fft(q, k, v, h, d_g, l_b, workspace=None, y=None, stream=None
     if workspace is None:
         workspace = _made(stream, q.device,
                           lambda: torch.empty(max(need, 1), dtype=torch.uint8, device=q.device))
-    rc = _native.lib().hyena_conv_fwd_fft(q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                          h.data_ptr(), y.data_ptr(), B, L, D, d_g, h.shape[1],
-                                          l_b, _dtype_code(q), workspace.data_ptr(),
-                                          workspace.numel() * workspace.element_size(),
-                                          _stream(stream))
-    _native.check("hyena_conv_fwd_fft", rc)
+    _same_device("workspace", workspace, q)
+    _run("hyena_conv_fwd_fft", q.device, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+         h.data_ptr(), y.data_ptr(), B, L, D, d_g, h.shape[1], l_b, _dtype_code(q),
+         workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+         _stream(q.device, stream))
     return y
 
 
@@ -174,10 +172,8 @@ def hyena_conv_fwd(q, k, v, h, d_g, l_b, y=None, stream=None):
     if _dtype_code(q) != HYENA_DTYPE_BF16:
         raise TypeError("hyena_conv_fwd takes bf16 q, k, v; use hyena_conv_fwd_f32 for fp32")
     B, L, D = q.shape
-    rc = _native.lib().hyena_conv_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), h.data_ptr(),
-                                      y.data_ptr(), B, L, D, d_g, h.shape[1], l_b,
-                                      _stream(stream))
-    _native.check("hyena_conv_fwd", rc)
+    _run("hyena_conv_fwd", q.device, q.data_ptr(), k.data_ptr(), v.data_ptr(), h.data_ptr(),
+         y.data_ptr(), B, L, D, d_g, h.shape[1], l_b, _stream(q.device, stream))
     return y
 
 
@@ -187,10 +183,8 @@ def hyena_conv_fwd_f32(q, k, v, h, d_g, l_b, y=None, stream=None):
     if _dtype_code(q) != HYENA_DTYPE_F32:
         raise TypeError("hyena_conv_fwd_f32 takes fp32 q, k, v")
     B, L, D = q.shape
-    rc = _native.lib().hyena_conv_fwd_f32(q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                          h.data_ptr(), y.data_ptr(), B, L, D, d_g, h.shape[1],
-                                          l_b, _stream(stream))
-    _native.check("hyena_conv_fwd_f32", rc)
+    _run("hyena_conv_fwd_f32", q.device, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+         h.data_ptr(), y.data_ptr(), B, L, D, d_g, h.shape[1], l_b, _stream(q.device, stream))
     return y
 
 
@@ -250,6 +244,7 @@ def hyena_conv_bwd_ex(q, k, v, h, dy, d_g, l_b, algo=HYENA_ALGO_AUTO, workspace=
     if (not isinstance(dy, torch.Tensor) or not dy.is_cuda or dy.shape != q.shape
             or dy.dtype != q.dtype or not dy.is_contiguous()):
         raise ValueError("dy must be a contiguous CUDA tensor like q")
+    _same_device("dy", dy, q)
     B, L, D = q.shape
     l_h = h.shape[1]
     if grads is None:
@@ -259,22 +254,23 @@ def hyena_conv_bwd_ex(q, k, v, h, dy, d_g, l_b, algo=HYENA_ALGO_AUTO, workspace=
         if (t.shape != q.shape or t.dtype != q.dtype or not t.is_cuda
                 or not t.is_contiguous()):
             raise ValueError("%s must be a contiguous CUDA tensor like q" % name)
+        _same_device(name, t, q)
     if dh.shape != h.shape or dh.dtype != torch.float32 or not dh.is_cuda \
             or not dh.is_contiguous():
         raise ValueError("dh must be a contiguous CUDA float32 tensor like h")
+    _same_device("dh", dh, q)
     need = hyena_conv_bwd_workspace_bytes(B, L, D, d_g, l_h)
     if workspace is None:
         workspace = _made(stream, q.device, lambda: torch.empty(max(need, 256), dtype=torch.uint8,
                                                                 device=q.device))
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
+    _same_device("workspace", workspace, q)
     ws_bytes = workspace.numel() * workspace.element_size()
-    rc = _native.lib().hyena_conv_bwd_ex(q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                         h.data_ptr(), dy.data_ptr(), dq.data_ptr(),
-                                         dk.data_ptr(), dv.data_ptr(), dh.data_ptr(), B, L, D,
-                                         d_g, l_h, l_b, _dtype_code(q), algo,
-                                         workspace.data_ptr(), ws_bytes, _stream(stream))
-    _native.check("hyena_conv_bwd_ex", rc)
+    _run("hyena_conv_bwd_ex", q.device, q.data_ptr(), k.data_ptr(), v.data_ptr(), h.data_ptr(),
+         dy.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dh.data_ptr(), B, L, D,
+         d_g, l_h, l_b, _dtype_code(q), algo, workspace.data_ptr(), ws_bytes,
+         _stream(q.device, stream))
     return dq, dk, dv, dh
 
 
@@ -287,9 +283,8 @@ def hyena_build_toeplitz(h, l_b, stream=None):
     G, l_h = h.shape
     H = _made(stream, h.device,
               lambda: torch.empty((3, G, l_b, l_b), dtype=torch.float32, device=h.device))
-    rc = _native.lib().hyena_build_toeplitz(h.data_ptr(), H[0].data_ptr(), H[1].data_ptr(),
-                                            H[2].data_ptr(), G, l_h, l_b, _stream(stream))
-    _native.check("hyena_build_toeplitz", rc)
+    _run("hyena_build_toeplitz", h.device, h.data_ptr(), H[0].data_ptr(), H[1].data_ptr(),
+         H[2].data_ptr(), G, l_h, l_b, _stream(h.device, stream))
     return H[0], H[1], H[2]
 
 
@@ -313,9 +308,8 @@ def hyena_build_toeplitz_blocks(h, l_b, S=None, stream=None):
         S = hyena_toeplitz_stages(l_h, l_b)
     H = _made(stream, h.device,
               lambda: torch.empty((S, G, l_b, l_b), dtype=torch.float32, device=h.device))
-    rc = _native.lib().hyena_build_toeplitz_blocks(h.data_ptr(), H.data_ptr(), S, G, l_h, l_b,
-                                                   _stream(stream))
-    _native.check("hyena_build_toeplitz_blocks", rc)
+    _run("hyena_build_toeplitz_blocks", h.device, h.data_ptr(), H.data_ptr(), S, G, l_h, l_b,
+         _stream(h.device, stream))
     return H
 
 
