@@ -347,9 +347,9 @@ def hyena_conv_fwd_from_host(q, k, v, h, d_g, l_b, out=None, device="cuda", stre
     (bf16 or fp32 [B, L, D], contiguous; pinned for overlapped copies) and h (fp32
     [D / d_g, l_h]) go to ``device`` chunk by chunk, the forward runs there and y comes back
     into ``out`` (a host tensor, pinned when created here).  The library queues every copy and
-    kernel; this wrapper only supplies the device workspace (cached per shape when not given)
-    and the stream.  Synchronise ``stream`` (default: the current stream) before reading
-    ``out``."""
+    kernel; this wrapper only supplies the device workspace (kept for the next call on the same
+    stream when not given) and the stream.  Synchronise ``stream`` (default: the current stream)
+    before reading ``out``."""
     torch = _torch()
     for name, t in (("q", q), ("k", k), ("v", v), ("h", h)):
         if t.device.type != "cpu" or not t.is_contiguous():
@@ -366,17 +366,22 @@ def hyena_conv_fwd_from_host(q, k, v, h, d_g, l_b, out=None, device="cuda", stre
             out.dtype != q.dtype:
         raise TypeError("out must be a contiguous host tensor like q")
     dev = torch.device(device)
+    if dev.index is None:
+        dev = torch.device(dev.type, torch.cuda.current_device())
+    st = torch.cuda.current_stream(dev) if stream is None else stream
     if workspace is None:
         need = int(_native.lib().hyena_conv_fwd_from_host_workspace_bytes(
             B, L, D, d_g, h.shape[1], dt, chunk))
         if need < 0:
             raise _native.HyenaError("hyena_conv_fwd_from_host", -need)
-        key = (str(dev), need)
+        # one for each stream: calls on two of them run at the same time
+        key = (dev.index, st.cuda_stream)
         workspace = _HOST_WS.get(key)
-        if workspace is None:
-            _HOST_WS.clear()
-            workspace = _HOST_WS[key] = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    st = torch.cuda.current_stream(dev) if stream is None else stream
+        if workspace is None or workspace.numel() < need:
+            if len(_HOST_WS) >= 8:
+                _HOST_WS.clear()
+            workspace = _HOST_WS[key] = _made(
+                stream, dev, lambda: torch.empty(max(need, 1), dtype=torch.uint8, device=dev))
     # the library's streams finish before `st` goes on: the allocator must not hand the
     # workspace out again before `st` has passed this call
     workspace.record_stream(st)

@@ -40,3 +40,25 @@ def test_a_given_stream_does_not_share_freed_memory_with_the_current_one(name):
                      [4 * 64 * 64 * 4 * S for S in (1, 2, 3)]),
     }[name]
     beside_queued_work(call, sizes)
+
+
+def test_calls_on_host_tensors_on_two_streams_have_workspaces_of_their_own():
+    """The same shape with two filters, in turn on two streams without waits between them."""
+    from gated_causal_fir_b200 import _HOST_WS
+    q, k, v = (torch.randn(1, 4096, 512).to(BF16).pin_memory() for _ in range(3))
+    hs = [(torch.randn(8, 128) / 11).pin_memory() for _ in range(2)]
+    want = []
+    for h in hs:
+        want.append(g.hyena_conv_fwd_from_host(q, k, v, h, 64, 64, chunk=512))
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    runs = []
+    for _ in range(6):
+        for h, s in zip(hs, streams):
+            runs.append(g.hyena_conv_fwd_from_host(q, k, v, h, 64, 64, stream=s, chunk=512))
+    torch.cuda.synchronize()
+    for i, y in enumerate(runs):
+        assert torch.equal(y, want[i % 2])
+    index = torch.cuda.current_device()
+    places = {_HOST_WS[(index, s.cuda_stream)].data_ptr() for s in streams}
+    assert len(places) == 2
