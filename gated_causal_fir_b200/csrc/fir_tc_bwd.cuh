@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Launched with programmatic stream serialisation after the dq forward, which only starts
   // its dependents once it has itself waited for every earlier kernel of the stream: the
   // inputs are complete when this grid starts, and nothing here reads what the forward writes
-  // (dq), so the work overlaps the forward's last tiles without a grid-dependency wait.
+  // (dq), so the work overlaps the forward's last tiles; it waits for the forward at its end.
   griddep_launch_dependents();
   // The gate threads issue the loads of the first segment's filter taps before the barrier
   // (and each gate warp leaves the group's largest |h| among its taps in tapmax[0][warp]).
@@ -714,6 +714,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (et == 0) p.seg_count[blockIdx.x] = nseg < p.max_segs ? nseg : p.max_segs;
   }
 
+  // This grid may not complete before the dq forward has: the kernels behind it wait for this grid
+  // alone, and the first that reads dq would start too early.
+  griddep_wait();
   __syncthreads();
   if (warp == kWarpMma) {
     __syncwarp();

@@ -936,12 +936,16 @@ int launch_tensor_bwd(const Problem &P, const void *dy, void *dq, void *dk, void
   Problem F = P;  // dq through the forward kernels
   F.q = dy;
   F.y = dq;
-  const int rf = run(F, HYENA_ALGO_AUTO, s);
+  const int fwd_algo = select_algo(F);
+  const int rf = run(F, fwd_algo, s);
   if (rf != HYENA_OK) return rf;
-  // Programmatic dependent launch: the set-up overlaps the end of the dq forward.
+  // Programmatic dependent launch: the set-up overlaps the end of the dq forward.  Only behind
+  // fir_tc_kernel, which lets it start once its own wait is over; other forward kernels do so
+  // before, and fir_tc_bwd_kernel waits for nothing before it reads.
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = HYENA_PDL;
+  attr[0].val.programmaticStreamSerializationAllowed =
+      HYENA_PDL && fwd_algo == HYENA_ALGO_TENSOR;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(tb::kThreads);
