@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kDhTaps)
                               const unsigned *__restrict__ run_if, unsigned run_token) {
   if (run_if) {  // as fir_tiled_kernel's run_if
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (*run_if != run_token) return;
+    if (*cc::behind_wait(run_if) != run_token) return;
   }
   extern __shared__ float sm[];
   // one (chunk, piece, sequence) block after another, grid-stride
@@ -155,6 +155,8 @@ __global__ void __launch_bounds__(kBwdWindowBlock)
                           const T *__restrict__ dy, T *__restrict__ dk, T *__restrict__ dv,
                           float *__restrict__ partial, const cc::WindowParams p) {
   cc::pdl_enter();  // launched with programmatic stream serialisation
+  q = cc::behind_wait(q), k = cc::behind_wait(k), v = cc::behind_wait(v);
+  h = cc::behind_wait(h), dy = cc::behind_wait(dy);
   using V = cc::Vec<T>;
   constexpr int VN = V::N;
   constexpr int U = LH <= 8 ? 4 : 2;  // rows of loads issued before their arithmetic
@@ -169,7 +171,7 @@ __global__ void __launch_bounds__(kBwdWindowBlock)
 
   float hr[LH];
 #pragma unroll
-  for (int j = 0; j < LH; ++j) hr[j] = __ldg(h + g * LH + j);
+  for (int j = 0; j < LH; ++j) hr[j] = h[g * LH + j];
   float zw[LH][VN];  // zw[j] = dz at time t + j
   float dh[LH];
 #pragma unroll
@@ -262,7 +264,8 @@ __global__ void __launch_bounds__(kReduceBlock)
                              const unsigned *__restrict__ run_if, unsigned run_token) {
   if (run_if) {  // as fir_tiled_kernel's run_if
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (*run_if != run_token) return;
+    if (*cc::behind_wait(run_if) != run_token) return;
+    partial = cc::behind_wait(partial);
   }
   const int lane = threadIdx.x & 31;
   const long long warps = static_cast<long long>(gridDim.x) * (kReduceBlock / 32);

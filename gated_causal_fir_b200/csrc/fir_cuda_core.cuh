@@ -28,7 +28,7 @@ template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int N = 8;
   __device__ static uint4 load(const __nv_bfloat16 *p) {
-    return __ldg(reinterpret_cast<const uint4 *>(p));
+    return *reinterpret_cast<const uint4 *>(p);
   }
   __device__ static void unpack(const uint4 &u, float (&o)[8]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -53,7 +53,7 @@ template <>
 struct Vec<float> {
   static constexpr int N = 4;
   __device__ static uint4 load(const float *p) {
-    return __ldg(reinterpret_cast<const uint4 *>(p));
+    return *reinterpret_cast<const uint4 *>(p);
   }
   __device__ static void unpack(const uint4 &u, float (&o)[4]) {
     o[0] = __uint_as_float(u.x);
@@ -72,6 +72,18 @@ struct Vec<float> {
 __device__ __forceinline__ void pdl_enter() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// A pointer to global memory that an earlier kernel may have written while this one already ran,
+// for reads after griddepcontrol.wait.  What a kernel only reads through a __restrict__ parameter
+// counts as constant for its whole life: the compiler may load it through the non-coherent cache,
+// and ahead of the wait (an FFT pass once read the last call's spectrum that way).  It knows
+// nothing about the pointer that comes out of here, so the loads stay behind this point.
+template <typename T>
+__device__ __forceinline__ const T *behind_wait(const T *p) {
+  size_t a = __cvta_generic_to_global(p);
+  asm volatile("" : "+l"(a)::"memory");
+  return static_cast<const T *>(__cvta_global_to_generic(a));
 }
 
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -111,6 +123,7 @@ __global__ void __launch_bounds__(kWindowBlock, HYENA_WINDOW_MIN_BLOCKS)
   // Longer windows hold more registers: they unroll no further than 4 rows.
   constexpr int U = LH <= 8 ? kWindowUnroll : (kWindowUnroll < 4 ? kWindowUnroll : 4);
   pdl_enter();  // launched with programmatic stream serialisation
+  q = behind_wait(q), k = behind_wait(k), v = behind_wait(v), h = behind_wait(h);
   const long long gid = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (gid >= p.B * p.n_tb * p.cv) return;
   const long long cvi = gid % p.cv;
@@ -122,7 +135,7 @@ __global__ void __launch_bounds__(kWindowBlock, HYENA_WINDOW_MIN_BLOCKS)
 
   float hr[LH];
 #pragma unroll
-  for (int j = 0; j < LH; ++j) hr[j] = __ldg(h + g * LH + j);
+  for (int j = 0; j < LH; ++j) hr[j] = h[g * LH + j];
 
   float xw[LH][VN];  // xw[j] = x at time t - j
 #pragma unroll
@@ -223,11 +236,12 @@ __global__ void __launch_bounds__(kTileThreads)
   // run_if (anti only; may be null): a device word; unless it holds run_token the kernel does
   // nothing (the fp32 recomputation behind the tensor-core backward, needed only where that
   // kernel raised its flag).  Such a launch may start early (programmatic dependent launch): it
-  // waits for the previous kernels of the stream before it reads anything.
+  // waits for the previous kernels of the stream before it reads anything.  Of what it reads only
+  // the word comes from kernels of the same call; the tensors were complete before those began.
   if constexpr (kAnti) {
     if (run_if) {
       asm volatile("griddepcontrol.wait;" ::: "memory");
-      if (*run_if != run_token) return;
+      if (*behind_wait(run_if) != run_token) return;
     }
   }
   extern __shared__ float xs[];  // [kTileWin][kTileC]

@@ -295,12 +295,13 @@ __global__ void __launch_bounds__(kThreads)
   const int idx = threadIdx.x / kP, sig = threadIdx.x % kP;
   fill_twiddles(tw, N1, tw2, n2, N);
   cc::pdl_enter();  // launched with programmatic stream serialisation (the tables overlap)
+  k = cc::behind_wait(k), v = cc::behind_wait(v), h = cc::behind_wait(h);
   // stage the rows t = N2 n1 + n2 of the CTA's 16 signals: ex[n1 * 16 + signal]
   if constexpr (kSpectrum) {
     for (int e = threadIdx.x; e < N1 * kP; e += blockDim.x) {
       const int n1 = e / kP, sg = e % kP;
       const int t = p.N2 * n1 + n2, s = s0 + sg;
-      ex[e] = make_float2(s < p.PT && t < p.l_h ? __ldg(h + s * p.l_h + t) : 0.f, 0.f);
+      ex[e] = make_float2(s < p.PT && t < p.l_h ? h[s * p.l_h + t] : 0.f, 0.f);
     }
   } else {
     constexpr int VP = PairVec<T>::VP, NV = kP / VP;
@@ -407,6 +408,7 @@ __global__ void __launch_bounds__(kThreads)
   const int idx = threadIdx.x / kP, sig = threadIdx.x % kP;
   fill_twiddles(tw, N1, tw2, n2, N);
   cc::pdl_enter();  // launched with programmatic stream serialisation (the tables overlap)
+  q = cc::behind_wait(q);
   __syncthreads();
   float2 va[R1], vb[BLay<N1>::M];
   {

@@ -258,13 +258,13 @@ __device__ __forceinline__ void lds_words(const uint8_t *p, uint32_t (&w)[kB / 4
 template <int kB>
 __device__ __forceinline__ void ldg_words(const uint8_t *p, uint32_t (&w)[kB / 4]) {
   if constexpr (kB == 16) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+    const uint4 u = *reinterpret_cast<const uint4 *>(p);
     w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
   } else if constexpr (kB == 8) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
     w[0] = u.x, w[1] = u.y;
   } else {
-    w[0] = __ldg(reinterpret_cast<const unsigned int *>(p));
+    w[0] = *reinterpret_cast<const unsigned int *>(p);
   }
 }
 template <int kB>
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(NT, 1) fir_fftblk_kernel(const BlkParams p) {
       __syncthreads();   // the table is written; the previous spectrum is no longer read
       const float *hg = p.h + static_cast<long long>(o.g) * p.l_h;
       for (int r = tid; r < N; r += NT)
-        Hs[slot(r)] = make_float2(r < p.l_h ? __ldg(hg + r) * inv_n : 0.f, 0.f);
+        Hs[slot(r)] = make_float2(r < p.l_h ? hg[r] * inv_n : 0.f, 0.f);
       __syncthreads();
       forward_outer<LGN>(Hs, 1, tw, tid, NT);
       middle<LGN, false>(Hs, 1, nullptr, tid, NT);

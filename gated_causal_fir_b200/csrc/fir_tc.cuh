@@ -377,6 +377,13 @@ __device__ __forceinline__ uint32_t kv_absmax(uint32_t kbase, uint32_t vbase, in
 // filters instead of each band lane fetching its own taps.  The loads (tap_load) are issued
 // into registers and written to shared memory later (tap_store), so their latency can overlap
 // other work.
+// A load that stays where it is among the waits, as a volatile instruction, without holding up the
+// other memory accesses around it.
+__device__ __forceinline__ float ld_tap(const float *p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
 template <int kPer>
 __device__ __forceinline__ void tap_load(float (&v)[kPer], const float *hblk, int l_h, int halo,
                                          int ng, int tid) {
@@ -385,7 +392,7 @@ __device__ __forceinline__ void tap_load(float (&v)[kPer], const float *hblk, in
   for (int k = 0; k < kPer; ++k) {
     const int e = tid + k * kGroupThreads;
     const int gg = e / stride, idx = e - gg * stride - 2 - 127;
-    v[k] = (gg < ng && idx >= 0 && idx < l_h) ? __ldg(hblk + gg * l_h + idx) : 0.f;
+    v[k] = (gg < ng && idx >= 0 && idx < l_h) ? ld_tap(hblk + gg * l_h + idx) : 0.f;
   }
 }
 
@@ -480,9 +487,9 @@ __device__ __forceinline__ void recompute_row_fp32(const Params &p, int blk, int
       } else {
         break;
       }
-      const uint4 kw = __ldg(reinterpret_cast<const uint4 *>(kr) + c8);
-      const uint4 vw = __ldg(reinterpret_cast<const uint4 *>(vr) + c8);
-      const float hj = __ldg(hg + j);
+      const uint4 kw = reinterpret_cast<const uint4 *>(kr)[c8];
+      const uint4 vw = reinterpret_cast<const uint4 *>(vr)[c8];
+      const float hj = hg[j];
       const uint32_t kk[4] = {kw.x, kw.y, kw.z, kw.w}, vv[4] = {vw.x, vw.y, vw.z, vw.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -492,7 +499,7 @@ __device__ __forceinline__ void recompute_row_fp32(const Params &p, int blk, int
         acc[2 * e + 1] = fmaf(hj, x1, acc[2 * e + 1]);
       }
     }
-    const uint4 qv = __ldg(reinterpret_cast<const uint4 *>(p.q + row) + c8);
+    const uint4 qv = reinterpret_cast<const uint4 *>(p.q + row)[c8];
     const uint32_t qw[4] = {qv.x, qv.y, qv.z, qv.w};
     uint32_t ow[4];
 #pragma unroll

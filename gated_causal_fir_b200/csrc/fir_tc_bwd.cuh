@@ -45,6 +45,7 @@
 //    instead of 192 us at the MR shape: this kernel's time follows its gate and epilogue
 //    warps' critical path, and every added step on it showed in the total.)
 #pragma once
+#include "fir_cuda_core.cuh"
 #include "fir_tc.cuh"
 
 namespace hyena {
@@ -740,6 +741,8 @@ __global__ void __launch_bounds__(256)
                              float *__restrict__ dh, int G, int l_h, long long per, long long rem,
                              long long span) {
   griddep_wait();  // launched with programmatic stream serialisation after fir_tc_bwd_kernel
+  partial = cc::behind_wait(partial);
+  seg_group = cc::behind_wait(seg_group), seg_count = cc::behind_wait(seg_count);
   const long long n = static_cast<long long>(G) * l_h;
   for (long long e = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; e < n;
        e += static_cast<long long>(gridDim.x) * blockDim.x) {
