@@ -978,30 +978,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The sums of the cut tiles' partial products, in order, and their epilogue: a tile per blockIdx.y,
-// four columns of a row per thread.
+// The sums of the cut tiles' partial products, in order, and their epilogue: a tile per blockIdx.y
+// (and every gridDim.y-th after it), four columns of a row per thread.
 template <typename T, int kM, int kN>
 __global__ void __launch_bounds__(256) proj_join_kernel(const Params p) {
   griddep_launch_dependents();
   griddep_wait();
-  int tm, tn;
-  tile_at(p, p.whole + blockIdx.y, &tm, &tn);
-  // rows of a tile that can be in range at all: a product of few rows fills little of its tiles
-  const int rows = min(kM, p.M - tm * kM);
-  const float *part = p.partial + static_cast<int64_t>(blockIdx.y) * p.splits * (kM * kN);
-  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < rows * (kN / 4); i += gridDim.x * blockDim.x) {
-    const int r = i / (kN / 4), c4 = i % (kN / 4) * 4, col = tn * kN + c4;
-    if (col >= p.N) continue;
-    float c[4] = {0.f, 0.f, 0.f, 0.f};
-    const float *from = part + r * kN + c4;
+  const int rest = p.tiles_m * p.tiles_n - p.whole;
+  for (int tile = blockIdx.y; tile < rest; tile += gridDim.y) {
+    int tm, tn;
+    tile_at(p, p.whole + tile, &tm, &tn);
+    // rows of a tile that can be in range at all: a product of few rows fills little of its tiles
+    const int rows = min(kM, p.M - tm * kM);
+    const float *part = p.partial + static_cast<int64_t>(tile) * p.splits * (kM * kN);
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < rows * (kN / 4);
+         i += gridDim.x * blockDim.x) {
+      const int r = i / (kN / 4), c4 = i % (kN / 4) * 4, col = tn * kN + c4;
+      if (col >= p.N) continue;
+      float c[4] = {0.f, 0.f, 0.f, 0.f};
+      const float *from = part + r * kN + c4;
 #pragma unroll 4
-    for (int s = 0; s < p.splits; ++s) {
-      const float4 v = *reinterpret_cast<const float4 *>(from + static_cast<int64_t>(s) * (kM * kN));
-      c[0] += v.x, c[1] += v.y, c[2] += v.z, c[3] += v.w;
-    }
+      for (int s = 0; s < p.splits; ++s) {
+        const float4 v = *reinterpret_cast<const float4 *>(from + static_cast<int64_t>(s) * (kM * kN));
+        c[0] += v.x, c[1] += v.y, c[2] += v.z, c[3] += v.w;
+      }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) c[e] += p.bias && col + e < p.N ? p.bias[col + e] : 0.0f;
-    finish<T, 4>(p, c, static_cast<int64_t>(tm) * kM + r, col);
+      for (int e = 0; e < 4; ++e) c[e] += p.bias && col + e < p.N ? p.bias[col + e] : 0.0f;
+      finish<T, 4>(p, c, static_cast<int64_t>(tm) * kM + r, col);
+    }
   }
 }
 

@@ -101,8 +101,9 @@ enum hyena_act {
  * x: [M, K], w: [N, K], residual, y, z: [M, N], all of `dtype`, 16-byte aligned.  bias: fp32 [N].
  * bias, residual and z may be NULL; z, where given, receives the value before the activation,
  * which hyena_proj_bwd wants (rounded to `dtype`).  y may be residual itself.
- * Any M >= 0, N, K >= 1 (M, N <= 2^30, K <= 2^24).  The products run on tensor cores with fp32 accumulation: bf16 operands
- * as they are (rows that are no multiple of 8 elements are copied into the workspace first); fp32
+ * Any M >= 0, N, K >= 1 (M, N <= 2^30, K <= 2^24).  The products run on tensor cores with fp32
+ * accumulation (which truncates: up to 2^-11 of sum |x| |w|, on sums of one sign): bf16 operands as
+ * they are (rows that are no multiple of 8 elements are copied into the workspace first); fp32
  * operands as three bf16 planes each and six products, which keeps fp32's precision (relative to
  * sum |x| |w|) for finite values; a product with an infinite operand may give NaN in its place.
  * Bias, activation and residual are fp32, y is rounded once.  Deterministic.
