@@ -8,7 +8,8 @@
 //
 // fp32 operands are split into three bf16 planes a = a0 + a1 + a2 (8 bits of the mantissa each),
 // and C is the sum of the six products of planes i + j <= 2, smallest first; the three left out
-// are below 2^-26 of a b.  The planes of a k-block are three stages of the ring, from which the six
+// are below 2^-26 of a b.  (An operand below 2^-110 has planes among bf16's subnormals, which the
+// tensor cores keep, or below the last of them, 2^-133, where its bits are lost.)  The planes of a k-block are three stages of the ring, from which the six
 // products take theirs.  The tensor cores' accumulator truncates at every addition, which over
 // thousands of k is a bias above fp32's own rounding: after each k-block the epilogue warps take
 // the accumulator into registers, where the sum goes on with rounding to nearest (normwise error
@@ -96,7 +97,7 @@ enum Fault { kNoFault = 0, kNoResidual = 1, kNoAccumulator = 2, kStagesEnd = 3 }
 
 // ------------------------------------------------------------------------------- activations
 // fp32 results take the accurate exp and division; a bf16 result rounds away what the fast ones
-// lose, and with the accurate division the epilogue of silu took longer than the product (8192 x
+// lose (their sigmoid and silu end at z = -87.3, below 1e-36), and with the accurate division the epilogue of silu took longer than the product (8192 x
 // 4096 x 4096: 340 us against 185).
 template <typename T> __device__ __forceinline__ float exp_of(float x) { return __expf(x); }
 template <> __device__ __forceinline__ float exp_of<float>(float x) { return expf(x); }
@@ -1012,7 +1013,7 @@ __global__ void __launch_bounds__(256) proj_join_kernel(const Params p) {
 // ------------------------------------------------------------------------------- operands
 // Eight values as bf16 planes, each the nearest to what the planes before leave; one plane is the
 // value rounded.  Of three, the first goes towards zero where the nearest would overflow, and values
-// that are not finite stay in it.
+// that are not finite stay in it (times a zero plane of their partner they give NaN).
 template <int kPlanes>
 __device__ __forceinline__ void planes_of(const float (&v)[8], VecOf<__nv_bfloat16, 8> (&o)[kPlanes]) {
   if constexpr (kPlanes == 1) {

@@ -105,7 +105,9 @@ enum hyena_act {
  * accumulation (which truncates: up to 2^-11 of sum |x| |w|, on sums of one sign): bf16 operands as
  * they are (rows that are no multiple of 8 elements are copied into the workspace first); fp32
  * operands as three bf16 planes each and six products, which keeps fp32's precision (relative to
- * sum |x| |w|) for finite values; a product with an infinite operand may give NaN in its place.
+ * sum |x| |w|) for finite operands that are 0 or at least 2^-110 in size.  bf16 ends at 2^-133: of
+ * smaller ones what lies below 2^-134 is lost, at most 2^-133 (sum |x| + sum |w|) in all.  A product
+ * with an infinite fp32 operand may give NaN in its place.
  * Bias, activation and residual are fp32, y is rounded once.  Deterministic.
  * workspace: at least hyena_proj_workspace_bytes(M, N, K, dtype) bytes, 256-byte aligned; NULL
  * where that is 0.

@@ -133,3 +133,27 @@ def test_tails_keep_their_bits(act, dtype):
                                  torch.zeros(n, 8, dtype=dtype, device="cuda"),
                                  torch.ones_like(z), z=z, act=act)[2]
         near(act + " slope", slope, *slope_definition(z[0].double(), act, dtype))
+
+
+def test_fp32_operands_down_to_the_smallest():
+    """Operands of every size against partners that bring their products back to ordinary ones.  At
+    2^-110 and above the three planes hold all 24 bits; below, bf16's last bit 2^-133 leaves an error
+    of half of it (2^-134) in the operand.  The bound is the products' own (test_proj_gpu: 2 u (1.1 K
+    / 16 + 18) S) and 2^-133 of the partner."""
+    small = torch.tensor([2.0 ** -100, 1.2345678 * 2.0 ** -109, (1 + 2.0 ** -23) * 2.0 ** -110,
+                          1.7654321 * 2.0 ** -111, 1.0001e-34, 3.3333333e-36, 1.0001e-38,
+                          1.1754945e-38, 5.4321e-39, 2.0 ** -133, 2.0 ** -140, 0.0],
+                         dtype=torch.float64).float().cuda()
+    big = torch.tensor([3.4e38, 2.0 ** 100, 1.5, -2.2222222e37], device="cuda")
+    n = small.numel()
+    w = torch.zeros(n, 8, device="cuda")
+    w[:, 3] = small
+    for b in big:
+        x = torch.zeros(5, 8, device="cuda")
+        x[:, 3] = b
+        y = g.hyena_proj_fwd(x, w)[0].double()
+        want = float(b) * small.double()
+        lost = torch.where(small.double().abs() >= 2.0 ** -110, 0.0, 2.0 ** -133) * abs(float(b))
+        err = 2 * U * (1.1 * 8 / 16 + 18) * want.abs() + lost
+        # results below fp32's normal numbers keep fewer bits
+        assert bool(((y - want).abs() <= err + U * want.abs() + 2.0 ** -126).all()), (float(b), y, want)
