@@ -344,9 +344,14 @@ int backward(const Shape &s, sc::Params p, void *ws, int sms, cudaStream_t strea
 
 // Which feed takes the tensors, from their rows and addresses; sets the copies' and stores' width.
 // TMA needs rows and bases of 16 bytes, and a group's decay for both channels of a pair.  The
-// compute warps take the exps of groups up to `raw` channels, the helpers those of wider ones.  L =
-// 8192, D = 4096, by compute warps | by helpers, in us: forward, bf16, d_g = 2 54 | 99; backward,
-// bf16, d_g = 2 132 | 163, 4 122 | 118; backward, fp32, d_g = 2 203 | 174, 4 158 | 159.
+// compute warps take the exps of groups up to `raw` channels, the helpers those of wider ones, whose
+// few exps the compute warps need not repeat.  L = 8192, D = 4096, by compute warps | by helpers, us:
+//   d_g                   2            4            8           16           64
+//   forward, bf16    52 | 127     50 |  85     50 |  78     49 |  50     50 |  48
+//   forward, fp32    99 | 121     93 | 108     89 | 102     89 |  88     88 |  87
+//   backward, bf16  132 | 163    122 | 118
+//   backward, fp32  203 | 174    158 | 159
+// (forward, d_g = 8, fp32, B = 8, L = 4096: 364 | 353, the one shape of five that went the other way)
 int choose_feed(const Shape &s, std::initializer_list<const void *> streams,
                 std::initializer_list<const void *> outs, const void *g, int raw, sc::Params *p) {
   uintptr_t bits = static_cast<uintptr_t>(s.D * s.es()), out_bits = bits;
@@ -441,7 +446,7 @@ int scan_fwd(const void *q, const void *k, const void *v, const void *g, const f
   p.y = y;
   p.fault = fault;
   if (wait_ns > 0) p.wait_ns = wait_ns;
-  const int feed = choose_feed(s, {q, k, v}, {y}, g, 4, &p);
+  const int feed = choose_feed(s, {q, k, v}, {y}, g, 8, &p);
   return with_one_feed(feed, [&](auto f) {
     constexpr int kFeed = decltype(f)::value;
     if (dtype == HYENA_DTYPE_F32)

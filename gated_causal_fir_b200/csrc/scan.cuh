@@ -50,8 +50,8 @@ constexpr unsigned int kTimeout = 1u; // HYENA_DEVICE_TIMEOUT
 // How a tile's inputs reach shared memory: the streams by TMA, or where their rows are no multiple
 // of 16 bytes by asynchronous 8- or 4-byte copies (single elements where not even those are
 // aligned).  One decay per channel: g is a stream like k and v and the compute warps take its exp.
-// One per group: the helper warps do, except for groups of 2 and 4 channels (kTmaRaw), whose many
-// exps are quicker where they are used (choose_feed on the host has the measurements).
+// One per group: the helper warps do, except for groups of few channels (kTmaRaw), whose many exps
+// are quicker where they are used (choose_feed on the host has the measurements).
 enum Feed { kTmaChannel = 0, kTmaGroup = 1, kCopyChannel = 2, kCopyGroup = 3, kTmaRaw = 4 };
 __host__ __device__ constexpr bool by_tma(int feed) {
   return feed == kTmaChannel || feed == kTmaGroup || feed == kTmaRaw;
@@ -843,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Sums over 2 kHalf neighbouring lanes of one value per row.  Each exchange halves the rows that a
 // lane holds: of n rows the upper lane keeps those from h = ceil(n / 2) on and gives the others; an
 // odd row out is summed in both.  row(p) is the row that position p holds after the exchanges
-// (rows 9 over 16 lanes: 11 exchanges where sums of each row would take 36).
+// (11 rows over 16 lanes: 12 exchanges where sums of each row would take 44).
 template <int kHalf, int n>
 struct GroupSum {
   static constexpr int h = (n + 1) / 2;

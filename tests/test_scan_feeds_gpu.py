@@ -70,3 +70,22 @@ def test_tiles_are_read_before_the_next_ones_land(L, D, d_g, dtype):
         if want is None:
             want = got
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", (BF16, F32), ids=("bf16", "f32"))
+@pytest.mark.parametrize("B,L,D", ((1, 400, 4096), (2, 1500, 128), (1, 20000, 64), (1, 333, 72),
+                                   (3, 200, 240), (1, 900, 48), (1, 178, 8)))
+def test_groups_of_eight(B, L, D, dtype):
+    """The widest groups whose exps the forward's compute warps take: whole rows, clusters, cuts,
+    groups' rows by TMA and by copies."""
+    q, k, v, lg, s0, dy, ds = make(B, L, D, 8, dtype, seed=2, resets=True)
+    ref = R.Ref(q, k, v, lg, 8, s0, dy, ds)
+    ckpt = g.hyena_scan_ckpt(q)
+    y, s_out = g.hyena_scan_fwd(q, k, v, lg, 8, s0=s0, ckpt=ckpt)
+    R.check("y", y, ref)
+    R.check("s_out", s_out, ref)
+    grads = g.hyena_scan_bwd(q, k, v, lg, dy, 8, s0=s0, ds_out=ds, ckpt=ckpt)
+    for name, t, again in zip(("dq", "dk", "dv", "dg", "ds0"), grads,
+                              g.hyena_scan_bwd(q, k, v, lg, dy, 8, s0=s0, ds_out=ds)):
+        R.check(name, t, ref)
+        assert torch.equal(t, again)
