@@ -96,3 +96,22 @@ def test_a_training_step_reads_what_this_pass_wrote(layer):
             run()
             for a, b in zip(chain.outputs(), want[i % 3]):
                 assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("layer", LAYERS[:6], ids=["x".join(map(str, s[:6])) + str(s[6])[-4:]
+                                                   for s in LAYERS[:6]])
+def test_the_layers_backward_is_the_chain_of_its_calls(layer):
+    """The same bits as the calls one by one, and what comes in stays as it was."""
+    chain = Layer(*layer)
+    chain.x.copy_(torch.randn_like(chain.x))
+    chain.dout.copy_(torch.randn_like(chain.dout))
+    chain.run(torch.cuda.synchronize)
+    kept = chain.x.clone(), chain.dout.clone()
+    out, _, saved = g.hyena_mixer_fwd(chain.x, chain.p, save=True)
+    dx, ds0, grads = g.hyena_mixer_bwd(chain.x, chain.p, saved, chain.dout)
+    assert torch.equal(out, chain.out) and torch.equal(dx, chain.dx) and ds0 is None
+    assert dx.data_ptr() != chain.dout.data_ptr()
+    for n, gp in zip("qkv", chain.gp):
+        assert torch.equal(grads[n][0], gp[1]) and torch.equal(grads[n][1], gp[2])
+    assert torch.equal(grads["out"][0], chain.gy[1]) and torch.equal(grads["filters"], chain.gf[3])
+    assert torch.equal(chain.x, kept[0]) and torch.equal(chain.dout, kept[1])
