@@ -1072,7 +1072,9 @@ __global__ void __launch_bounds__(256)
 
 // dz = dy act'(z) as a product's operand (planes and row length as above; null where dy itself
 // serves) and its column sums over `block_rows` rows, part[row block][N] (db itself where there is
-// one block).  A CTA takes 64 columns: 8 threads of 8 columns x 32 rows at a time.
+// one block).  bf16 has one plane: the rounding leaves 0.0023 of the gradients' size in error where
+// their own rounding is 0.0017, and a second plane would double the products.  A CTA takes 64
+// columns: 8 threads of 8 columns x 32 rows at a time.
 constexpr int kDbCols = 64;
 template <typename T, int kAct>
 __global__ void __launch_bounds__(256)
