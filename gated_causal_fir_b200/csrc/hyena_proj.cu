@@ -22,9 +22,9 @@ constexpr int64_t kMaxReduced = int64_t{1} << 24;  // a tile's sum ends well ins
 constexpr int kSms = 148;
 constexpr int kMaxSplits = 16;
 // k-blocks that one bf16 accumulator takes at most.  It truncates at every addition, which on sums
-// of one sign is a bias: the mean error of dw over 2^18, 2^20 rows of positive values was 0.11, 0.67
-// percent (of 4096 x 4096 outputs; half a step of bf16 is 0.2 to 0.4).  Longer sums are cut, and
-// the cuts added with rounding to nearest.
+// of one sign is a bias: the mean error of dw over 2^18 and 2^20 rows of positive values was 0.11
+// and 0.67 percent (4096 x 4096 outputs; half a step of bf16 is 0.2 to 0.4).  Longer sums are cut,
+// and the cuts added with rounding to nearest.
 constexpr int64_t kMaxRun = 2048;
 
 int64_t elem(int dtype) { return dtype == HYENA_DTYPE_F32 ? 4 : 2; }
@@ -110,6 +110,12 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int dtype) {
   Entry &e = seen[next++ % 8];
   e = Entry{M, N, K, dtype, find_plan(M, N, K, dtype)};
   return e.plan;
+}
+
+// Whether a product's tiles and cuts cannot be counted in 32 bits.
+bool too_many(int64_t M, int64_t N, int64_t K, int dtype) {
+  const Plan p = plan_of(M, N, K, dtype);
+  return p.tiles_m * p.tiles_n * p.splits > std::numeric_limits<int32_t>::max();
 }
 
 int64_t partial_bytes(int64_t M, int64_t N, int64_t K, int dtype) {
@@ -249,8 +255,6 @@ template <typename T, bool kAMn, bool kBMn>
 int product(const Operand &a, const Operand &b, int64_t K, pj::Params p, int dtype, float *partial,
             const Device &d, cudaStream_t stream) {
   const Plan pl = plan_of(p.M, p.N, K, dtype);
-  if (pl.tiles_m * pl.tiles_n * pl.splits > std::numeric_limits<int32_t>::max())
-    return HYENA_ERR_UNSUPPORTED;
   p.kb = pl.kb;
   p.tiles_m = static_cast<int>(pl.tiles_m);
   p.tiles_n = static_cast<int>(pl.tiles_n);
@@ -466,6 +470,7 @@ int proj_fwd(const void *x, const void *w, const float *bias, const void *residu
   if (misaligned16({x, w, residual, y, z}) || !aligned(bias, 4) || !aligned(workspace, 256))
     return HYENA_ERR_MISALIGNED;
   const int64_t need = hyena_proj_workspace_bytes(M, N, K, dtype), es = elem(dtype);
+  if (need < 0) return static_cast<int>(-need);
   if (need > 0 && (!workspace || static_cast<int64_t>(workspace_bytes) < need))
     return HYENA_ERR_INVALID_ARG;
   const int64_t nx = M * K * es, nw = N * K * es, ny = M * N * es;
@@ -498,6 +503,7 @@ extern "C" {
 int64_t hyena_proj_workspace_bytes(int64_t M, int64_t N, int64_t K, int dtype) {
   if (check_shape(M, N, K, dtype) != HYENA_OK) return -HYENA_ERR_INVALID_ARG;
   if (M == 0) return 0;
+  if (too_many(M, N, K, dtype)) return -HYENA_ERR_UNSUPPORTED;
   int64_t n = partial_bytes(M, N, K, dtype);
   if (needs_pack(K, dtype)) n += pack_bytes(M, K, dtype) + pack_bytes(N, K, dtype);
   return n;
@@ -507,6 +513,9 @@ int64_t hyena_proj_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int act,
   if (check_shape(M, N, K, dtype) != HYENA_OK || act < HYENA_ACT_NONE || act > HYENA_ACT_LOGSIGMOID)
     return -HYENA_ERR_INVALID_ARG;
   if (M == 0) return 0;
+  if (db_blocks(M) > 65535 || N > kMaxReduced || too_many(M, K, N, dtype) ||
+      too_many(N, K, M, dtype))
+    return -HYENA_ERR_UNSUPPORTED;
   int64_t n = round_up(db_blocks(M) * N * 4, 256);
   if (needs_dz(N, act, dtype)) n += pack_bytes(M, N, dtype);
   if (needs_pack(K, dtype)) n += pack_bytes(M, K, dtype) + pack_bytes(N, K, dtype);
@@ -527,7 +536,7 @@ int hyena_testing_proj_fault(const void *x, const void *w, const void *residual,
   if (fault < pj::kNoFault || fault > pj::kStagesEnd || wait_ns < 1000000ull ||
       wait_ns > hyena::kWaitTimeoutNs)
     return HYENA_ERR_INVALID_ARG;
-  if (N % 8 != 0 || hyena_proj_workspace_bytes(M, N, K, HYENA_DTYPE_BF16) > 0)
+  if (N % 8 != 0 || hyena_proj_workspace_bytes(M, N, K, HYENA_DTYPE_BF16) != 0)
     return HYENA_ERR_UNSUPPORTED;
   return proj_fwd(x, w, nullptr, residual, y, nullptr, M, N, K, HYENA_ACT_NONE, HYENA_DTYPE_BF16,
                   nullptr, 0, fault, wait_ns, stream);
@@ -550,8 +559,8 @@ int hyena_proj_bwd(const void *x, const void *w, const void *z, const void *dy,
     return HYENA_OK;
   }
   if (!dy || (dx && !w) || (dw && !x) || (act != HYENA_ACT_NONE && !z)) return HYENA_ERR_INVALID_ARG;
-  if (db_blocks(M) > 65535 || N > kMaxReduced) return HYENA_ERR_UNSUPPORTED;
   const int64_t need = hyena_proj_bwd_workspace_bytes(M, N, K, act, dtype);
+  if (need < 0) return static_cast<int>(-need);
   if (!workspace || static_cast<int64_t>(workspace_bytes) < need) return HYENA_ERR_INVALID_ARG;
   if (clash({{dx, nx}, {dw, nw}, {db, N * 4}, {workspace, need}},
             {{x, nx}, {w, nw}, {z, ny}, {dy, ny}}) ||

@@ -9,12 +9,12 @@
 // fp32 operands are split into three bf16 planes a = a0 + a1 + a2 (8 bits of the mantissa each),
 // and C is the sum of the six products of planes i + j <= 2, smallest first; the three left out
 // are below 2^-26 of a b.  (An operand below 2^-110 has planes among bf16's subnormals, which the
-// tensor cores keep, or below the last of them, 2^-133, where its bits are lost.)  The planes of a k-block are three stages of the ring, from which the six
-// products take theirs.  The tensor cores' accumulator truncates at every addition, which over
-// thousands of k is a bias above fp32's own rounding: after each k-block the epilogue warps take
-// the accumulator into registers, where the sum goes on with rounding to nearest (normwise error
-// of a product over 4096 k: 1.2e-7, over 16384 k: 1.7e-7; fp32 FMAs: 1.1e-6 and 2.3e-6).  2048^3:
-// 97 us (fp32 FMA units: 306).
+// tensor cores keep, or below the last of them, 2^-133, where its bits are lost.)  The planes of a
+// k-block are three stages of the ring, from which the six products take theirs.  The tensor cores'
+// accumulator truncates at every addition, which over thousands of k is a bias above fp32's own
+// rounding: after each k-block the epilogue warps take the accumulator into registers, where the
+// sum goes on with rounding to nearest (normwise error of a product over 4096 k: 1.2e-7, over
+// 16384 k: 1.7e-7; fp32 FMAs: 1.1e-6 and 2.3e-6).  2048^3: 97 us (fp32 FMA units: 306).
 //
 // Tiles.  kCG = 2: a pair of CTAs works on 256 x 256 outputs with tcgen05.mma.cta_group::2, each
 // holding 128 rows of A, 128 rows of B and 128 rows of the accumulator.  Each byte staged then
@@ -97,8 +97,8 @@ enum Fault { kNoFault = 0, kNoResidual = 1, kNoAccumulator = 2, kStagesEnd = 3 }
 
 // ------------------------------------------------------------------------------- activations
 // fp32 results take the accurate exp and division; a bf16 result rounds away what the fast ones
-// lose (their sigmoid and silu end at z = -87.3, below 1e-36), and with the accurate division the epilogue of silu took longer than the product (8192 x
-// 4096 x 4096: 340 us against 185).
+// lose (their sigmoid and silu end at z = -87.3, below 1e-36), and with the accurate division the
+// epilogue of silu took longer than the product (8192 x 4096 x 4096: 340 us against 185).
 template <typename T> __device__ __forceinline__ float exp_of(float x) { return __expf(x); }
 template <> __device__ __forceinline__ float exp_of<float>(float x) { return expf(x); }
 template <typename T> __device__ __forceinline__ float ratio(float a, float b) { return __fdividef(a, b); }
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t res_full[kEpiWarps];
   __shared__ uint32_t tmem_at;
   __shared__ int abort;
-  __shared__ int issued, peer_abort, peer_issued;  // (pairs) stages that a CTA's copies were issued for
+  __shared__ int issued, peer_abort, peer_issued;  // issued: stages with copies under way or landed
   uint8_t *stages = dynamic + (1024 - smem_u32(dynamic) % 1024) % 1024;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const uint32_t rank = kCG == 2 ? cluster_rank() : 0;
@@ -560,7 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               b_lo = static_cast<uint32_t>(db0);
             }
           }
-          if (ok && lead && (kPromote || p.fault != kNoAccumulator || n > 0)) commit<kCG>(&acc_full[acc]);
+          if (ok && lead && (kPromote || p.fault != kNoAccumulator || n > 0))
+            commit<kCG>(&acc_full[acc]);
           __syncwarp();
         }
       }

@@ -7,7 +7,8 @@
  * device allocation, asynchronous on `stream`, argument errors found on the host before anything
  * is queued.  Outputs must not overlap inputs or each other unless an entry point says so.
  * Make the first call of each kind on a device before any stream capture (kernel attributes are
- * set then).  A timeout inside a kernel raises HYENA_DEVICE_TIMEOUT in the status word of hyena_conv.h.
+ * set then).  A timeout inside a kernel raises HYENA_DEVICE_TIMEOUT in the status word of
+ * hyena_conv.h.
  */
 #ifndef HYENA_MIXER_H
 #define HYENA_MIXER_H
@@ -86,8 +87,8 @@ int hyena_scan_step(const void *q, const void *k, const void *v, const void *g, 
 
 enum hyena_act {
     HYENA_ACT_NONE = 0,
-    HYENA_ACT_GELU = 1,          /* z Phi(z), the exact form (erf); inf at inf; NaN, as silu, at -inf
-                                    (inf times 0) */
+    HYENA_ACT_GELU = 1,          /* z Phi(z), the exact form (erf); at -inf NaN (inf times 0), as
+                                    silu */
     HYENA_ACT_SILU = 2,          /* z sigmoid(z) */
     HYENA_ACT_SIGMOID = 3,
     HYENA_ACT_LOGSIGMOID = 4     /* log sigmoid(z): a log decay for hyena_scan_* */
@@ -116,7 +117,9 @@ int hyena_proj_fwd(const void *x, const void *w, const float *bias, const void *
                    void *z, int64_t M, int64_t N, int64_t K, int act, int dtype, void *workspace,
                    size_t workspace_bytes, cudaStream_t stream);
 
-/* Host-only: workspace of hyena_proj_fwd (a multiple of 256), or minus HYENA_ERR_INVALID_ARG. */
+/* Host-only: workspace of hyena_proj_fwd (a multiple of 256), or minus HYENA_ERR_INVALID_ARG, or
+ * minus HYENA_ERR_UNSUPPORTED for more than 2^31 tiles of outputs (at most 256 x 256, in as many
+ * cuts as K has pieces of 2^17), which the call refuses too. */
 int64_t hyena_proj_workspace_bytes(int64_t M, int64_t N, int64_t K, int dtype);
 
 /*
@@ -137,7 +140,8 @@ int hyena_proj_bwd(const void *x, const void *w, const void *z, const void *dy,
                    int64_t K, int act, int dtype, void *workspace, size_t workspace_bytes,
                    cudaStream_t stream);
 
-/* Host-only: workspace of hyena_proj_bwd (a multiple of 256), or minus HYENA_ERR_INVALID_ARG. */
+/* Host-only: workspace of hyena_proj_bwd (a multiple of 256), or minus the error that the call
+ * returns for such sizes. */
 int64_t hyena_proj_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int act, int dtype);
 
 #ifdef __cplusplus

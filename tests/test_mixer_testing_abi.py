@@ -1,4 +1,4 @@
-"""Host-side refusals of the mixer operators' test entry points (no GPU)."""
+"""Host-side refusals of the mixer operators' test entry points, and of sizes (no GPU)."""
 import pytest
 
 from gated_causal_fir_b200 import _native, build
@@ -15,6 +15,25 @@ def test_refusals(kw, code):
     build.build()
     a = dict(ARGS, **kw)
     assert _native.lib().hyena_testing_proj_fault(*[a[n] for n in ARGS], None) == code
+
+
+BIG = 1 << 30
+
+
+@pytest.mark.parametrize("M,N,K", ((BIG, BIG, 8), (BIG, BIG, 1 << 24), (1 << 26, 1 << 26, 1 << 20)))
+def test_more_tiles_than_can_be_counted_are_refused(M, N, K):
+    """By the size queries as by the calls, for the product itself and as a backward's."""
+    build.build()
+    lib = _native.lib()
+    assert lib.hyena_proj_workspace_bytes(M, N, K, 0) == -2
+    at = [(i + 1) << 58 for i in range(4)]
+    assert lib.hyena_proj_fwd(at[0], at[1], None, None, at[2], None, M, N, K, 0, 0, None, 0,
+                              None) == 2
+    m = min(M, 8388480)
+    assert lib.hyena_proj_bwd_workspace_bytes(m, 1 << 24, 1 << 24, 0, 0) == -2
+    assert lib.hyena_proj_bwd_workspace_bytes(8388481, 8, 8, 0, 0) == -2
+    assert lib.hyena_proj_bwd_workspace_bytes(8, (1 << 24) + 1, 8, 0, 0) == -2
+    assert lib.hyena_proj_bwd_workspace_bytes(8388480, 8, 8, 0, 0) > 0
 
 
 SCAN = dict(q=1 << 24, k=2 << 24, v=3 << 24, g=4 << 24, y=5 << 24, s_out=6 << 24, B=1, L=1250, D=320,
