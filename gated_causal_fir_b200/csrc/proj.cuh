@@ -971,6 +971,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    __syncwarp();    // the barrier wants whole warps, and the lanes' shares of the rows may differ
     cluster_sync();  // no CTA leaves while others read its product
   }
   if (warp == 1) {
